@@ -15,7 +15,8 @@
  * Between mhc_pre and mhc_post_res the caller runs its own layer F
  * (attention / FFN) to turn F_pre into F_out; that layer is not part of mHC.
  * mhc_post_res_coeffs fuses a layer's apply with the next layer's
- * coefficients (one pass over the residual stream instead of two).
+ * coefficients (one pass over the residual stream instead of two).  The
+ * gradients of these steps, for training, are further down.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -511,6 +512,157 @@ int mhc_post_res_coeffs_phi32(int64_t B, int32_t n, int64_t C,
  * rules as for the calls above. */
 int mhc_lazy_prenorm_gemm(int64_t M, int64_t N, int64_t K, const void *A, const void *W,
                           float eps, void *C, float *rstd, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Training: the gradients of the calls above, the 8-bit checkpoint of the
+ * stream that they read, and the embeddings the first stream is built from.
+ *
+ * The gradients are those of [mHC-cutile] section 2's formulas.  With
+ * G = dX_next (the gradient that arrives at a layer's X_next), a layer's
+ * backward pass is
+ *
+ *   mhc_post_res_bwd    dF_out and the gradients of H_post and H_res;
+ *   (the caller's own backward pass of the layer F: dF_out -> dF_pre)
+ *   mhc_coeffs_pre_bwd  dX_t -- complete: through the apply, the pre-mix, the
+ *                       product and the row's root mean square -- and the
+ *                       gradients of phi, the alphas and the biases.
+ *
+ * dX_t is the G of the layer before.  The calls take what the forward calls
+ * returned (logits, r, H) and X_t either as the bf16 stream or, in the *_ckpt
+ * calls, as its checkpoint (mhc_ckpt_pack).  The forward calls on a bf16
+ * stream with a bf16 phi are the ones they belong to.
+ *
+ * Gradients of the stream and of F are bf16, rounded once (nearest even);
+ * gradients of parameters and coefficients are fp32.  Sums are fp32 or wider
+ * and run in a fixed order (no atomics on values): equal inputs give equal
+ * bits.  A row with r = 0 has no gradient (NaN), as it has no logits in the
+ * forward.  Conventions, checks and errors are those at the top of this file;
+ * beyond them the gradients of parameters of no rows (B == 0) are zeros, so
+ * those calls fill their parameter outputs at B == 0 and then need those
+ * pointers.
+ * ------------------------------------------------------------------------ */
+
+/* The checkpoint of a stream: for every 32 channels of a stream of a row (the
+ * last block of a stream is shorter where C % 32 != 0) one scale byte s, and
+ * for every channel an E4M3 code q (OCP "fn", as in the *_fp8 calls); the
+ * value is q * 2^(s - 127), exact in bf16.  s is the least one >= 1 with
+ * |x| <= 448 * 2^(s - 127) for all finite x of the block, so finite values
+ * never saturate; codes round to nearest even (relative error at most 2^-4,
+ * absolute at most 2^-10 * 2^(s - 127) where E4M3 is subnormal), and values
+ * above 240 * 2^120 become that (2^128 is no bf16 number).  Inf and NaN become
+ * NaN.  C + ceil(C / 32) bytes a stream and row instead of 2 C.
+ *
+ * mhc_ckpt_scales_per_row: n * ceil(C / 32); 0 for an invalid n or C. */
+int64_t mhc_ckpt_scales_per_row(int32_t n, int64_t C);
+
+/*   X_t     in  bf16 [B, n*C]
+ *   codes   out E4M3 [B, n*C], 16-byte aligned
+ *   scales  out uint8 [B, mhc_ckpt_scales_per_row(n, C)] */
+int mhc_ckpt_pack(int64_t B, int32_t n, int64_t C, const void *X_t, void *codes,
+                  uint8_t *scales, void *stream);
+
+/* X_t as bf16 again (the values the checkpoint stands for, exactly), where a
+ * forward call is to run on it once more.  Scale bytes as mhc_ckpt_pack
+ * writes them (1 to 247). */
+int mhc_ckpt_unpack(int64_t B, int32_t n, int64_t C, const void *codes,
+                    const uint8_t *scales, void *X_t, void *stream);
+
+/* Gradients of step (4b), X_next[i] = sum_j H_res[i,j] X_t[j] + H_post[i] F_out:
+ *
+ *   dF_out[b, c]        = sum_i H_post[b, i] G[b, i*C + c]
+ *   dH_post[b, i]       = sum_c G[b, i*C + c] F_out[b, c]
+ *   dH_res[b, i, j]     = sum_c G[b, i*C + c] X_t[b, j*C + c]
+ *
+ *   X_t      in  bf16 [B, n*C]   (mhc_post_res_bwd_ckpt: codes and scales)
+ *   F_out    in  bf16 [B, C]
+ *   H        in  fp32 [B, N] (the post block is read)
+ *   dX_next  in  bf16 [B, n*C]
+ *   dF_out   out bf16 [B, C]
+ *   dH       out fp32 [B, N]; the pre block is written as zeros (the apply
+ *            does not read H_pre)
+ *
+ * The gradient of X_t through the apply is part of mhc_coeffs_pre_bwd. */
+int mhc_post_res_bwd(int64_t B, int32_t n, int64_t C, const void *X_t, const void *F_out,
+                     const float *H, const void *dX_next, void *dF_out, float *dH, void *stream);
+
+int mhc_post_res_bwd_ckpt(int64_t B, int32_t n, int64_t C, const void *codes,
+                          const uint8_t *scales, const void *F_out, const float *H,
+                          const void *dX_next, void *dF_out, float *dH, void *stream);
+
+/* Gradients of steps (1)-(4a), joined with the path of X_t through the apply.
+ * With dF_pre the gradient of the layer's input and dH what mhc_post_res_bwd
+ * wrote,
+ *
+ *   dH_pre[i] = sum_c dF_pre[c] X_t[i*C + c];
+ *   dz        = dH through the gates and the 20 normalisations at
+ *               z = alpha * logits / r + b;
+ *   dlogits   = alpha * dz / r;
+ *   dX_t[j]   = sum_i H_res[i,j] G[i] + H_pre[j] dF_pre + dlogits . phi_j^T
+ *               - (sum_k dlogits_k logits_k) / (n C r^2) X_t[j];
+ *   dphi      = X_t^T . dlogits,  dalpha_x = sum dz_x logits_x / r,
+ *   db_x      = sum dz_x          (sums over the rows).
+ *
+ *   X_t ... b_res   as in mhc_coeffs (X_t as codes and scales in the _ckpt
+ *                   call); logits, r, H as the forward call returned them
+ *   dX_next  in  bf16 [B, n*C]
+ *   dH       in  fp32 [B, N] (the post and res blocks are read)
+ *   dF_pre   in  bf16 [B, C]
+ *   dX_t     out bf16 [B, n*C]; must not overlap dX_next
+ *   dphi     out fp32 [n*C, N], 16-byte aligned
+ *   dalpha   out fp32 [3] (pre, post, res)
+ *   db_pre   out fp32 [n];  db_post out fp32 [n];  db_res out fp32 [n*n]
+ *   workspace  scratch, >= mhc_coeffs_pre_bwd_workspace_size(B, n, C) bytes
+ *              (both calls); contents on entry ignored.
+ *
+ * The parameter gradients are overwritten, not added to. */
+size_t mhc_coeffs_pre_bwd_workspace_size(int64_t B, int32_t n, int64_t C);
+
+int mhc_coeffs_pre_bwd(int64_t B, int32_t n, int64_t C, const void *X_t, const void *phi,
+                       float alpha_pre, float alpha_post, float alpha_res,
+                       const float *b_pre, const float *b_post, const float *b_res,
+                       const float *logits, const float *r, const float *H,
+                       const void *dX_next, const float *dH, const void *dF_pre, void *dX_t,
+                       float *dphi, float *dalpha, float *db_pre, float *db_post, float *db_res,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+int mhc_coeffs_pre_bwd_ckpt(int64_t B, int32_t n, int64_t C, const void *codes,
+                            const uint8_t *scales, const void *phi,
+                            float alpha_pre, float alpha_post, float alpha_res,
+                            const float *b_pre, const float *b_post, const float *b_res,
+                            const float *logits, const float *r, const float *H,
+                            const void *dX_next, const float *dH, const void *dF_pre, void *dX_t,
+                            float *dphi, float *dalpha, float *db_pre, float *db_post,
+                            float *db_res, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The first layer's stream from token embeddings: X_0[b, i*C + c] =
+ * bf16(scale * table[tokens[b], c]) for every stream i.  A token outside
+ * [0, V) (padding) gives a row of zeros.
+ *
+ *   tokens  in  int64 [B], 8-byte aligned
+ *   table   in  bf16 [V, C]
+ *   scale   host fp32
+ *   X_0     out bf16 [B, n*C]
+ *
+ * V >= 1 (else MHC_ERR_INVALID_ARG), V < 2^31 and V * C <= 2^40. */
+int mhc_embed(int64_t B, int32_t n, int64_t C, int64_t V, const int64_t *tokens,
+              const void *table, float scale, void *X_0, void *stream);
+
+/* Its gradient: dtable[v, c] = scale * sum over the rows b with tokens[b] = v
+ * and the streams i of dX_0[b, i*C + c], in the order of the rows.  Tokens
+ * outside [0, V) add nothing.
+ *
+ *   tokens      in  int64 [B];  dX_0 in bf16 [B, n*C]
+ *   accumulate  0: dtable is overwritten (zeros where no token points);
+ *               otherwise the rows of the tokens that occur are added to and
+ *               the others left as they are
+ *   dtable      out fp32 [V, C], 16-byte aligned
+ *   workspace   scratch, >= mhc_embed_bwd_workspace_size(B, n, C, V) bytes;
+ *               contents on entry ignored. */
+size_t mhc_embed_bwd_workspace_size(int64_t B, int32_t n, int64_t C, int64_t V);
+
+int mhc_embed_bwd(int64_t B, int32_t n, int64_t C, int64_t V, const int64_t *tokens,
+                  const void *dX_0, float scale, int32_t accumulate, float *dtable,
+                  void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Testing and tuning.

@@ -1,5 +1,5 @@
 """MI355X-native mHC (manifold-constrained hyper-connections) residual-stream
-forward: HIP kernels for gfx950 behind the C ABI of include/mhc.h, with a thin
+forward and its gradients: HIP kernels for gfx950 behind the C ABI of include/mhc.h, with a thin
 ctypes binding.  See binding.py for the Python entry points."""
 
 from .binding import (  # noqa: F401
@@ -16,4 +16,7 @@ from .binding import (  # noqa: F401
     mhc_post_res_coeffs_pre_fp8, mhc_post_res_coeffs_pre_fp8_one_pass,
     mhc_coeffs_pre_workspace_size, mhc_coeffs_pre, mhc_coeffs_pre_one_pass, mhc_coeffs_pre_check,
     mhc_coeffs_pre_fp8_workspace_size, mhc_coeffs_pre_fp8, mhc_coeffs_pre_fp8_one_pass,
+    mhc_ckpt_scales_per_row, mhc_ckpt_pack, mhc_ckpt_unpack, mhc_post_res_bwd, mhc_post_res_bwd_ckpt,
+    mhc_coeffs_pre_bwd_workspace_size, mhc_coeffs_pre_bwd, mhc_coeffs_pre_bwd_ckpt, mhc_embed,
+    mhc_embed_bwd_workspace_size, mhc_embed_bwd,
 )

@@ -34,7 +34,10 @@ EXPORTED = ("mhc_status_string", "mhc_coeffs_workspace_size", "mhc_coeffs_split_
             "mhc_tuning_set", "mhc_tuning_reset", "mhc_post_res_coeffs_pre_noalloc",
             "mhc_coeffs_pre_workspace_size", "mhc_coeffs_pre", "mhc_coeffs_pre_one_pass",
             "mhc_coeffs_pre_check", "mhc_coeffs_pre_fp8_workspace_size", "mhc_coeffs_pre_fp8",
-            "mhc_coeffs_pre_fp8_one_pass")
+            "mhc_coeffs_pre_fp8_one_pass", "mhc_ckpt_scales_per_row", "mhc_ckpt_pack", "mhc_ckpt_unpack",
+            "mhc_post_res_bwd", "mhc_post_res_bwd_ckpt", "mhc_coeffs_pre_bwd_workspace_size",
+            "mhc_coeffs_pre_bwd", "mhc_coeffs_pre_bwd_ckpt", "mhc_embed", "mhc_embed_bwd_workspace_size",
+            "mhc_embed_bwd")
 
 MHC_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -125,6 +128,19 @@ def load():
         getattr(lib, f"mhc_coeffs_pre{suffix}_one_pass").restype = i32
     lib.mhc_coeffs_pre_check.argtypes = [i64, i32, i64, i32, vp, sz, vp]
     lib.mhc_coeffs_pre_check.restype = ctypes.c_int
+    lib.mhc_ckpt_scales_per_row.argtypes = [i32, i64]
+    lib.mhc_ckpt_scales_per_row.restype = i64
+    lib.mhc_coeffs_pre_bwd_workspace_size.argtypes = [i64, i32, i64]
+    lib.mhc_coeffs_pre_bwd_workspace_size.restype = sz
+    lib.mhc_embed_bwd_workspace_size.argtypes = [i64, i32, i64, i64]
+    lib.mhc_embed_bwd_workspace_size.restype = sz
+    shape, bwd = [i64, i32, i64], [vp, f32, f32, f32] + [vp] * 16 + [sz, vp]
+    for name, args in (("mhc_ckpt_pack", [vp] * 4), ("mhc_ckpt_unpack", [vp] * 4), ("mhc_post_res_bwd", [vp] * 7),
+                       ("mhc_post_res_bwd_ckpt", [vp] * 8), ("mhc_coeffs_pre_bwd", [vp] + bwd),
+                       ("mhc_coeffs_pre_bwd_ckpt", [vp] * 2 + bwd), ("mhc_embed", [i64, vp, vp, f32, vp, vp]),
+                       ("mhc_embed_bwd", [i64, vp, vp, f32, i32, vp, vp, sz, vp])):
+        getattr(lib, name).argtypes = shape + args
+        getattr(lib, name).restype = ctypes.c_int
     lib.mhc_tuning_reset.argtypes = []
     lib.mhc_tuning_reset.restype = None
     _lib = lib
@@ -492,6 +508,151 @@ def mhc_lazy_prenorm_gemm(M, N, K, A, W, C, rstd=None, eps=1e-5, stream=None, ch
                                       _ptr(rstd, m * 4, 4, "rstd"), _stream(stream))
     if check:
         _check(st, "mhc_lazy_prenorm_gemm")
+    return st
+
+
+# Training: the stream's 8-bit checkpoint, the gradients of the calls above,
+# the embeddings.  These calls launch on the current device, so they take
+# tensors of that device only.
+
+def _here(*tensors):
+    """ValueError where a device tensor is not on the current device (the
+    kernels would run on another device than the tensor's)."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def mhc_ckpt_scales_per_row(n, C):
+    """Scale bytes a row of the checkpoint has: n * ceil(C / 32)."""
+    return int(load().mhc_ckpt_scales_per_row(int(n), int(C)))
+
+
+def _ckpt_ptrs(B, n, C, codes, scales):
+    B, n, C = max(int(B), 0), int(n), int(C)
+    return (_ptr(codes, B * n * C, 1, "codes"), _ptr(scales, B * mhc_ckpt_scales_per_row(n, C), 1, "scales"))
+
+
+def mhc_ckpt_pack(B, n, C, X_t, codes, scales, stream=None, check=True):
+    """The 8-bit checkpoint of X_t: codes (E4M3 or uint8 [B, n*C]) and scales
+    (uint8 [B, mhc_ckpt_scales_per_row(n, C)]); see include/mhc.h."""
+    _here(X_t, codes, scales)
+    st = load().mhc_ckpt_pack(int(B), int(n), int(C), _ptr(X_t, _Sizes(B, n, C).x, 2, "X_t"),
+                              *_ckpt_ptrs(B, n, C, codes, scales), _stream(stream))
+    if check:
+        _check(st, "mhc_ckpt_pack")
+    return st
+
+
+def mhc_ckpt_unpack(B, n, C, codes, scales, X_t, stream=None, check=True):
+    """X_t in bf16 from its checkpoint (see include/mhc.h)."""
+    _here(X_t, codes, scales)
+    st = load().mhc_ckpt_unpack(int(B), int(n), int(C), *_ckpt_ptrs(B, n, C, codes, scales),
+                                _ptr(X_t, _Sizes(B, n, C).x, 2, "X_t"), _stream(stream))
+    if check:
+        _check(st, "mhc_ckpt_unpack")
+    return st
+
+
+def _post_res_bwd(fn, name, held, B, n, C, F_out, H, dX_next, dF_out, dH, stream, check):
+    z = _Sizes(B, n, C)
+    _here(F_out, H, dX_next, dF_out, dH)
+    st = fn(int(B), int(n), int(C), *held, _ptr(F_out, z.f, 2, "F_out"), _ptr(H, z.coef, 4, "H"),
+            _ptr(dX_next, z.x, 2, "dX_next"), _ptr(dF_out, z.f, 2, "dF_out"), _ptr(dH, z.coef, 4, "dH"),
+            _stream(stream))
+    if check:
+        _check(st, name)
+    return st
+
+
+def mhc_post_res_bwd(B, n, C, X_t, F_out, H, dX_next, dF_out, dH, stream=None, check=True):
+    """Gradients of step (4b) with respect to F_out and H (see include/mhc.h)."""
+    _here(X_t)
+    return _post_res_bwd(load().mhc_post_res_bwd, "mhc_post_res_bwd", (_ptr(X_t, _Sizes(B, n, C).x, 2, "X_t"),),
+                         B, n, C, F_out, H, dX_next, dF_out, dH, stream, check)
+
+
+def mhc_post_res_bwd_ckpt(B, n, C, codes, scales, F_out, H, dX_next, dF_out, dH, stream=None, check=True):
+    """mhc_post_res_bwd with X_t as its checkpoint (see include/mhc.h)."""
+    _here(codes, scales)
+    return _post_res_bwd(load().mhc_post_res_bwd_ckpt, "mhc_post_res_bwd_ckpt", _ckpt_ptrs(B, n, C, codes, scales),
+                         B, n, C, F_out, H, dX_next, dF_out, dH, stream, check)
+
+
+def mhc_coeffs_pre_bwd_workspace_size(B, n, C):
+    return int(load().mhc_coeffs_pre_bwd_workspace_size(int(B), int(n), int(C)))
+
+
+def _coeffs_pre_bwd(fn, name, held, B, n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res, logits, r,
+                    H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace, workspace_bytes,
+                    stream, check):
+    z, n = _Sizes(B, n, C), int(n)
+    _here(phi, b_pre, b_post, b_res, logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res,
+          workspace)
+    wb = _ws_bytes(workspace, workspace_bytes)
+    pp, bp, bq, br, lg, rr, hh = _coeff_args(z, phi, b_pre, b_post, b_res, logits, r, H)
+    # The parameters' gradients are written at B == 0 too.
+    st = fn(int(B), n, int(C), *held, pp, float(alpha_pre), float(alpha_post), float(alpha_res), bp, bq, br, lg, rr,
+            hh, _ptr(dX_next, z.x, 2, "dX_next"), _ptr(dH, z.coef, 4, "dH"), _ptr(dF_pre, z.f, 2, "dF_pre"),
+            _ptr(dX_t, z.x, 2, "dX_t"), _ptr(dphi, n * int(C) * (n * n + 2 * n) * 4, 4, "dphi"),
+            _ptr(dalpha, 12, 4, "dalpha"), _ptr(db_pre, n * 4, 4, "db_pre"), _ptr(db_post, n * 4, 4, "db_post"),
+            _ptr(db_res, n * n * 4, 4, "db_res"), _ptr(workspace, wb, None, "workspace"), wb, _stream(stream))
+    if check:
+        _check(st, name)
+    return st
+
+
+def mhc_coeffs_pre_bwd(B, n, C, X_t, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res, logits, r, H,
+                       dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace,
+                       workspace_bytes=None, stream=None, check=True):
+    """Gradients of steps (1)-(4a) and of X_t through the apply (see include/mhc.h)."""
+    _here(X_t)
+    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd, "mhc_coeffs_pre_bwd",
+                           (_ptr(X_t, _Sizes(B, n, C).x, 2, "X_t"),), B, n, C, phi, alpha_pre, alpha_post, alpha_res,
+                           b_pre, b_post, b_res, logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre,
+                           db_post, db_res, workspace, workspace_bytes, stream, check)
+
+
+def mhc_coeffs_pre_bwd_ckpt(B, n, C, codes, scales, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res,
+                            logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res,
+                            workspace, workspace_bytes=None, stream=None, check=True):
+    """mhc_coeffs_pre_bwd with X_t as its checkpoint (see include/mhc.h)."""
+    _here(codes, scales)
+    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd_ckpt, "mhc_coeffs_pre_bwd_ckpt",
+                           _ckpt_ptrs(B, n, C, codes, scales), B, n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre,
+                           b_post, b_res, logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post,
+                           db_res, workspace, workspace_bytes, stream, check)
+
+
+def mhc_embed(B, n, C, V, tokens, table, scale, X_0, stream=None, check=True):
+    """X_0: the scaled embeddings of the tokens (int64) in every stream (see include/mhc.h)."""
+    B, n, C, V = int(B), int(n), int(C), int(V)
+    _here(tokens, table, X_0)
+    st = load().mhc_embed(B, n, C, V, _ptr(tokens, max(B, 0) * 8, 8, "tokens"),
+                          _ptr(table, max(V, 0) * C * 2 if B > 0 else 0, 2, "table"), float(scale),
+                          _ptr(X_0, _Sizes(B, n, C).x, 2, "X_0"), _stream(stream))
+    if check:
+        _check(st, "mhc_embed")
+    return st
+
+
+def mhc_embed_bwd_workspace_size(B, n, C, V):
+    return int(load().mhc_embed_bwd_workspace_size(int(B), int(n), int(C), int(V)))
+
+
+def mhc_embed_bwd(B, n, C, V, tokens, dX_0, scale, dtable, workspace, accumulate=False, workspace_bytes=None,
+                  stream=None, check=True):
+    """The embedding table's gradient (fp32 [V, C]), overwritten or, with
+    accumulate, added to (see include/mhc.h)."""
+    B, n, C, V = int(B), int(n), int(C), int(V)
+    _here(tokens, dX_0, dtable, workspace)
+    wb = _ws_bytes(workspace, workspace_bytes)
+    st = load().mhc_embed_bwd(B, n, C, V, _ptr(tokens, max(B, 0) * 8, 8, "tokens"),
+                              _ptr(dX_0, _Sizes(B, n, C).x, 2, "dX_0"), float(scale), int(bool(accumulate)),
+                              _ptr(dtable, max(V, 0) * C * 4, 4, "dtable"),
+                              _ptr(workspace, wb, None, "workspace"), wb, _stream(stream))
+    if check:
+        _check(st, "mhc_embed_bwd")
     return st
 
 
