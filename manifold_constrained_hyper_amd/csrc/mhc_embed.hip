@@ -5,10 +5,12 @@
 //   dtable[v, :] = scale * sum over {b : token[b] = v} and i of dX_0[b, i, :]
 //
 // The gradient goes over the rows in the order of their tokens (and of their
-// index where tokens are equal), so that a table row is summed by one
-// workgroup in a fixed order, without atomics.
+// index where tokens are equal): equal tokens are neighbours then, each table
+// row is summed in a fixed order without atomics, and dX_0 is read once.
 #include "mhc_device.h"
 #include "mhc_train.h"
+
+#include <utility>
 
 namespace mhc {
 
@@ -36,66 +38,285 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t *__restri
   }
 }
 
-// Position of each row in the order of (token, row), by counting the rows
-// before it.
-__global__ __launch_bounds__(kThreads) void order_kernel(const int64_t *__restrict__ tokens, uint32_t B,
-                                                         int64_t *__restrict__ keys, int32_t *__restrict__ rows) {
-  __shared__ int64_t tile[kThreads];
-  const uint64_t b = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t mine = b < B ? tokens[b] : 0;
-  uint32_t before = 0;
-  for (uint64_t t0 = 0; t0 < B; t0 += kThreads) {
-    const uint64_t t = t0 + threadIdx.x;
-    __syncthreads();
-    if (t < B) tile[threadIdx.x] = tokens[t];
-    __syncthreads();
-    const uint32_t m = (uint32_t)(B - t0 < kThreads ? B - t0 : kThreads);
-    for (uint32_t k = 0; k < m; ++k) before += tile[k] < mine || (tile[k] == mine && t0 + k < b);
+// -- the rows in the order of their tokens ----------------------------------
+//
+// A key is (token << 32) | row; tokens outside the table get kNoToken, which
+// sorts last.  Keys are all different, so any correct sort gives the same
+// order.  Tiles of 1024 keys are sorted in one workgroup each; then runs are
+// joined 16 at a time: a key's place in the joined run is its place in its
+// own run plus, for each other run, the number of smaller keys there (a
+// binary search).  One launch for up to 1024 rows, two for up to 16384.
+typedef unsigned long long u64;
+constexpr uint32_t kNoToken = 0xffffffffu;
+constexpr uint32_t kTile = 1024, kJoin = 16;
+
+__device__ __forceinline__ uint32_t token_of(u64 key) { return (uint32_t)(key >> 32); }
+
+// Bitonic sort, one key a thread: partners inside a wave trade by lane moves,
+// others through LDS (10 of the 55 steps).
+__global__ __launch_bounds__(kTile) void sort_tiles_kernel(const int64_t *__restrict__ tokens, uint32_t B, int64_t V,
+                                                           u64 *__restrict__ keys) {
+  __shared__ u64 swap[kTile];
+  const uint32_t t = threadIdx.x;
+  const uint64_t row = (uint64_t)blockIdx.x * kTile + t;
+  u64 key = ~0ull;
+  if (row < B) {
+    const int64_t id = tokens[row];
+    key = ((u64)(id >= 0 && id < V ? (uint32_t)id : kNoToken) << 32) | row;
   }
-  if (b < B) {
-    keys[before] = mine;
-    rows[before] = (int32_t)b;
-  }
+  for (uint32_t size = 2; size <= kTile; size <<= 1)
+    for (uint32_t d = size >> 1; d > 0; d >>= 1) {
+      u64 other;
+      if (d >= 64) {
+        __syncthreads();
+        swap[t] = key;
+        __syncthreads();
+        other = swap[t ^ d];
+      } else {
+        other = __shfl_xor(key, (int)d);
+      }
+      const bool up = (t & size) == 0, low = (t & d) == 0;
+      const bool less = key < other;
+      key = (up == low) == less ? key : other;
+    }
+  if (row < B) keys[row] = key;
 }
 
-__global__ __launch_bounds__(kThreads) void zero_table_kernel(f32x4 *__restrict__ p, uint64_t count) {
-  for (uint64_t t = (uint64_t)blockIdx.x * kThreads + threadIdx.x; t < count; t += (uint64_t)gridDim.x * kThreads)
-    p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-}
-
-// A workgroup for each place in the sorted order that begins a token.
-template <int NS>
-__global__ __launch_bounds__(kThreads) void table_kernel(const int64_t *__restrict__ keys,
-                                                         const int32_t *__restrict__ rows,
-                                                         const u32x4 *__restrict__ G, float scale, bool accumulate,
-                                                         f32x4 *__restrict__ dtable, uint32_t B, uint32_t cvec,
-                                                         int64_t V) {
-  for (uint32_t p = blockIdx.x; p < B; p += gridDim.x) {
-    const int64_t id = keys[p];
-    if (id < 0 || id >= V || (p > 0 && keys[p - 1] == id)) continue;
-    for (uint32_t v = threadIdx.x; v < cvec; v += kThreads) {
-      float acc[8];
+// Runs of `run` sorted keys -> runs of kJoin times that.
+__global__ __launch_bounds__(kThreads) void join_runs_kernel(const u64 *__restrict__ in, u64 *__restrict__ out,
+                                                             uint32_t B, uint64_t run) {
+  const uint64_t p = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (p >= B) return;
+  const u64 key = in[p];
+  const uint64_t mine = p / run, first = mine / kJoin * kJoin;
+  uint64_t at = p - mine * run;
+  for (uint64_t q0 = first; q0 < first + kJoin; q0 += 4) {
+    uint64_t lo[4], len[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-      for (uint32_t q = p; q < B && keys[q] == id; ++q) {
+    for (int u = 0; u < 4; ++u) {
+      const uint64_t q = q0 + u;
+      lo[u] = q * run;
+      len[u] = q == mine || lo[u] >= B ? 0 : (B - lo[u] < run ? B - lo[u] : run);
+    }
+    // Four searches side by side; [lo, lo + len) holds the first key that is not smaller.
+    for (uint64_t left = run; left > 0; left >>= 1) {
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const u32x4 g = G[((size_t)rows[q] * NS + i) * cvec + v];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            acc[2 * w] += bf16_lo(g[w]);
-            acc[2 * w + 1] += bf16_hi(g[w]);
-          }
+      for (int u = 0; u < 4; ++u) {
+        if (len[u] == 0) continue;
+        const uint64_t half = len[u] >> 1;
+        if (in[lo[u] + half] < key) {
+          lo[u] += half + 1;
+          len[u] -= half + 1;
+        } else {
+          len[u] = half;
         }
       }
-      f32x4 *o = dtable + ((size_t)id * cvec + v) * 2;
+    }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f32x4 x = f32x4{acc[4 * h], acc[4 * h + 1], acc[4 * h + 2], acc[4 * h + 3]} * scale;
-        if (accumulate) x += o[h];
-        o[h] = x;
+    for (int u = 0; u < 4; ++u)
+      if (q0 + u != mine && (q0 + u) * run < B) at += lo[u] - (q0 + u) * run;
+  }
+  out[first * run + at] = key;
+}
+
+// First place whose token is not below `token`.
+__device__ __forceinline__ uint32_t first_place(const u64 *keys, uint32_t B, u64 token) {
+  uint32_t lo = 0, len = B;
+  while (len > 0) {
+    const uint32_t half = len >> 1;
+    if ((keys[lo + half] >> 32) < token) {
+      lo += half + 1;
+      len -= half + 1;
+    } else {
+      len = half;
+    }
+  }
+  return lo;
+}
+
+// -- the table's gradient ---------------------------------------------------
+
+__device__ __forceinline__ void write_row(f32x4 *o, const float (&acc)[8], float scale, bool accumulate) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    f32x4 x = f32x4{acc[4 * h], acc[4 * h + 1], acc[4 * h + 2], acc[4 * h + 3]} * scale;
+    if (accumulate) x += o[h];
+    __builtin_nontemporal_store(x, o + h);
+  }
+}
+
+// A wave takes `rb` places of the sorted order (a block) and 512 channels and
+// adds up each token's rows in their order.  A token whose rows all lie in
+// the block is written to the table; a block's first token that began before
+// it, and its last that goes on after it, are left in `part` ([blocks][2][C]:
+// from the left, to the right) for the join below.  Workgroups from sum_wgs
+// on write zeros to the table rows that have no token, kZeroRows each.
+constexpr int kAhead = 16;  // 16-byte loads a lane has in flight
+constexpr uint32_t kZeroRows = 8;
+
+__device__ __forceinline__ void zero_rows(const u64 *keys, uint32_t B, uint64_t v0, uint32_t V, uint32_t cvec,
+                                          f32x4 *dtable) {
+  const uint32_t lane = threadIdx.x & 63;
+  bool absent = false;
+  if (lane < kZeroRows && v0 + lane < V) {
+    const uint32_t at = first_place(keys, B, v0 + lane);
+    absent = at >= B || token_of(keys[at]) != v0 + lane;
+  }
+  uint32_t rows = (uint32_t)__ballot(absent);
+  while (rows) {
+    const uint64_t v = v0 + (uint32_t)__builtin_ctz(rows);
+    rows &= rows - 1;
+    for (uint32_t c = threadIdx.x; c < 2 * cvec; c += kThreads)
+      __builtin_nontemporal_store(f32x4{0.f, 0.f, 0.f, 0.f}, dtable + v * 2 * cvec + c);
+  }
+}
+
+template <int NS>
+__device__ __forceinline__ void sum_block(const u64 *__restrict__ keys, const u32x4 *__restrict__ G, float scale,
+                                          bool accumulate, f32x4 *__restrict__ dtable, float *__restrict__ part,
+                                          uint32_t B, uint32_t cvec, uint32_t rb, uint32_t block, uint32_t slice) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t v = slice * 64 + lane;
+  const uint32_t p0 = block * rb, m = B - p0 < rb ? B - p0 : rb;
+  const u64 key = lane < m ? keys[p0 + lane] : ~0ull;
+  const uint32_t tok = token_of(key), row = (uint32_t)key;
+  const uint32_t before = p0 > 0 ? token_of(keys[p0 - 1]) : kNoToken;
+  const uint32_t after = p0 + m < B ? token_of(keys[p0 + m]) : kNoToken;
+  constexpr int U = kAhead / NS;
+  float acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  bool began = __builtin_amdgcn_readlane((int)tok, 0) != (int)before;
+  for (uint32_t base = 0; base < m; base += U) {
+    u32x4 g[U][NS];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t q = base + u;
+      if (q >= m || v >= cvec || (uint32_t)__builtin_amdgcn_readlane((int)tok, (int)q) == kNoToken) continue;
+      const uint32_t r = (uint32_t)__builtin_amdgcn_readlane((int)row, (int)q);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) g[u][i] = __builtin_nontemporal_load(G + ((size_t)r * NS + i) * cvec + v);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t q = base + u;
+      if (q >= m) break;
+      const uint32_t here = (uint32_t)__builtin_amdgcn_readlane((int)tok, (int)q);
+      if (here == kNoToken) return;  // and so are all after it
+      const uint32_t next = q + 1 < m ? (uint32_t)__builtin_amdgcn_readlane((int)tok, (int)(q + 1)) : after;
+      if (v < cvec) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            acc[2 * w] += bf16_lo(g[u][i][w]);
+            acc[2 * w + 1] += bf16_hi(g[u][i][w]);
+          }
+        const bool ends = next != here;
+        if (ends && began) {
+          write_row(dtable + ((size_t)here * cvec + v) * 2, acc, scale, accumulate);
+        } else if (ends || q + 1 == m) {
+          f32x4 *o = reinterpret_cast<f32x4 *>(part) + (((size_t)block * 2 + (began ? 1 : 0)) * cvec + v) * 2;
+          o[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
+          o[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+        }
+      }
+      if (next != here) {
+        began = true;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
       }
     }
+  }
+}
+
+template <int NS>
+__global__ __launch_bounds__(kThreads) void table_kernel(const u64 *__restrict__ keys, const u32x4 *__restrict__ G,
+                                                         float scale, bool accumulate, f32x4 *__restrict__ dtable,
+                                                         float *__restrict__ part, uint32_t B, uint32_t cvec,
+                                                         uint32_t slices, uint32_t rb, uint64_t items,
+                                                         uint64_t sum_wgs, uint64_t all_wgs, uint32_t V) {
+  for (uint64_t wg = blockIdx.x; wg < all_wgs; wg += gridDim.x) {
+    if (wg >= sum_wgs) {
+      zero_rows(keys, B, (wg - sum_wgs) * kZeroRows, V, cvec, dtable);
+      continue;
+    }
+    const uint64_t item = (uint64_t)uniform((int64_t)(wg * (kThreads / 64) + (threadIdx.x >> 6)));
+    if (item >= items) continue;
+    const uint64_t block = item / slices;
+    sum_block<NS>(keys, G, scale, accumulate, dtable, part, B, cvec, rb, (uint32_t)block,
+                  (uint32_t)(item - block * slices));
+  }
+}
+
+// The tokens whose rows span blocks: the piece that begins one, then the
+// pieces of the blocks that follow, in their order.  A workgroup a block and
+// slice; its four waves take a quarter of the following blocks each, and the
+// quarters are added in their order.
+__device__ __forceinline__ void join_part(const u64 *__restrict__ keys, const float *__restrict__ part, float scale,
+                                          bool accumulate, f32x4 *__restrict__ dtable, uint32_t B, uint32_t cvec,
+                                          uint32_t rb, uint32_t block, uint32_t slice) {
+  constexpr int W = kThreads / 64;
+  __shared__ float quarter[W - 1][8][64];
+  const uint32_t p0 = block * rb, p1 = p0 + rb;
+  if (p1 >= B) return;
+  const uint32_t tok = token_of(keys[p1]);
+  if (tok == kNoToken || token_of(keys[p1 - 1]) != tok) return;               // nothing goes on to the right
+  if (p0 > 0 && token_of(keys[p0]) == tok && token_of(keys[p0 - 1]) == tok) return;  // it did not begin here
+  const uint32_t last = (first_place(keys, B, (u64)tok + 1) - 1) / rb;
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, v = slice * 64 + lane;
+  const uint32_t follow = last - block, each = (follow + W - 1) / W;
+  const uint32_t lo = block + 1 + wave * each;
+  const uint32_t hi = lo + each < last + 1 ? lo + each : last + 1;
+  const f32x4 *src = reinterpret_cast<const f32x4 *>(part);
+  float acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  if (v < cvec) {
+    if (wave == 0) {
+      const f32x4 *s = src + (((size_t)block * 2 + 1) * cvec + v) * 2;
+      const f32x4 a = s[0], b = s[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = a[e], acc[4 + e] = b[e];
+    }
+    for (uint32_t k = lo; k < hi; k += 8) {
+      f32x4 a[8], b[8];
+#pragma unroll
+      for (uint32_t u = 0; u < 8; ++u)
+        if (k + u < hi) {
+          const f32x4 *s = src + ((size_t)(k + u) * 2 * cvec + v) * 2;
+          a[u] = s[0], b[u] = s[1];
+        }
+#pragma unroll
+      for (uint32_t u = 0; u < 8; ++u)
+        if (k + u < hi) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += a[u][e], acc[4 + e] += b[u][e];
+        }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) quarter[wave - 1][e][lane] = acc[e];
+  }
+  __syncthreads();
+  if (wave > 0 || v >= cvec) return;
+#pragma unroll
+  for (int w = 0; w < W - 1; ++w)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += quarter[w][e][lane];
+  write_row(dtable + ((size_t)tok * cvec + v) * 2, acc, scale, accumulate);
+}
+
+__global__ __launch_bounds__(kThreads) void join_parts_kernel(const u64 *__restrict__ keys,
+                                                              const float *__restrict__ part, float scale,
+                                                              bool accumulate, f32x4 *__restrict__ dtable, uint32_t B,
+                                                              uint32_t cvec, uint32_t slices, uint32_t rb,
+                                                              uint64_t items) {
+  for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint64_t block = item / slices;
+    join_part(keys, part, scale, accumulate, dtable, B, cvec, rb, (uint32_t)block, (uint32_t)(item - block * slices));
+    __syncthreads();
   }
 }
 
@@ -117,20 +338,28 @@ hipError_t embed_n(int64_t B, int64_t C, int64_t V, const int64_t *tokens, const
 template <int NS>
 hipError_t table_n(const EmbedBwdPlan &p, int64_t B, int64_t C, int64_t V, const int64_t *tokens, const void *G,
                    float scale, bool accumulate, float *dtable, char *ws, hipStream_t st) {
-  const uint32_t cvec = (uint32_t)(C / 8);
-  int64_t *keys = reinterpret_cast<int64_t *>(ws + p.keys);
-  int32_t *rows = reinterpret_cast<int32_t *>(ws + p.rows);
+  const uint32_t cvec = (uint32_t)(C / 8), slices = (cvec + 63) / 64, rows = (uint32_t)B, rb = (uint32_t)p.rb;
+  u64 *keys = reinterpret_cast<u64 *>(ws + p.keys), *other = reinterpret_cast<u64 *>(ws + p.other);
+  float *part = reinterpret_cast<float *>(ws + p.part);
   f32x4 *out = reinterpret_cast<f32x4 *>(dtable);
   hipError_t e;
-  if (!accumulate) {
-    const uint64_t count = (uint64_t)V * cvec * 2;
-    zero_table_kernel<<<wgs(count, kThreads, 1u << 22), kThreads, 0, st>>>(out, count);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  order_kernel<<<(uint32_t)((B + kThreads - 1) / kThreads), kThreads, 0, st>>>(tokens, (uint32_t)B, keys, rows);
+  sort_tiles_kernel<<<(uint32_t)((B + kTile - 1) / kTile), kTile, 0, st>>>(tokens, rows, V, keys);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  table_kernel<NS><<<wgs(B, 1, 1u << 22), kThreads, 0, st>>>(keys, rows, static_cast<const u32x4 *>(G), scale,
-                                                             accumulate, out, (uint32_t)B, cvec, V);
+  for (uint64_t run = kTile; run < (uint64_t)B; run *= kJoin) {
+    join_runs_kernel<<<(uint32_t)((B + kThreads - 1) / kThreads), kThreads, 0, st>>>(keys, other, rows, run);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    std::swap(keys, other);
+  }
+  const uint64_t blocks = (B + rb - 1) / rb, items = blocks * slices;
+  const uint64_t sum_wgs = (items + kThreads / 64 - 1) / (kThreads / 64);
+  const uint64_t all_wgs = sum_wgs + (accumulate ? 0 : (uint64_t)(V + kZeroRows - 1) / kZeroRows);
+  table_kernel<NS><<<wgs(all_wgs, 1, 1u << 22), kThreads, 0, st>>>(keys, static_cast<const u32x4 *>(G), scale,
+                                                                   accumulate, out, part, rows, cvec, slices, rb,
+                                                                   items, sum_wgs, all_wgs, (uint32_t)V);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (blocks > 1)
+    join_parts_kernel<<<wgs(items, 1, 1u << 22), kThreads, 0, st>>>(keys, part, scale, accumulate, out, rows, cvec,
+                                                                    slices, rb, items);
   return hipGetLastError();
 }
 
@@ -147,12 +376,15 @@ hipError_t launch_embed(int n, int64_t B, int64_t C, int64_t V, const int64_t *t
   }
 }
 
-EmbedBwdPlan plan_embed_bwd(int64_t B, int n, int64_t C, int64_t V) {
-  (void)n, (void)C, (void)V;
+EmbedBwdPlan plan_embed_bwd(int64_t B, int64_t C) {
   EmbedBwdPlan p;
+  const int64_t slices = (C + 511) / 512;
+  p.rb = B * slices >= 32 * 4096 ? 32 : 8;
+  const size_t list = ((size_t)B * 8 + 15) / 16 * 16;
   p.keys = 0;
-  p.rows = (size_t)B * 8;
-  p.total_bytes = (p.rows + (size_t)B * 4 + 15) / 16 * 16;
+  p.other = list;
+  p.part = 2 * list;
+  p.total_bytes = p.part + (size_t)((B + p.rb - 1) / p.rb) * 2 * (size_t)C * 4;
   return p;
 }
 

@@ -59,12 +59,14 @@ hipError_t launch_coeffs_pre_bwd(const CoeffsBwdPlan &p, int n, int64_t B, int64
 hipError_t launch_embed(int n, int64_t B, int64_t C, int64_t V, const int64_t *tokens, const void *table, float scale,
                         void *X_0, hipStream_t st);
 
-// Workspace of the embedding gradient: [B] sorted tokens (int64), then [B]
-// the row of each (int32).
+// Workspace of the embedding gradient (bytes from its start): two lists of
+// [B] sort keys (uint64), then fp32 [ceil(B / rb), 2, C] partial sums of the
+// tokens whose rows span blocks of rb places of the sorted order.
 struct EmbedBwdPlan {
-  size_t keys, rows, total_bytes;
+  int64_t rb;
+  size_t keys, other, part, total_bytes;
 };
-EmbedBwdPlan plan_embed_bwd(int64_t B, int n, int64_t C, int64_t V);
+EmbedBwdPlan plan_embed_bwd(int64_t B, int64_t C);
 hipError_t launch_embed_bwd(const EmbedBwdPlan &p, int n, int64_t B, int64_t C, int64_t V, const int64_t *tokens,
                             const void *dX_0, float scale, bool accumulate, float *dtable, void *ws, hipStream_t st);
 

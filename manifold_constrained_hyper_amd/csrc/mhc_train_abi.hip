@@ -187,7 +187,7 @@ int mhc_embed(int64_t B, int32_t n, int64_t C, int64_t V, const int64_t *tokens,
 
 size_t mhc_embed_bwd_workspace_size(int64_t B, int32_t n, int64_t C, int64_t V) {
   if (check_table(B, n, C, V) != MHC_OK || B == 0) return 0;
-  return plan_embed_bwd(B, n, C, V).total_bytes;
+  return plan_embed_bwd(B, C).total_bytes;
 }
 
 int mhc_embed_bwd(int64_t B, int32_t n, int64_t C, int64_t V, const int64_t *tokens, const void *dX_0, float scale,
@@ -200,7 +200,7 @@ int mhc_embed_bwd(int64_t B, int32_t n, int64_t C, int64_t V, const int64_t *tok
     st = check_buffers({}, {table});
     return st != MHC_OK || accumulate ? st : from_hip(launch_zero_f32(dtable, V * C, s));
   }
-  const EmbedBwdPlan plan = plan_embed_bwd(B, n, C, V);
+  const EmbedBwdPlan plan = plan_embed_bwd(B, C);
   st = check_buffers({{tokens, (size_t)B * 8, 8}, {dX_0, (size_t)B * n * C * 2, 16}},
                      {table, {workspace, plan.total_bytes, 16}});
   if (st != MHC_OK) return st;

@@ -442,6 +442,28 @@ def test_embedding_matches_oracle(B, n, C, V, how):
     assert torch.equal(twice, d.t)
 
 
+@pytest.mark.parametrize("how", ["any", "padded", "one"])
+@pytest.mark.parametrize("B,n,C,V", [(17001, 2, 4104, 900), (40000, 1, 8, 70000), (16384, 1, 520, 2)])
+def test_embedding_gradient_of_many_rows(B, n, C, V, how):
+    """More rows than one joining pass sorts, long blocks, and tokens whose
+    rows span hundreds of blocks (64-bit sums by torch)."""
+    _say(f"embedding gradient B={B} n={n} C={C} V={V} {how}")
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    tokens = _tokens(B, V, B + C, how)
+    G = torch.randn(B, n * C, generator=gen, device="cuda").to(torch.bfloat16)
+    ws = Guarded(mhc.mhc_embed_bwd_workspace_size(B, n, C, V), dtype=torch.uint8, fill=0xFF)
+    d = Guarded(V, C)
+    mhc.mhc_embed_bwd(B, n, C, V, tokens, G, 0.25, d.t, ws.t)
+    torch.cuda.synchronize()
+    assert d.check() and ws.check()
+    fine = (tokens >= 0) & (tokens < V)
+    g = G[fine].double().view(-1, n, C)
+    want = torch.zeros(V, C, dtype=torch.float64, device="cuda").index_add_(0, tokens[fine], 0.25 * g.sum(1))
+    total = torch.zeros_like(want).index_add_(0, tokens[fine], 0.25 * g.abs().sum(1))
+    count = torch.bincount(tokens[fine], minlength=V)[:, None]
+    assert bool(((d.t.double() - want).abs() <= (count * n + 2) * U * total).all())
+
+
 # -- a training step --------------------------------------------------------------------------------
 
 class Model:
