@@ -74,11 +74,7 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const u32x2 *__restric
     const uint32_t v = (uint32_t)(g - stream * slots_per_stream);
     if (v >= cvec) continue;
     const uint64_t at = stream * cvec + v;
-    Held8<true> h;
-    h.load(codes, scales, at, g >> 2);
-    float o[8];
-    h.widen(o);
-    X[at] = u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
+    X[at] = held_bf16(__builtin_nontemporal_load(codes + at), scales[g >> 2]);
   }
 }
 

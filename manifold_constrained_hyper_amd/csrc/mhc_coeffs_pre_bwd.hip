@@ -25,8 +25,23 @@ namespace mhc {
 
 namespace {
 
-constexpr int kSumThreads = 256;
 constexpr int64_t kMaxSumBlocks = 512;
+
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// How the matrix-core kernel below splits the work for n streams.
+template <int NS>
+struct Tiles {
+  static constexpr int N = NS * NS + 2 * NS;
+  static constexpr int KS = (N + 31) / 32;      // 32-wide steps over the coefficients (dlogit . phi^T)
+  static constexpr int MT = (N + 15) / 16;      // 16-row tiles of dphi^T
+  static constexpr int JW = NS == 8 ? 2 : NS;   // streams a wave forms dX and dphi of
+  static constexpr int GROUPS = NS / JW;        // waves that share a tile of rows and channels
+  static constexpr int HW = NS >= 4 ? 1 : 2;    // 32-channel steps a wave
+  static constexpr int CW = 32 * HW;            // channels a wave
+  // Bytes of the packed operands of a tile of 16 rows.
+  static constexpr int kRowsB = 2 * KS * 1024, kColsA = MT * 1024, kColsC = MT * 512;
+};
 
 // dH_pre [B, n]: a workgroup a row.
 template <int NS, bool CK, int W>
@@ -89,16 +104,39 @@ __device__ __forceinline__ float axis_sum(float x) {
 // the accurate ones: a 1 x 1 matrix normalises to exactly 1 and its gradient
 // to exactly 0, as in the definition.  The partial sums of db and dalpha are
 // kept in fp64 (few adds, and gates' gradients cancel over a batch).
+//
+// dlogit leaves in the matrix core's operand order, split into bf16 parts
+// whose sum is dlogit to 2^-17 (hi + mid) or 2^-25 (hi + mid + low) of it:
+//   rows_b  [tile][hi, mid][KS][lane][8]  B operand of dlogit . phi^T: lane
+//           16 q + i has coefficients 32 ks + 8 q .. + 7 of row i; two parts
+//           (the product is rounded to bf16)
+//   cols_a  [tile][MT][lane][8]  A operand of dphi^T += dlogit^T X: lane
+//           16 q + m has hi, then mid, of rows 4 q .. + 3 of coefficient
+//           16 mt + m;
+//   cols_c  [tile][MT][lane][4]  the same with the low parts (dphi is fp32).
+// Rows past the last and coefficients past N are zeros.
 template <int NS>
-__global__ __launch_bounds__(kSumThreads) void coeffs_bwd_kernel(
+constexpr int sum_threads() { return NS == 8 ? 1024 : 256; }  // a multiple of 16 rows a workgroup
+
+__device__ __forceinline__ float bf16_round(float x) { return bf16_lo(pack_bf16x2(x, 0.f)); }
+
+template <int NS>
+__global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
     const float *__restrict__ logits, const float *__restrict__ r_in, float alpha_pre, float alpha_post,
     float alpha_res, const float *__restrict__ b_pre, const float *__restrict__ b_post,
     const float *__restrict__ b_res, const float *__restrict__ dH, const float *__restrict__ dpre,
-    float *__restrict__ dl, float *__restrict__ turn, double *__restrict__ sums, uint32_t B, double inv_k) {
-  constexpr int NN = NS * NS, N = NN + 2 * NS, R = kSumThreads / NN;
+    u32x4 *__restrict__ rows_b, u32x4 *__restrict__ cols_a, u32x2 *__restrict__ cols_c, float *__restrict__ turn,
+    double *__restrict__ sums, uint32_t B, double inv_k) {
+  using T = Tiles<NS>;
+  constexpr int TH = sum_threads<NS>();
+  constexpr int NN = NS * NS, N = NN + 2 * NS, R = TH / NN;
   constexpr int GATES = (2 * NS + NN - 1) / NN;  // gates a lane: 2 at n = 1, else 1
   constexpr int IT = kSinkhornIters;
-  __shared__ double part[R][N + 3];
+  constexpr int NP = N | 1;  // odd: rows start in different LDS banks
+  __shared__ union {
+    float dl[R][NP];
+    double part[R][N + 3];
+  } sh;
   const int e = threadIdx.x % NN, slot = threadIdx.x / NN;
   double sum_res = 0.0, sum_gate[GATES] = {}, sum_a[3] = {};
   const uint32_t stride = gridDim.x * R;
@@ -150,9 +188,12 @@ __global__ __launch_bounds__(kSumThreads) void coeffs_bwd_kernel(
 #pragma unroll
     for (int o = 1; o < NN; o <<= 1) scaled += __shfl_xor(scaled, o);
 
+    float *out = sh.dl[slot];
+    out[2 * NS + e] = in ? dlr : 0.f;
+#pragma unroll
+    for (int q = 0; q < GATES; ++q)
+      if (e + q * NN < 2 * NS) out[e + q * NN] = in ? dl_gate[q] : 0.f;
     if (in) {
-      float *out = dl + (size_t)row * N;
-      out[2 * NS + e] = dlr;
       if (e == 0) turn[row] = (float)(-(double)scaled * inv_k / ((double)r * r));
       sum_res += dz;
       sum_a[2] += (double)dz * lr / r;
@@ -160,28 +201,64 @@ __global__ __launch_bounds__(kSumThreads) void coeffs_bwd_kernel(
       for (int q = 0; q < GATES; ++q) {
         const int k = e + q * NN;
         if (k < 2 * NS) {
-          out[k] = dl_gate[q];
           sum_gate[q] += dz_gate[q];
           sum_a[k >= NS ? 1 : 0] += (double)dz_gate[q] * lg[k] / r;
         }
       }
     }
+    __syncthreads();
+    const auto at_row = [&](int i, int k) { return k < N ? sh.dl[i][k] : 0.f; };
+    constexpr int kItems = T::KS + T::MT;  // rows_b steps (both parts at once), then cols tiles
+    const uint32_t tiles = (B + 15) / 16;
+    for (int w = threadIdx.x; w < R / 16 * kItems * 64; w += TH) {
+      const int lane = w & 63, item = (w >> 6) % kItems, tl = (w >> 6) / kItems;
+      const size_t tile = row0 / 16 + tl;
+      if (tile >= tiles) continue;
+      const int lo16 = lane & 15, q = lane >> 4;
+      if (item < T::KS) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = at_row(tl * 16 + lo16, 32 * item + 8 * q + j);
+        u32x4 hi, mid;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          hi[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+          mid[j] = pack_bf16x2(v[2 * j] - bf16_lo(hi[j]), v[2 * j + 1] - bf16_hi(hi[j]));
+        }
+        rows_b[((tile * 2 + 0) * T::KS + item) * 64 + lane] = hi;
+        rows_b[((tile * 2 + 1) * T::KS + item) * 64 + lane] = mid;
+      } else {
+        const int mt = item - T::KS;
+        float v[4], h[4], m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] = at_row(tl * 16 + 4 * q + j, 16 * mt + lo16);
+          h[j] = bf16_round(v[j]);
+          m[j] = bf16_round(v[j] - h[j]);
+          v[j] = v[j] - h[j] - m[j];
+        }
+        cols_a[(tile * T::MT + mt) * 64 + lane] = u32x4{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]),
+                                                        pack_bf16x2(m[0], m[1]), pack_bf16x2(m[2], m[3])};
+        cols_c[(tile * T::MT + mt) * 64 + lane] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
+    }
+    __syncthreads();
   }
   // [db_pre | db_post | db_res | dalpha_pre, _post, _res] of this workgroup
-  part[slot][2 * NS + e] = sum_res;
+  sh.part[slot][2 * NS + e] = sum_res;
 #pragma unroll
   for (int q = 0; q < GATES; ++q)
-    if (e + q * NN < 2 * NS) part[slot][e + q * NN] = sum_gate[q];
+    if (e + q * NN < 2 * NS) sh.part[slot][e + q * NN] = sum_gate[q];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
 #pragma unroll
     for (int o = 1; o < NN; o <<= 1) sum_a[k] += __shfl_xor(sum_a[k], o);
-    if (e == 0) part[slot][N + k] = sum_a[k];
+    if (e == 0) sh.part[slot][N + k] = sum_a[k];
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < N + 3; k += kSumThreads) {
+  for (int k = threadIdx.x; k < N + 3; k += TH) {
     double a = 0.0;
-    for (int s = 0; s < R; ++s) a += part[s][k];
+    for (int s = 0; s < R; ++s) a += sh.part[s][k];
     sums[(size_t)blockIdx.x * (N + 3) + k] = a;
   }
 }
@@ -199,77 +276,255 @@ __global__ __launch_bounds__(128) void sums_kernel(const double *__restrict__ su
   }
 }
 
-// dX: a lane takes eight channels of all streams of a row.
+// dX and the partial dphi, in one pass over G, X_t and dF_pre.
+//
+// A wave holds a tile of 16 rows and 32 channels at a time: lane 16 q + i has
+// channels 8 q .. 8 q + 7 of row i, of every stream, as loaded (16 rows x 64
+// bytes a load).  That is the matrix core's A layout (16 x 32, bf16), and the
+// C layout of a product whose rows are channels and whose columns are the
+// tile's rows, so both products happen where the data is:
+//
+//  * dlogit . phi^T: A = phi of 16 channels (from LDS, staged once), B =
+//    dlogit of the 16 rows.  Two of them, for channels 8 q + 0..3 and + 4..7
+//    of each lane, leave each lane its own eight sums; the row's terms
+//    (H_res, H_pre and the r term, a row's coefficients in its four lanes)
+//    are added in fp32 and dX is rounded once.
+//  * dphi^T += dlogit^T X needs X with its rows along K.  X times a 32 x 16
+//    selection (ones and zeros) moves it there: the product is X itself,
+//    exactly, with lane 16 q + c holding rows 4 q .. 4 q + 3 of channel c --
+//    the B layout.  dlogit^T goes in three bf16 parts (coeffs_bwd_kernel), two
+//    of them in one 32-deep product against the same X twice, so dphi has
+//    fp32's accuracy (the third's product has zeros in its other half: a
+//    16x16x16 product before a 16x16x32 one on the same sums gave results
+//    that changed from run to run).  Sums over a wave's rows stay in registers, are joined
+//    over the workgroup's row lanes through LDS and over the row ranges by
+//    dphi_sum_kernel, each in a fixed order.
+//
+// A NaN in X_t reaches dphi in the 32 channels around it (NaN times the
+// selection's zeros); a row with one has no finite r either.
 template <int NS, bool CK>
-__global__ __launch_bounds__(256) void dx_kernel(const void *__restrict__ X, const uint8_t *__restrict__ scales,
-                                                 const uint16_t *__restrict__ phi, const float *__restrict__ H,
-                                                 const u32x4 *__restrict__ G, const u32x4 *__restrict__ dF,
-                                                 const float *__restrict__ dl, const float *__restrict__ turn,
-                                                 u32x4 *__restrict__ dX, uint64_t total, uint32_t cvec,
-                                                 uint32_t blocks) {
-  constexpr int N = NS * NS + 2 * NS;
-  for (uint64_t t = (uint64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (uint64_t)gridDim.x * 256) {
-    const uint64_t row = t / cvec;
-    const uint32_t v = (uint32_t)(t - row * cvec);
-    const float *h = H + row * N, *d = dl + row * N;
-    const float c = turn[row];
-    float gw[NS][8], fw[8];
-#pragma unroll
-    for (int i = 0; i < NS; ++i) widen8(G[(row * NS + i) * cvec + v], gw[i]);
-    widen8(dF[row * cvec + v], fw);
-    for (int j = 0; j < NS; ++j) {
-      Held8<CK> x;
-      x.load(X, scales, (row * NS + j) * cvec + v, (row * NS + j) * blocks + (v >> 2));
-      float o[8], xw[8];
-      x.widen(xw);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        o[q] = fmaf(c, xw[q], h[j] * fw[q]);
-        const uint16_t *p = phi + ((size_t)j * cvec * 8 + (size_t)v * 8 + q) * N;
-        for (int k = 0; k < N; ++k) o[q] = fmaf(d[k], __uint_as_float((uint32_t)p[k] << 16), o[q]);
-#pragma unroll
-        for (int i = 0; i < NS; ++i) o[q] = fmaf(h[2 * NS + i * NS + j], gw[i][q], o[q]);
-      }
-      dX[(row * NS + j) * cvec + v] = u32x4{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                                            pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7])};
-    }
-  }
-}
+__global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
+    const char *__restrict__ X, const uint8_t *__restrict__ scales, const uint16_t *__restrict__ phi,
+    const float *__restrict__ H, const u32x4 *__restrict__ G, const u32x4 *__restrict__ dF,
+    const u32x4 *__restrict__ rows_b, const u32x4 *__restrict__ cols_a, const u32x2 *__restrict__ cols_c,
+    const float *__restrict__ turn, u32x4 *__restrict__ dX, float *__restrict__ out, uint32_t B, uint32_t tiles_each,
+    uint32_t cvec, uint32_t blocks, uint32_t slices, int wc) {
+  using T = Tiles<NS>;
+  constexpr int N = T::N, KS = T::KS, MT = T::MT, JW = T::JW, GROUPS = T::GROUPS, HW = T::HW;
+  constexpr int kPhi = 8 / GROUPS * HW * NS * 2 * KS * 64;  // 16-byte operands, all waves along the channels
+  constexpr int kJoin = 4 * JW * 2 * MT * 64;               // a step's sums of half the waves
+  __shared__ u32x4 lds[kPhi > kJoin ? kPhi : kJoin];
+  const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+  // wc waves along the channels (a power of two), GROUPS along the streams,
+  // the rest along the rows.
+  const int cw = wave / GROUPS % wc, group = wave % GROUPS, rl = wave / (GROUPS * wc), row_lanes = 8 / (GROUPS * wc);
+  const uint32_t slice = blockIdx.x % slices, range = blockIdx.x / slices;
+  const uint32_t v_wg = slice * (uint32_t)wc * (HW * 4);  // the workgroup's first vector of eight channels
+  const uint32_t v_wave = v_wg + cw * (HW * 4);
+  const int lo16 = lane & 15, q = lane >> 4, j0 = group * JW;
 
-// Partial dphi over a range of rows: a lane takes eight rows of phi (eight
-// channels of a stream) and eight of its columns.
-template <int NS, bool CK>
-__global__ __launch_bounds__(256) void dphi_kernel(const void *__restrict__ X, const uint8_t *__restrict__ scales,
-                                                   const float *__restrict__ dl, float *__restrict__ out, uint32_t B,
-                                                   uint32_t rows, uint32_t cvec, uint32_t blocks) {
-  constexpr int N = NS * NS + 2 * NS;
-  const uint32_t kv = blockIdx.x * 256 + threadIdx.x;
-  if (kv >= NS * cvec) return;
-  const uint32_t j = kv / cvec, v = kv - j * cvec, col = blockIdx.y * 8;
-  const uint32_t lo = blockIdx.z * rows, hi = min(B, lo + rows);
-  float acc[8][8];
+  // phi: operand (cw, stream, step h, t, ks), lane 16 q + m: coefficients
+  // 32 ks + 8 q .. + 7 of channel 32 (HW cw + h) + 8 (m / 4) + 4 t + m % 4.
+  for (int w = threadIdx.x; w < wc * (HW * NS * 2 * KS * 64); w += 512) {
+    const int l = w & 63, ks = (w >> 6) % KS, rest = (w >> 6) / KS;
+    const int t = rest & 1, h = (rest >> 1) % HW, j = rest / (2 * HW) % NS, s = rest / (2 * HW * NS);
+    const uint32_t v = v_wg + (s * HW + h) * 4 + ((l & 15) >> 2);
+    const int k0 = 32 * ks + 8 * (l >> 4);
+    u32x4 a = {0u, 0u, 0u, 0u};
+    if (v < cvec && k0 < N) {
+      const size_t at = ((size_t)j * cvec * 8 + (size_t)v * 8 + 4 * t + (l & 3)) * N + k0;
+      if constexpr (N % 8 == 0) {
+        a = load16(phi + at);
+      } else {
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
+        for (int k = 0; k < 8; ++k)
+          if (k0 + k < N) a[k / 2] |= (uint32_t)phi[at + k] << (16 * (k & 1));
+      }
+    }
+    lds[w] = a;
+  }
+  // Selections: channels 16 s .. 16 s + 15 of the 32.
+  s16x8 sel[2];
 #pragma unroll
-    for (int m = 0; m < 8; ++m) acc[q][m] = 0.f;
-  for (uint32_t row = lo; row < hi; ++row) {
-    Held8<CK> x;
-    x.load(X, scales, ((size_t)row * NS + j) * cvec + v, ((size_t)row * NS + j) * blocks + (v >> 2));
-    float xw[8];
-    x.widen(xw);
+  for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const float d = col + m < N ? dl[(size_t)row * N + col + m] : 0.f;
+    for (int j = 0; j < 8; ++j) sel[s][j] = 8 * q + j == 16 * s + lo16 ? (short)0x3f80 : (short)0;
+  f32x4 acc[JW][HW][2][MT];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q][m] = fmaf(xw[q], d, acc[q][m]);
+  for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+    for (int h = 0; h < HW; ++h)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) acc[jj][h][s][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+
+  const uint32_t tiles = (B + 15) / 16, first = range * tiles_each;
+  const uint32_t last = tiles - first < tiles_each ? tiles : first + tiles_each;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  for (uint32_t tile = first + rl; tile < last; tile += row_lanes) {
+    const uint32_t row = tile * 16 + lo16;
+    const bool row_in = row < B;
+    bf16x8 bh[KS], bm[KS], ca[MT], cc[MT];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      bh[ks] = __builtin_bit_cast(bf16x8, rows_b[((size_t)(tile * 2 + 0) * KS + ks) * 64 + lane]);
+      bm[ks] = __builtin_bit_cast(bf16x8, rows_b[((size_t)(tile * 2 + 1) * KS + ks) * 64 + lane]);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      ca[mt] = __builtin_bit_cast(bf16x8, cols_a[((size_t)tile * MT + mt) * 64 + lane]);
+      const u32x2 low = cols_c[((size_t)tile * MT + mt) * 64 + lane];
+      cc[mt] = __builtin_bit_cast(bf16x8, u32x4{low[0], low[1], 0u, 0u});
+    }
+    float hres[NS][JW], hpre[JW], c = 0.f;
+#pragma unroll
+    for (int jj = 0; jj < JW; ++jj) {
+      hpre[jj] = row_in ? H[(size_t)row * N + j0 + jj] : 0.f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) hres[i][jj] = row_in ? H[(size_t)row * N + 2 * NS + i * NS + j0 + jj] : 0.f;
+    }
+    if (row_in) c = turn[row];
+#pragma unroll
+    for (int h = 0; h < HW; ++h) {
+      const uint32_t v = v_wave + h * 4 + q;
+      const bool in = row_in && v < cvec;
+      const size_t at = (size_t)row * NS * cvec + v;
+      u32x4 g[NS], f = {0u, 0u, 0u, 0u};
+      u32x4 x[JW];
+#pragma unroll
+      for (int i = 0; i < NS; ++i) g[i] = in ? G[at + (size_t)i * cvec] : u32x4{0u, 0u, 0u, 0u};
+      if (in) f = dF[(size_t)row * cvec + v];
+      if constexpr (CK) {
+        u32x2 code[JW];
+        int s[JW];
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj) {
+          code[jj] = u32x2{0u, 0u};
+          s[jj] = 1;
+          if (in) {
+            code[jj] = *reinterpret_cast<const u32x2 *>(X + (at + (size_t)(j0 + jj) * cvec) * 8);
+            s[jj] = scales[((size_t)row * NS + j0 + jj) * blocks + (v >> 2)];
+          }
+        }
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj) x[jj] = held_bf16(code[jj], s[jj]);
+      } else {
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj)
+          x[jj] = in ? load16(X + (at + (size_t)(j0 + jj) * cvec) * 16) : u32x4{0u, 0u, 0u, 0u};
+      }
+      float o[JW][8];
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj) {
+        f32x4 d[2] = {zero, zero};
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const bf16x8 a =
+                __builtin_bit_cast(bf16x8, lds[((((cw * NS + j0 + jj) * HW + h) * 2 + t) * KS + ks) * 64 + lane]);
+            d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bm[ks], d[t], 0, 0, 0);
+            d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bh[ks], d[t], 0, 0, 0);
+          }
+        float xw[8];
+        widen8(x[jj], xw);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(c, xw[e], d[e >> 2][e & 3]);
+      }
+      {
+        float fw[8];
+        widen8(f, fw);
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hpre[jj], fw[e], o[jj][e]);
+      }
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        float gw[8];
+        widen8(g[i], gw);
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hres[i][jj], gw[e], o[jj][e]);
+      }
+      if (in) {
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj)
+          dX[at + (size_t)(j0 + jj) * cvec] =
+              u32x4{pack_bf16x2(o[jj][0], o[jj][1]), pack_bf16x2(o[jj][2], o[jj][3]),
+                    pack_bf16x2(o[jj][4], o[jj][5]), pack_bf16x2(o[jj][6], o[jj][7])};
+      }
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const f32x4 m = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, x[jj]), __builtin_bit_cast(bf16x8, sel[s]), zero, 0, 0, 0);
+          const uint32_t p0 = pack_bf16x2(m[0], m[1]), p1 = pack_bf16x2(m[2], m[3]);
+          const bf16x8 twice = __builtin_bit_cast(bf16x8, u32x4{p0, p1, p0, p1});
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cc[mt], twice, acc[jj][h][s][mt], 0, 0, 0);
+            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ca[mt], twice, acc[jj][h][s][mt], 0, 0, 0);
+          }
+        }
+      }
     }
   }
-  float *o = out + ((size_t)blockIdx.z * NS * cvec * 8 + (size_t)kv * 8) * N;
+
+  // Lane 16 q + c of acc[jj][h][s][mt]: coefficients 16 mt + 4 q .. + 3 of
+  // the wave's channel 32 h + 16 s + c.  Row lanes past the first hand theirs
+  // over through LDS, one after the other.
+  float *po = out + (size_t)range * NS * cvec * 8 * N;
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
+  for (int h = 0; h < HW; ++h) {
+    for (int r = 1; r < row_lanes; ++r) {
+      __syncthreads();
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
-      if (col + m < N) o[(size_t)q * N + col + m] = acc[q][m];
+      for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            u32x4 *slot = lds + ((((cw * GROUPS + group) * JW + jj) * 2 + s) * MT + mt) * 64 + lane;
+            if (rl == r) *slot = __builtin_bit_cast(u32x4, acc[jj][h][s][mt]);
+          }
+      __syncthreads();
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const u32x4 *slot = lds + ((((cw * GROUPS + group) * JW + jj) * 2 + s) * MT + mt) * 64 + lane;
+            if (rl == 0) acc[jj][h][s][mt] += __builtin_bit_cast(f32x4, *slot);
+          }
+    }
+    if (rl > 0) continue;
+#pragma unroll
+    for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const f32x4 a = acc[jj][h][s][mt];
+          const uint32_t ch = v_wave * 8 + 32 * h + 16 * s + lo16;
+          const int k = 16 * mt + 4 * q;
+          if (ch < cvec * 8 && k < N) {
+            float *p = po + ((size_t)(j0 + jj) * cvec * 8 + ch) * N + k;
+            if constexpr (N % 4 == 0) {
+              *reinterpret_cast<f32x4 *>(p) = a;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (k + e < N) p[e] = a[e];
+            }
+          }
+        }
+  }
 }
 
 // dphi: the partial sums in the order of their row ranges.
@@ -293,30 +548,29 @@ uint32_t wgs(uint64_t work, uint64_t per, uint64_t most) {
 
 template <int NS, bool CK>
 hipError_t launch_t(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBwdArgs &a, char *ws, hipStream_t st) {
-  constexpr int N = NS * NS + 2 * NS;
-  float *dl = reinterpret_cast<float *>(ws + p.dl), *turn = reinterpret_cast<float *>(ws + p.turn);
-  float *dpre = reinterpret_cast<float *>(ws + p.dpre), *part = reinterpret_cast<float *>(ws + p.dphi);
+  using T = Tiles<NS>;
+  u32x4 *rows_b = reinterpret_cast<u32x4 *>(ws + p.rows_b), *cols_a = reinterpret_cast<u32x4 *>(ws + p.cols_a);
+  u32x2 *cols_c = reinterpret_cast<u32x2 *>(ws + p.cols_c);
+  float *turn = reinterpret_cast<float *>(ws + p.turn), *dpre = reinterpret_cast<float *>(ws + p.dpre);
   double *sums = reinterpret_cast<double *>(ws + p.sums);
+  float *part = p.split > 1 ? reinterpret_cast<float *>(ws + p.dphi) : a.dphi;
   const uint32_t cvec = (uint32_t)(C / 8), blocks = (uint32_t)ckpt_blocks(C), rows = (uint32_t)B;
   const u32x4 *dF = static_cast<const u32x4 *>(a.dF_pre);
   hipError_t e;
   pre_dots_kernel<NS, CK, 4><<<wgs(B, 1, 1u << 22), 256, 0, st>>>(a.X.x, a.X.scales, dF, dpre, rows, cvec, blocks);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  coeffs_bwd_kernel<NS><<<(uint32_t)p.sum_blocks, kSumThreads, 0, st>>>(
-      a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre, a.b_post, a.b_res, a.dH, dpre, dl, turn, sums, rows,
-      1.0 / ((double)NS * (double)C));
+  coeffs_bwd_kernel<NS><<<(uint32_t)p.sum_blocks, sum_threads<NS>(), 0, st>>>(
+      a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre, a.b_post, a.b_res, a.dH, dpre, rows_b, cols_a, cols_c,
+      turn, sums, rows, 1.0 / ((double)NS * (double)C));
   if ((e = hipGetLastError()) != hipSuccess) return e;
   sums_kernel<<<1, 128, 0, st>>>(sums, (int)p.sum_blocks, NS, a.dalpha, a.db_pre, a.db_post, a.db_res);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const uint64_t total = (uint64_t)B * cvec;
-  dx_kernel<NS, CK><<<wgs(total, 256, 1u << 22), 256, 0, st>>>(
-      a.X.x, a.X.scales, static_cast<const uint16_t *>(a.phi), a.H, static_cast<const u32x4 *>(a.dX_next), dF, dl,
-      turn, static_cast<u32x4 *>(a.dX), total, cvec, blocks);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const dim3 grid(wgs((uint64_t)NS * cvec, 256, UINT32_MAX), (N + 7) / 8, (uint32_t)p.split);
-  dphi_kernel<NS, CK><<<grid, 256, 0, st>>>(a.X.x, a.X.scales, dl, part, rows, (uint32_t)p.rows, cvec, blocks);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const uint64_t count = (uint64_t)NS * C * N;
+  dx_dphi_kernel<NS, CK><<<(uint32_t)(p.slices * p.split), 512, 0, st>>>(
+      static_cast<const char *>(a.X.x), a.X.scales, static_cast<const uint16_t *>(a.phi), a.H,
+      static_cast<const u32x4 *>(a.dX_next), dF, rows_b, cols_a, cols_c, turn, static_cast<u32x4 *>(a.dX), part, rows,
+      (uint32_t)p.tiles_each, cvec, blocks, (uint32_t)p.slices, p.wc);
+  if ((e = hipGetLastError()) != hipSuccess || p.split == 1) return e;
+  const uint64_t count = (uint64_t)NS * C * T::N;
   dphi_sum_kernel<<<wgs(count, 256, 1u << 22), 256, 0, st>>>(part, a.dphi, count, (uint32_t)p.split);
   return hipGetLastError();
 }
@@ -328,22 +582,46 @@ hipError_t launch_n(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBw
 
 size_t up16(size_t v) { return (v + 15) / 16 * 16; }
 
+constexpr int64_t kRound = 256;
+
+template <int NS>
+CoeffsBwdPlan plan_n(int64_t B, int64_t C) {
+  using T = Tiles<NS>;
+  CoeffsBwdPlan p;
+  const int64_t K = (int64_t)NS * C, tiles = (B + 15) / 16;
+  p.wc = 1;  // waves along the channels, as many as there are channels for
+  while (p.wc < 8 / T::GROUPS && p.wc * T::CW < C) p.wc *= 2;
+  p.slices = (C + p.wc * T::CW - 1) / (p.wc * T::CW);
+  const int64_t row_lanes = 8 / (T::GROUPS * p.wc);
+  // One workgroup fits a compute unit: as many row ranges as make one round
+  // of them, and no range without a tile for each of its row lanes.
+  int64_t split = kRound / p.slices;
+  if (split > (tiles + row_lanes - 1) / row_lanes) split = (tiles + row_lanes - 1) / row_lanes;
+  if (split < 1) split = 1;
+  p.tiles_each = (tiles + split - 1) / split;
+  p.split = (tiles + p.tiles_each - 1) / p.tiles_each;
+  const int64_t per = sum_threads<NS>() / (NS * NS), groups = (B + per - 1) / per;
+  p.sum_blocks = groups < kMaxSumBlocks ? groups : kMaxSumBlocks;
+  p.rows_b = 0;
+  p.cols_a = p.rows_b + (size_t)tiles * T::kRowsB;
+  p.cols_c = p.cols_a + (size_t)tiles * T::kColsA;
+  p.turn = p.cols_c + (size_t)tiles * T::kColsC;
+  p.dpre = up16(p.turn + (size_t)B * 4);
+  p.sums = up16(p.dpre + (size_t)B * NS * 4);
+  p.dphi = up16(p.sums + (size_t)p.sum_blocks * (T::N + 3) * 8);
+  p.total_bytes = up16(p.dphi + (p.split > 1 ? (size_t)p.split * K * T::N * 4 : 0));
+  return p;
+}
+
 }  // namespace
 
 CoeffsBwdPlan plan_coeffs_pre_bwd(int64_t B, int n, int64_t C) {
-  CoeffsBwdPlan p;
-  const int64_t N = (int64_t)n * n + 2 * n, K = (int64_t)n * C;
-  p.split = B < 1024 ? 1 : B < 8192 ? 4 : 16;
-  p.rows = (B + p.split - 1) / p.split;
-  const int64_t per = kSumThreads / (n * n), groups = (B + per - 1) / per;
-  p.sum_blocks = groups < kMaxSumBlocks ? groups : kMaxSumBlocks;
-  p.dl = 0;
-  p.turn = up16(p.dl + (size_t)B * N * 4);
-  p.dpre = up16(p.turn + (size_t)B * 4);
-  p.sums = up16(p.dpre + (size_t)B * n * 4);
-  p.dphi = up16(p.sums + (size_t)p.sum_blocks * (N + 3) * 8);
-  p.total_bytes = up16(p.dphi + (size_t)p.split * K * N * 4);
-  return p;
+  switch (n) {
+    case 1: return plan_n<1>(B, C);
+    case 2: return plan_n<2>(B, C);
+    case 4: return plan_n<4>(B, C);
+    default: return plan_n<8>(B, C);
+  }
 }
 
 hipError_t launch_coeffs_pre_bwd(const CoeffsBwdPlan &p, int n, int64_t B, int64_t C, const CoeffsBwdArgs &a,

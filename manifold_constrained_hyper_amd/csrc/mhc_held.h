@@ -75,6 +75,18 @@ struct Held8<true> {
   }
 };
 
+// Eight codes and their scale byte as bf16 (exact, one conversion a pair).
+__device__ __forceinline__ u32x4 held_bf16(u32x2 codes, int s) {
+  const float f = ckpt_value(s);
+  u32x4 o;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    o[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)codes[w], f, false));
+    o[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)codes[w], f, true));
+  }
+  return o;
+}
+
 __device__ __forceinline__ void widen8(u32x4 v, float (&o)[8]) {
 #pragma unroll
   for (int w = 0; w < 4; ++w) {

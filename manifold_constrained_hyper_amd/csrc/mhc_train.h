@@ -29,16 +29,19 @@ hipError_t launch_post_res_bwd(int n, int64_t B, int64_t C, HeldX X, const void 
                                const void *dX_next, void *dF_out, float *dH, hipStream_t st);
 
 // Workspace of the coefficient and pre-mix gradient (bytes from its start):
-//   [dl, ...)    fp32 [B, N]      gradient of the logits
-//   [turn, ...)  fp32 [B]         the factor of X_t that r contributes
-//   [dpre, ...)  fp32 [B, n]      gradient of H_pre
-//   [sums, ...)  fp64 [blocks, N + 3]  partial sums of the bias and alpha gradients
-//   [dphi, ...)  fp32 [split, K, N]    partial sums of dphi
+//   rows_b, cols_a, cols_c   dlogit in bf16 parts, in matrix operand order, by
+//                            tiles of 16 rows (mhc_coeffs_pre_bwd.hip)
+//   turn   fp32 [B]          the factor of X_t that r contributes
+//   dpre   fp32 [B, n]       gradient of H_pre
+//   sums   fp64 [sum_blocks, N + 3]  partial sums of the bias and alpha gradients
+//   dphi   fp32 [split, K, N]        partial sums of dphi (split > 1)
 struct CoeffsBwdPlan {
-  int64_t split;       // row ranges of the dphi product
-  int64_t rows;        // rows in each
+  int wc;              // waves along the channels in a workgroup
+  int64_t slices;      // workgroups along the channels
+  int64_t split;       // row ranges
+  int64_t tiles_each;  // tiles of 16 rows in each
   int64_t sum_blocks;  // workgroups of the coefficient kernel
-  size_t dl, turn, dpre, sums, dphi, total_bytes;
+  size_t rows_b, cols_a, cols_c, turn, dpre, sums, dphi, total_bytes;
 };
 CoeffsBwdPlan plan_coeffs_pre_bwd(int64_t B, int n, int64_t C);
 
