@@ -29,18 +29,29 @@ constexpr int64_t kMaxSumBlocks = 512;
 
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-// How the matrix-core kernel below splits the work for n streams.
+// How dx_dphi_kernel splits the work for n streams.
 template <int NS>
 struct Tiles {
   static constexpr int N = NS * NS + 2 * NS;
   static constexpr int KS = (N + 31) / 32;      // 32-wide steps over the coefficients (dlogit . phi^T)
   static constexpr int MT = (N + 15) / 16;      // 16-row tiles of dphi^T
-  static constexpr int JW = NS == 8 ? 2 : NS;   // streams a wave forms dX and dphi of
+  static constexpr int JW = NS == 8 ? 1 : NS;   // streams a wave forms dX and dphi of
   static constexpr int GROUPS = NS / JW;        // waves that share a tile of rows and channels
-  static constexpr int HW = NS >= 4 ? 1 : 2;    // 32-channel steps a wave
+  static constexpr int HW = NS == 8 ? 2 : 1;    // 32-channel steps a wave
   static constexpr int CW = 32 * HW;            // channels a wave
-  // Bytes of the packed operands of a tile of 16 rows.
-  static constexpr int kRowsB = 2 * KS * 1024, kColsA = MT * 1024, kColsC = MT * 512;
+  // What dx_dphi_kernel needs of a tile of 16 rows, written by coeffs_bwd_kernel
+  // (byte offsets in the tile's record; every part is a multiple of 16):
+  //   rows_b  [hi, mid][KS][lane][8] bf16  B operand of dlogit . phi^T: lane
+  //           16 q + i has coefficients 32 ks + 8 q .. + 7 of row i
+  //   cols_a  [MT][lane][8] bf16  A operand of dphi^T += dlogit^T X: lane
+  //           16 q + m has hi, then mid, of rows 4 q .. + 3 of coefficient 16 mt + m
+  //   cols_c  [MT][lane][4] bf16  the same with the low parts
+  //   mix     [KH][16 rows] fp32  H_pre and H_res
+  //   turn    [16 rows] fp32      the factor of X_t that r contributes
+  static constexpr int KH = NS + NS * NS;
+  static constexpr int kColsA = 2 * KS * 1024, kColsC = kColsA + MT * 1024, kMix = kColsC + MT * 512;
+  static constexpr int kTurn = kMix + KH * 64, kBytes = kTurn + 64;
+  static constexpr int kChunks = (kBytes + 1023) / 1024, kStride = kChunks * 1024;
 };
 
 // dH_pre [B, n]: a workgroup a row.
@@ -105,16 +116,10 @@ __device__ __forceinline__ float axis_sum(float x) {
 // to exactly 0, as in the definition.  The partial sums of db and dalpha are
 // kept in fp64 (few adds, and gates' gradients cancel over a batch).
 //
-// dlogit leaves in the matrix core's operand order, split into bf16 parts
-// whose sum is dlogit to 2^-17 (hi + mid) or 2^-25 (hi + mid + low) of it:
-//   rows_b  [tile][hi, mid][KS][lane][8]  B operand of dlogit . phi^T: lane
-//           16 q + i has coefficients 32 ks + 8 q .. + 7 of row i; two parts
-//           (the product is rounded to bf16)
-//   cols_a  [tile][MT][lane][8]  A operand of dphi^T += dlogit^T X: lane
-//           16 q + m has hi, then mid, of rows 4 q .. + 3 of coefficient
-//           16 mt + m;
-//   cols_c  [tile][MT][lane][4]  the same with the low parts (dphi is fp32).
-// Rows past the last and coefficients past N are zeros.
+// dlogit leaves in the tiles' records, in the matrix core's operand order,
+// split into bf16 parts whose sum is dlogit to 2^-17 (hi + mid: for dX, which
+// is rounded to bf16) or 2^-25 (hi + mid + low: for dphi, fp32) of it.  Rows
+// past the last and coefficients past N are zeros.
 template <int NS>
 constexpr int sum_threads() { return NS == 8 ? 1024 : 256; }  // a multiple of 16 rows a workgroup
 
@@ -125,14 +130,14 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
     const float *__restrict__ logits, const float *__restrict__ r_in, float alpha_pre, float alpha_post,
     float alpha_res, const float *__restrict__ b_pre, const float *__restrict__ b_post,
     const float *__restrict__ b_res, const float *__restrict__ dH, const float *__restrict__ dpre,
-    u32x4 *__restrict__ rows_b, u32x4 *__restrict__ cols_a, u32x2 *__restrict__ cols_c, float *__restrict__ turn,
-    double *__restrict__ sums, uint32_t B, double inv_k) {
+    const float *__restrict__ H, char *__restrict__ records, double *__restrict__ sums, uint32_t B, double inv_k) {
   using T = Tiles<NS>;
   constexpr int TH = sum_threads<NS>();
   constexpr int NN = NS * NS, N = NN + 2 * NS, R = TH / NN;
   constexpr int GATES = (2 * NS + NN - 1) / NN;  // gates a lane: 2 at n = 1, else 1
   constexpr int IT = kSinkhornIters;
   constexpr int NP = N | 1;  // odd: rows start in different LDS banks
+  __shared__ float turn[R];
   __shared__ union {
     float dl[R][NP];
     double part[R][N + 3];
@@ -193,8 +198,8 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
 #pragma unroll
     for (int q = 0; q < GATES; ++q)
       if (e + q * NN < 2 * NS) out[e + q * NN] = in ? dl_gate[q] : 0.f;
+    if (e == 0) turn[slot] = in ? (float)(-(double)scaled * inv_k / ((double)r * r)) : 0.f;
     if (in) {
-      if (e == 0) turn[row] = (float)(-(double)scaled * inv_k / ((double)r * r));
       sum_res += dz;
       sum_a[2] += (double)dz * lr / r;
 #pragma unroll
@@ -214,6 +219,7 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
       const int lane = w & 63, item = (w >> 6) % kItems, tl = (w >> 6) / kItems;
       const size_t tile = row0 / 16 + tl;
       if (tile >= tiles) continue;
+      char *rec = records + tile * T::kStride;
       const int lo16 = lane & 15, q = lane >> 4;
       if (item < T::KS) {
         float v[8];
@@ -225,8 +231,9 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
           hi[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
           mid[j] = pack_bf16x2(v[2 * j] - bf16_lo(hi[j]), v[2 * j + 1] - bf16_hi(hi[j]));
         }
-        rows_b[((tile * 2 + 0) * T::KS + item) * 64 + lane] = hi;
-        rows_b[((tile * 2 + 1) * T::KS + item) * 64 + lane] = mid;
+        u32x4 *rows_b = reinterpret_cast<u32x4 *>(rec);
+        rows_b[item * 64 + lane] = hi;
+        rows_b[(T::KS + item) * 64 + lane] = mid;
       } else {
         const int mt = item - T::KS;
         float v[4], h[4], m[4];
@@ -237,10 +244,22 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
           m[j] = bf16_round(v[j] - h[j]);
           v[j] = v[j] - h[j] - m[j];
         }
-        cols_a[(tile * T::MT + mt) * 64 + lane] = u32x4{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]),
+        reinterpret_cast<u32x4 *>(rec + T::kColsA)[mt * 64 + lane] = u32x4{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]),
                                                         pack_bf16x2(m[0], m[1]), pack_bf16x2(m[2], m[3])};
-        cols_c[(tile * T::MT + mt) * 64 + lane] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        reinterpret_cast<u32x2 *>(rec + T::kColsC)[mt * 64 + lane] =
+            u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
       }
+    }
+    for (int w = threadIdx.x; w < R * (T::KH + 1); w += TH) {
+      const int i = w & 15, k = (w >> 4) % (T::KH + 1), tl = (w >> 4) / (T::KH + 1);
+      const size_t tile = row0 / 16 + tl, row = tile * 16 + i;
+      if (tile >= tiles) continue;
+      float x = 0.f;
+      if (k == T::KH)
+        x = turn[tl * 16 + i];
+      else if (row < B)
+        x = H[row * N + (k < NS ? k : k + NS)];  // the post block is not needed
+      reinterpret_cast<float *>(records + tile * T::kStride + T::kMix)[k * 16 + i] = x;
     }
     __syncthreads();
   }
@@ -263,32 +282,33 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
   }
 }
 
-// The workgroups' partial sums of db and dalpha, in their order.
-__global__ __launch_bounds__(128) void sums_kernel(const double *__restrict__ sums, int blocks, int n,
-                                                   float *__restrict__ dalpha, float *__restrict__ db_pre,
-                                                   float *__restrict__ db_post, float *__restrict__ db_res) {
-  const int N = n * n + 2 * n;
-  for (int k = threadIdx.x; k < N + 3; k += 128) {
-    double a = 0.0;
-    for (int b = 0; b < blocks; ++b) a += sums[(size_t)b * (N + 3) + k];
-    float *out = k < n ? db_pre + k : k < 2 * n ? db_post + (k - n) : k < N ? db_res + (k - 2 * n) : dalpha + (k - N);
-    *out = (float)a;
-  }
+// The workgroups' partial sums of db and dalpha: a workgroup for each sum, a
+// thread every 64th partial sum, then the threads as a tree.
+__global__ __launch_bounds__(64) void sums_kernel(const double *__restrict__ sums, int blocks, int n,
+                                                  float *__restrict__ dalpha, float *__restrict__ db_pre,
+                                                  float *__restrict__ db_post, float *__restrict__ db_res) {
+  const int N = n * n + 2 * n, k = blockIdx.x;
+  double a = 0.0;
+  for (int b = threadIdx.x; b < blocks; b += 64) a += sums[(size_t)b * (N + 3) + k];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) a += __shfl_xor(a, o);
+  float *out = k < n ? db_pre + k : k < 2 * n ? db_post + (k - n) : k < N ? db_res + (k - 2 * n) : dalpha + (k - N);
+  if (threadIdx.x == 0) *out = (float)a;
 }
 
 // dX and the partial dphi, in one pass over G, X_t and dF_pre.
 //
-// A wave holds a tile of 16 rows and 32 channels at a time: lane 16 q + i has
-// channels 8 q .. 8 q + 7 of row i, of every stream, as loaded (16 rows x 64
-// bytes a load).  That is the matrix core's A layout (16 x 32, bf16), and the
-// C layout of a product whose rows are channels and whose columns are the
-// tile's rows, so both products happen where the data is:
+// A wave takes 16 rows and 32 channels at a time: lane 16 q + i has channels
+// 8 q .. 8 q + 7 of row i, of every stream.  That is the matrix core's A
+// layout (16 x 32, bf16), and the C layout of a product whose rows are
+// channels and whose columns are the tile's rows, so both products happen
+// where the data is:
 //
-//  * dlogit . phi^T: A = phi of 16 channels (from LDS, staged once), B =
-//    dlogit of the 16 rows.  Two of them, for channels 8 q + 0..3 and + 4..7
-//    of each lane, leave each lane its own eight sums; the row's terms
-//    (H_res, H_pre and the r term, a row's coefficients in its four lanes)
-//    are added in fp32 and dX is rounded once.
+//  * dlogit . phi^T: A = phi of 16 channels (in registers for the whole
+//    kernel), B = dlogit of the 16 rows.  Two of them, for channels
+//    8 q + 0..3 and + 4..7 of each lane, leave each lane its own eight sums;
+//    the row's terms (H_res, H_pre and the r term) are added in fp32 and dX is
+//    rounded once.
 //  * dphi^T += dlogit^T X needs X with its rows along K.  X times a 32 x 16
 //    selection (ones and zeros) moves it there: the product is X itself,
 //    exactly, with lane 16 q + c holding rows 4 q .. 4 q + 3 of channel c --
@@ -296,53 +316,167 @@ __global__ __launch_bounds__(128) void sums_kernel(const double *__restrict__ su
 //    of them in one 32-deep product against the same X twice, so dphi has
 //    fp32's accuracy (the third's product has zeros in its other half: a
 //    16x16x16 product before a 16x16x32 one on the same sums gave results
-//    that changed from run to run).  Sums over a wave's rows stay in registers, are joined
-//    over the workgroup's row lanes through LDS and over the row ranges by
-//    dphi_sum_kernel, each in a fixed order.
+//    that changed from run to run).  Sums over a workgroup's rows stay in
+//    registers and are joined over the row ranges by dphi_sum_kernel, in
+//    their order.
 //
 // A NaN in X_t reaches dphi in the 32 channels around it (NaN times the
 // selection's zeros); a row with one has no finite r either.
+//
+// Memory: in that layout the lanes of a quad have four different rows, so
+// loads straight into it touch 64 separate 16-byte pieces each (measured 915
+// us at n=4, C=7168, B=16384 from the checkpoint).  Direct-to-LDS loads take
+// the data in memory order instead (lanes 4 r .. 4 r + 3: 64 bytes of row r),
+// one tile ahead, without registers; a row's four pieces are rotated by its
+// row / 4 (xor), so that the reads in the matrix layout meet no bank twice.
+// dX goes back through LDS the same way and is stored in memory order.  The
+// tile's record is staged the same way, shared by the workgroup's waves.
+//
+// Waits: a tile's loads are issued a whole tile before they are waited for,
+// and vmcnt counts in order; only the dX stores of the tile in between are
+// younger, so "at most that many outstanding" means the loads have landed.
+__device__ __attribute__((aligned(256))) uint32_t g_train_zero[64];  // what loads past the edges read
+
+template <int BYTES>
+__device__ __forceinline__ void dma(const void *src, uint32_t lds_addr) {  // lane l's data lands at lds_addr + BYTES l
+  lds_addr = (uint32_t)uniform((int)lds_addr);
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_addr) : "memory");
+  else if constexpr (BYTES == 4)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_addr) : "memory");
+  else  // one byte, zero-extended to the lane's four
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off" ::"v"(src), "s"(lds_addr) : "memory");
+}
+typedef __attribute__((address_space(3))) char lds_char;
+__device__ __forceinline__ uint32_t lds_addr_of(const char *p) { return (uint32_t)(uintptr_t)(lds_char *)p; }
+
+template <int NS, bool CK>
+struct Stage {
+  using T = Tiles<NS>;
+  // Bytes of a stage: G (a KiB a stream and step), X_t, dF_pre, scale bytes
+  // (a dword each).  With one stream a wave (n = 8) dX leaves through the
+  // wave's X slots, else through its G slots, which nobody else reads.
+  static constexpr int kWaves = 8, kAlong = kWaves / T::GROUPS;
+  static constexpr bool kShared = T::GROUPS > 1;
+  static constexpr int kG = kAlong * T::HW * NS * 1024;
+  static constexpr int kXWave = T::JW * T::HW * (CK && !kShared ? 512 : 1024);
+  static constexpr int kX = kWaves * kXWave;
+  static constexpr int kF = kAlong * T::HW * 1024;
+  static constexpr int kS = CK ? kWaves * 256 : 0;
+  static constexpr int kBytes = kG + kX + kF + kS;
+  // Codes of a wave: [JW][16 rows][32] bytes, or at n = 8 [16 rows][64] in the
+  // second KiB (dX of the first step goes to the first).
+  static constexpr int kCodes = kShared ? 1024 : 0;
+};
+
 template <int NS, bool CK>
 __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     const char *__restrict__ X, const uint8_t *__restrict__ scales, const uint16_t *__restrict__ phi,
-    const float *__restrict__ H, const u32x4 *__restrict__ G, const u32x4 *__restrict__ dF,
-    const u32x4 *__restrict__ rows_b, const u32x4 *__restrict__ cols_a, const u32x2 *__restrict__ cols_c,
-    const float *__restrict__ turn, u32x4 *__restrict__ dX, float *__restrict__ out, uint32_t B, uint32_t tiles_each,
-    uint32_t cvec, uint32_t blocks, uint32_t slices, int wc) {
+    const char *__restrict__ G, const char *__restrict__ dF, const char *__restrict__ records, char *__restrict__ dX,
+    float *__restrict__ out, uint32_t B, uint32_t tiles_each, uint32_t cvec, uint32_t blocks, uint32_t slices,
+    int wc) {
   using T = Tiles<NS>;
+  using S = Stage<NS, CK>;
   constexpr int N = T::N, KS = T::KS, MT = T::MT, JW = T::JW, GROUPS = T::GROUPS, HW = T::HW;
-  constexpr int kPhi = 8 / GROUPS * HW * NS * 2 * KS * 64;  // 16-byte operands, all waves along the channels
-  constexpr int kJoin = 4 * JW * 2 * MT * 64;               // a step's sums of half the waves
-  __shared__ u32x4 lds[kPhi > kJoin ? kPhi : kJoin];
+  __shared__ __attribute__((aligned(1024))) char stage[2][S::kBytes];
+  __shared__ __attribute__((aligned(1024))) char record[2][T::kStride];
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
-  // wc waves along the channels (a power of two), GROUPS along the streams,
-  // the rest along the rows.
-  const int cw = wave / GROUPS % wc, group = wave % GROUPS, rl = wave / (GROUPS * wc), row_lanes = 8 / (GROUPS * wc);
+  // wc waves along the channels, GROUPS along the streams.
+  const int cw = wave / GROUPS, group = wave % GROUPS, waves = wc * GROUPS;
   const uint32_t slice = blockIdx.x % slices, range = blockIdx.x / slices;
-  const uint32_t v_wg = slice * (uint32_t)wc * (HW * 4);  // the workgroup's first vector of eight channels
-  const uint32_t v_wave = v_wg + cw * (HW * 4);
+  const uint32_t v_wave = (slice * (uint32_t)wc + cw) * (HW * 4);  // the wave's first vector of eight channels
   const int lo16 = lane & 15, q = lane >> 4, j0 = group * JW;
+  const uint32_t tiles = (B + 15) / 16, first = range * tiles_each;
+  const uint32_t last = tiles - first < tiles_each ? tiles : first + tiles_each;
+  const size_t row_bytes = (size_t)cvec * 16;  // a stream of a row
 
-  // phi: operand (cw, stream, step h, t, ks), lane 16 q + m: coefficients
-  // 32 ks + 8 q .. + 7 of channel 32 (HW cw + h) + 8 (m / 4) + 4 t + m % 4.
-  for (int w = threadIdx.x; w < wc * (HW * NS * 2 * KS * 64); w += 512) {
-    const int l = w & 63, ks = (w >> 6) % KS, rest = (w >> 6) / KS;
-    const int t = rest & 1, h = (rest >> 1) % HW, j = rest / (2 * HW) % NS, s = rest / (2 * HW * NS);
-    const uint32_t v = v_wg + (s * HW + h) * 4 + ((l & 15) >> 2);
-    const int k0 = 32 * ks + 8 * (l >> 4);
-    u32x4 a = {0u, 0u, 0u, 0u};
-    if (v < cvec && k0 < N) {
-      const size_t at = ((size_t)j * cvec * 8 + (size_t)v * 8 + 4 * t + (l & 3)) * N + k0;
-      if constexpr (N % 8 == 0) {
-        a = load16(phi + at);
-      } else {
+  // The 16-byte piece a lane takes in memory order, and its place in the
+  // matrix layout.
+  const int mrow = lane >> 2, mq = (lane & 3) ^ ((lane >> 4) & 3);
+  const int slot16 = (lo16 * 4 + (q ^ ((lo16 >> 2) & 3))) * 16;
+
+  const auto issue = [&](uint32_t tile, int st) {
+    const char *zero = reinterpret_cast<const char *>(g_train_zero);
+    const uint32_t at = lds_addr_of(stage[st]), row0 = tile * 16;
+    const uint32_t g_at = at + (uint32_t)cw * (HW * NS * 1024), x_at = at + S::kG + (uint32_t)wave * S::kXWave;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k0 + k < N) a[k / 2] |= (uint32_t)phi[at + k] << (16 * (k & 1));
+    for (int h = 0; h < HW; ++h) {
+      const uint32_t row = row0 + mrow, v = v_wave + h * 4 + mq;
+      const bool in = row < B && v < cvec;
+      const size_t at_row = (size_t)row * NS * row_bytes + (size_t)v * 16;
+      if constexpr (!S::kShared) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          dma<16>(in ? G + at_row + (size_t)i * row_bytes : zero, g_at + (h * NS + i) * 1024);
+      } else {
+        dma<16>(in ? G + at_row + (size_t)group * row_bytes : zero, g_at + (h * NS + group) * 1024);
+      }
+      if (!S::kShared || group == h)
+        dma<16>(in ? dF + (size_t)row * row_bytes + (size_t)v * 16 : zero, at + S::kG + S::kX + (cw * HW + h) * 1024);
+      if constexpr (!CK) {
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj)
+          dma<16>(in ? X + at_row + (size_t)(j0 + jj) * row_bytes : zero, x_at + (h * JW + jj) * 1024);
       }
     }
-    lds[w] = a;
-  }
+    if constexpr (CK) {
+      // Rows of 32 HW codes, linear; 16 bytes a lane where a stream's codes
+      // are that aligned, else four.
+      constexpr int kRow = 32 * HW;
+      const size_t stream = (size_t)cvec * 8;
+      const auto code = [&](int byte, int width) -> const char * {  // of [JW][16][kRow]
+        const int jj = byte / (16 * kRow), r = byte / kRow % 16, c = byte % kRow;
+        const uint32_t row = row0 + r, ch = v_wave * 8 + c;
+        return jj < JW && row < B && ch < cvec * 8 ? X + ((size_t)row * NS + j0 + jj) * stream + ch : zero;
+      };
+      if (cvec % 2 == 0) {
+#pragma unroll
+        for (int k = 0; k < (JW * 16 * kRow + 1023) / 1024; ++k)
+          if (JW * 16 * kRow >= 1024 || lane < JW * 16 * kRow / 16)
+            dma<16>(code(k * 1024 + lane * 16, 16), x_at + S::kCodes + k * 1024);
+      } else {
+#pragma unroll
+        for (int k = 0; k < JW * 16 * kRow / 256; ++k)
+          dma<4>(code(k * 256 + lane * 4, 4), x_at + S::kCodes + k * 256);
+      }
+      // One scale byte for each row and stream (n = 8: row and step).
+      const uint32_t row = row0 + lo16, v = v_wave + (S::kShared ? q * 4 : 0);
+      const int j = S::kShared ? j0 : q;
+      const bool in = row < B && v < cvec && (S::kShared ? q < HW : q < JW);
+      dma<1>(in ? reinterpret_cast<const char *>(scales) + ((size_t)row * NS + j) * blocks + (v >> 2) : zero,
+             at + S::kG + S::kX + S::kF + (uint32_t)wave * 256);
+    }
+    for (int k = wave; k < T::kChunks; k += waves)
+      dma<16>(records + (size_t)tile * T::kStride + k * 1024 + lane * 16, lds_addr_of(record[st]) + k * 1024);
+  };
+  issue(first, 0);
+
+  // phi: operand (stream, step h, t, ks), lane 16 q + m: coefficients
+  // 32 ks + 8 q .. + 7 of channel 32 h + 8 (m / 4) + 4 t + m % 4 of the wave.
+  bf16x8 pa[JW][HW][2][KS];
+#pragma unroll
+  for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+    for (int h = 0; h < HW; ++h)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t v = v_wave + h * 4 + (lo16 >> 2);
+          const int k0 = 32 * ks + 8 * q;
+          u32x4 a = {0u, 0u, 0u, 0u};
+          if (v < cvec && k0 < N) {
+            const size_t at = ((size_t)(j0 + jj) * cvec * 8 + (size_t)v * 8 + 4 * t + (lo16 & 3)) * N + k0;
+            if constexpr (N % 8 == 0) {
+              a = load16(phi + at);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (k0 + k < N) a[k / 2] |= (uint32_t)phi[at + k] << (16 * (k & 1));
+            }
+          }
+          pa[jj][h][t][ks] = __builtin_bit_cast(bf16x8, a);
+        }
   // Selections: channels 16 s .. 16 s + 15 of the 32.
   s16x8 sel[2];
 #pragma unroll
@@ -358,76 +492,59 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) acc[jj][h][s][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  __syncthreads();
 
-  const uint32_t tiles = (B + 15) / 16, first = range * tiles_each;
-  const uint32_t last = tiles - first < tiles_each ? tiles : first + tiles_each;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  for (uint32_t tile = first + rl; tile < last; tile += row_lanes) {
-    const uint32_t row = tile * 16 + lo16;
-    const bool row_in = row < B;
-    bf16x8 bh[KS], bm[KS], ca[MT], cc[MT];
+  // Every step of the wave has channels: its stores are issued each tile.
+  const bool full = v_wave + (HW - 1) * 4 < cvec;
+  for (uint32_t tile = first; tile < last; ++tile) {
+    const int st = (int)(tile - first) & 1;
+    if (tile == first || !full)
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(JW * HW) : "memory");
+    // The other waves' share of the tile has landed, and everybody has read
+    // the last of the stage that the next loads fill.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (tile + 1 < last) issue(tile + 1, st ^ 1);
+    char *mine = stage[st];
+    const char *now = record[st];
+    bf16x8 bh[KS], bm[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      bh[ks] = __builtin_bit_cast(bf16x8, rows_b[((size_t)(tile * 2 + 0) * KS + ks) * 64 + lane]);
-      bm[ks] = __builtin_bit_cast(bf16x8, rows_b[((size_t)(tile * 2 + 1) * KS + ks) * 64 + lane]);
+      bh[ks] = reinterpret_cast<const bf16x8 *>(now)[ks * 64 + lane];
+      bm[ks] = reinterpret_cast<const bf16x8 *>(now)[(KS + ks) * 64 + lane];
     }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      ca[mt] = __builtin_bit_cast(bf16x8, cols_a[((size_t)tile * MT + mt) * 64 + lane]);
-      const u32x2 low = cols_c[((size_t)tile * MT + mt) * 64 + lane];
-      cc[mt] = __builtin_bit_cast(bf16x8, u32x4{low[0], low[1], 0u, 0u});
-    }
-    float hres[NS][JW], hpre[JW], c = 0.f;
-#pragma unroll
-    for (int jj = 0; jj < JW; ++jj) {
-      hpre[jj] = row_in ? H[(size_t)row * N + j0 + jj] : 0.f;
-#pragma unroll
-      for (int i = 0; i < NS; ++i) hres[i][jj] = row_in ? H[(size_t)row * N + 2 * NS + i * NS + j0 + jj] : 0.f;
-    }
-    if (row_in) c = turn[row];
+    const float *mix = reinterpret_cast<const float *>(now + T::kMix) + lo16;
+    const float c = reinterpret_cast<const float *>(now + T::kTurn)[lo16];
+    const bf16x8 *cols_a = reinterpret_cast<const bf16x8 *>(now + T::kColsA) + lane;
+    const u32x2 *cols_c = reinterpret_cast<const u32x2 *>(now + T::kColsC) + lane;
 #pragma unroll
     for (int h = 0; h < HW; ++h) {
-      const uint32_t v = v_wave + h * 4 + q;
-      const bool in = row_in && v < cvec;
-      const size_t at = (size_t)row * NS * cvec + v;
-      u32x4 g[NS], f = {0u, 0u, 0u, 0u};
+      char *g_at = mine + cw * (HW * NS * 1024) + h * NS * 1024;
+      char *x_at = mine + S::kG + wave * S::kXWave;
       u32x4 x[JW];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) g[i] = in ? G[at + (size_t)i * cvec] : u32x4{0u, 0u, 0u, 0u};
-      if (in) f = dF[(size_t)row * cvec + v];
-      if constexpr (CK) {
-        u32x2 code[JW];
-        int s[JW];
-#pragma unroll
-        for (int jj = 0; jj < JW; ++jj) {
-          code[jj] = u32x2{0u, 0u};
-          s[jj] = 1;
-          if (in) {
-            code[jj] = *reinterpret_cast<const u32x2 *>(X + (at + (size_t)(j0 + jj) * cvec) * 8);
-            s[jj] = scales[((size_t)row * NS + j0 + jj) * blocks + (v >> 2)];
-          }
+      for (int jj = 0; jj < JW; ++jj) {
+        if constexpr (CK) {
+          const u32x2 code = *reinterpret_cast<const u32x2 *>(x_at + S::kCodes + (jj * 16 + lo16) * (32 * HW) + h * 32 + q * 8);
+          const uint32_t s = reinterpret_cast<const uint32_t *>(mine + S::kG + S::kX + S::kF + wave * 256)[(S::kShared ? h : jj) * 16 + lo16];
+          x[jj] = held_bf16(code, (int)s);
+        } else {
+          x[jj] = *reinterpret_cast<const u32x4 *>(x_at + (h * JW + jj) * 1024 + slot16);
         }
-#pragma unroll
-        for (int jj = 0; jj < JW; ++jj) x[jj] = held_bf16(code[jj], s[jj]);
-      } else {
-#pragma unroll
-        for (int jj = 0; jj < JW; ++jj)
-          x[jj] = in ? load16(X + (at + (size_t)(j0 + jj) * cvec) * 16) : u32x4{0u, 0u, 0u, 0u};
       }
       float o[JW][8];
 #pragma unroll
       for (int jj = 0; jj < JW; ++jj) {
         f32x4 d[2] = {zero, zero};
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const bf16x8 a =
-                __builtin_bit_cast(bf16x8, lds[((((cw * NS + j0 + jj) * HW + h) * 2 + t) * KS + ks) * 64 + lane]);
-            d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bm[ks], d[t], 0, 0, 0);
-            d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bh[ks], d[t], 0, 0, 0);
-          }
+          for (int t = 0; t < 2; ++t) d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pa[jj][h][t][ks], bm[ks], d[t], 0, 0, 0);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pa[jj][h][t][ks], bh[ks], d[t], 0, 0, 0);
         float xw[8];
         widen8(x[jj], xw);
 #pragma unroll
@@ -435,30 +552,48 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
       }
       {
         float fw[8];
-        widen8(f, fw);
+        widen8(*reinterpret_cast<const u32x4 *>(mine + S::kG + S::kX + (cw * HW + h) * 1024 + slot16), fw);
 #pragma unroll
-        for (int jj = 0; jj < JW; ++jj)
+        for (int jj = 0; jj < JW; ++jj) {
+          const float hpre = mix[(j0 + jj) * 16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hpre[jj], fw[e], o[jj][e]);
+          for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hpre, fw[e], o[jj][e]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         float gw[8];
-        widen8(g[i], gw);
+        widen8(*reinterpret_cast<const u32x4 *>(g_at + i * 1024 + slot16), gw);
 #pragma unroll
-        for (int jj = 0; jj < JW; ++jj)
+        for (int jj = 0; jj < JW; ++jj) {
+          const float hres = mix[(NS + i * NS + j0 + jj) * 16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hres[i][jj], gw[e], o[jj][e]);
+          for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hres, gw[e], o[jj][e]);
+        }
       }
-      if (in) {
+      // Out in memory order: over the wave's own G (or X) pieces of this step.
+      char *o_at = S::kShared ? x_at + h * 1024 : g_at;
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int jj = 0; jj < JW; ++jj)
-          dX[at + (size_t)(j0 + jj) * cvec] =
-              u32x4{pack_bf16x2(o[jj][0], o[jj][1]), pack_bf16x2(o[jj][2], o[jj][3]),
-                    pack_bf16x2(o[jj][4], o[jj][5]), pack_bf16x2(o[jj][6], o[jj][7])};
+      for (int jj = 0; jj < JW; ++jj)
+        *reinterpret_cast<u32x4 *>(o_at + jj * 1024 + slot16) =
+            u32x4{pack_bf16x2(o[jj][0], o[jj][1]), pack_bf16x2(o[jj][2], o[jj][3]), pack_bf16x2(o[jj][4], o[jj][5]),
+                  pack_bf16x2(o[jj][6], o[jj][7])};
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
+      {
+        const uint32_t row = tile * 16 + mrow, v = v_wave + h * 4 + mq;
+        char *dst = dX + ((size_t)row * NS + j0) * row_bytes + (size_t)v * 16;
+        u32x4 y[JW];
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj) y[jj] = *reinterpret_cast<const u32x4 *>(o_at + jj * 1024 + lane * 16);
+        if (row < B && v < cvec) {
+#pragma unroll
+          for (int jj = 0; jj < JW; ++jj) *reinterpret_cast<u32x4 *>(dst + (size_t)jj * row_bytes) = y[jj];
+        }
       }
 #pragma unroll
-      for (int jj = 0; jj < JW; ++jj) {
+      for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const f32x4 m = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -467,43 +602,20 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
           const bf16x8 twice = __builtin_bit_cast(bf16x8, u32x4{p0, p1, p0, p1});
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cc[mt], twice, acc[jj][h][s][mt], 0, 0, 0);
-            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ca[mt], twice, acc[jj][h][s][mt], 0, 0, 0);
+            const u32x2 low = cols_c[mt * 64];
+            const bf16x8 cc = __builtin_bit_cast(bf16x8, u32x4{low[0], low[1], 0u, 0u});
+            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cc, twice, acc[jj][h][s][mt], 0, 0, 0);
+            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cols_a[mt * 64], twice, acc[jj][h][s][mt], 0, 0, 0);
           }
         }
-      }
     }
   }
 
   // Lane 16 q + c of acc[jj][h][s][mt]: coefficients 16 mt + 4 q .. + 3 of
-  // the wave's channel 32 h + 16 s + c.  Row lanes past the first hand theirs
-  // over through LDS, one after the other.
+  // the wave's channel 32 h + 16 s + c.
   float *po = out + (size_t)range * NS * cvec * 8 * N;
 #pragma unroll
-  for (int h = 0; h < HW; ++h) {
-    for (int r = 1; r < row_lanes; ++r) {
-      __syncthreads();
-#pragma unroll
-      for (int jj = 0; jj < JW; ++jj)
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            u32x4 *slot = lds + ((((cw * GROUPS + group) * JW + jj) * 2 + s) * MT + mt) * 64 + lane;
-            if (rl == r) *slot = __builtin_bit_cast(u32x4, acc[jj][h][s][mt]);
-          }
-      __syncthreads();
-#pragma unroll
-      for (int jj = 0; jj < JW; ++jj)
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const u32x4 *slot = lds + ((((cw * GROUPS + group) * JW + jj) * 2 + s) * MT + mt) * 64 + lane;
-            if (rl == 0) acc[jj][h][s][mt] += __builtin_bit_cast(f32x4, *slot);
-          }
-    }
-    if (rl > 0) continue;
+  for (int h = 0; h < HW; ++h)
 #pragma unroll
     for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
@@ -524,7 +636,6 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
             }
           }
         }
-  }
 }
 
 // dphi: the partial sums in the order of their row ranges.
@@ -549,9 +660,8 @@ uint32_t wgs(uint64_t work, uint64_t per, uint64_t most) {
 template <int NS, bool CK>
 hipError_t launch_t(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBwdArgs &a, char *ws, hipStream_t st) {
   using T = Tiles<NS>;
-  u32x4 *rows_b = reinterpret_cast<u32x4 *>(ws + p.rows_b), *cols_a = reinterpret_cast<u32x4 *>(ws + p.cols_a);
-  u32x2 *cols_c = reinterpret_cast<u32x2 *>(ws + p.cols_c);
-  float *turn = reinterpret_cast<float *>(ws + p.turn), *dpre = reinterpret_cast<float *>(ws + p.dpre);
+  char *records = ws + p.records;
+  float *dpre = reinterpret_cast<float *>(ws + p.dpre);
   double *sums = reinterpret_cast<double *>(ws + p.sums);
   float *part = p.split > 1 ? reinterpret_cast<float *>(ws + p.dphi) : a.dphi;
   const uint32_t cvec = (uint32_t)(C / 8), blocks = (uint32_t)ckpt_blocks(C), rows = (uint32_t)B;
@@ -560,15 +670,14 @@ hipError_t launch_t(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBw
   pre_dots_kernel<NS, CK, 4><<<wgs(B, 1, 1u << 22), 256, 0, st>>>(a.X.x, a.X.scales, dF, dpre, rows, cvec, blocks);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   coeffs_bwd_kernel<NS><<<(uint32_t)p.sum_blocks, sum_threads<NS>(), 0, st>>>(
-      a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre, a.b_post, a.b_res, a.dH, dpre, rows_b, cols_a, cols_c,
-      turn, sums, rows, 1.0 / ((double)NS * (double)C));
+      a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre, a.b_post, a.b_res, a.dH, dpre, a.H, records, sums,
+      rows, 1.0 / ((double)NS * (double)C));
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  sums_kernel<<<1, 128, 0, st>>>(sums, (int)p.sum_blocks, NS, a.dalpha, a.db_pre, a.db_post, a.db_res);
+  sums_kernel<<<T::N + 3, 64, 0, st>>>(sums, (int)p.sum_blocks, NS, a.dalpha, a.db_pre, a.db_post, a.db_res);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  dx_dphi_kernel<NS, CK><<<(uint32_t)(p.slices * p.split), 512, 0, st>>>(
-      static_cast<const char *>(a.X.x), a.X.scales, static_cast<const uint16_t *>(a.phi), a.H,
-      static_cast<const u32x4 *>(a.dX_next), dF, rows_b, cols_a, cols_c, turn, static_cast<u32x4 *>(a.dX), part, rows,
-      (uint32_t)p.tiles_each, cvec, blocks, (uint32_t)p.slices, p.wc);
+  dx_dphi_kernel<NS, CK><<<(uint32_t)(p.slices * p.split), 64 * T::GROUPS * p.wc, 0, st>>>(
+      static_cast<const char *>(a.X.x), a.X.scales, static_cast<const uint16_t *>(a.phi),
+      static_cast<const char *>(a.dX_next), static_cast<const char *>(a.dF_pre), records, static_cast<char *>(a.dX), part, rows, (uint32_t)p.tiles_each, cvec, blocks, (uint32_t)p.slices, p.wc);
   if ((e = hipGetLastError()) != hipSuccess || p.split == 1) return e;
   const uint64_t count = (uint64_t)NS * C * T::N;
   dphi_sum_kernel<<<wgs(count, 256, 1u << 22), 256, 0, st>>>(part, a.dphi, count, (uint32_t)p.split);
@@ -582,7 +691,7 @@ hipError_t launch_n(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBw
 
 size_t up16(size_t v) { return (v + 15) / 16 * 16; }
 
-constexpr int64_t kRound = 256;
+constexpr int64_t kRound = 256, kMinTiles = 4;
 
 template <int NS>
 CoeffsBwdPlan plan_n(int64_t B, int64_t C) {
@@ -592,21 +701,18 @@ CoeffsBwdPlan plan_n(int64_t B, int64_t C) {
   p.wc = 1;  // waves along the channels, as many as there are channels for
   while (p.wc < 8 / T::GROUPS && p.wc * T::CW < C) p.wc *= 2;
   p.slices = (C + p.wc * T::CW - 1) / (p.wc * T::CW);
-  const int64_t row_lanes = 8 / (T::GROUPS * p.wc);
-  // One workgroup fits a compute unit: as many row ranges as make one round
-  // of them, and no range without a tile for each of its row lanes.
-  int64_t split = kRound / p.slices;
-  if (split > (tiles + row_lanes - 1) / row_lanes) split = (tiles + row_lanes - 1) / row_lanes;
+  // As many row ranges as fill the compute units once (a full workgroup has
+  // one to itself), but at least kMinTiles tiles in each: a range costs a copy
+  // of dphi.
+  int64_t split = kRound * (8 / (T::GROUPS * p.wc)) / p.slices;
+  if (split > tiles / kMinTiles) split = tiles / kMinTiles;
   if (split < 1) split = 1;
   p.tiles_each = (tiles + split - 1) / split;
   p.split = (tiles + p.tiles_each - 1) / p.tiles_each;
   const int64_t per = sum_threads<NS>() / (NS * NS), groups = (B + per - 1) / per;
   p.sum_blocks = groups < kMaxSumBlocks ? groups : kMaxSumBlocks;
-  p.rows_b = 0;
-  p.cols_a = p.rows_b + (size_t)tiles * T::kRowsB;
-  p.cols_c = p.cols_a + (size_t)tiles * T::kColsA;
-  p.turn = p.cols_c + (size_t)tiles * T::kColsC;
-  p.dpre = up16(p.turn + (size_t)B * 4);
+  p.records = 0;
+  p.dpre = p.records + (size_t)tiles * T::kStride;
   p.sums = up16(p.dpre + (size_t)B * NS * 4);
   p.dphi = up16(p.sums + (size_t)p.sum_blocks * (T::N + 3) * 8);
   p.total_bytes = up16(p.dphi + (p.split > 1 ? (size_t)p.split * K * T::N * 4 : 0));

@@ -29,9 +29,9 @@ hipError_t launch_post_res_bwd(int n, int64_t B, int64_t C, HeldX X, const void 
                                const void *dX_next, void *dF_out, float *dH, hipStream_t st);
 
 // Workspace of the coefficient and pre-mix gradient (bytes from its start):
-//   rows_b, cols_a, cols_c   dlogit in bf16 parts, in matrix operand order, by
-//                            tiles of 16 rows (mhc_coeffs_pre_bwd.hip)
-//   turn   fp32 [B]          the factor of X_t that r contributes
+//   records                  a record for each tile of 16 rows: dlogit in bf16
+//                            parts and what else its dX needs of H and r
+//                            (mhc_coeffs_pre_bwd.hip)
 //   dpre   fp32 [B, n]       gradient of H_pre
 //   sums   fp64 [sum_blocks, N + 3]  partial sums of the bias and alpha gradients
 //   dphi   fp32 [split, K, N]        partial sums of dphi (split > 1)
@@ -41,7 +41,7 @@ struct CoeffsBwdPlan {
   int64_t split;       // row ranges
   int64_t tiles_each;  // tiles of 16 rows in each
   int64_t sum_blocks;  // workgroups of the coefficient kernel
-  size_t rows_b, cols_a, cols_c, turn, dpre, sums, dphi, total_bytes;
+  size_t records, dpre, sums, dphi, total_bytes;
 };
 CoeffsBwdPlan plan_coeffs_pre_bwd(int64_t B, int n, int64_t C);
 
