@@ -515,12 +515,33 @@ def mhc_lazy_prenorm_gemm(M, N, K, A, W, C, rstd=None, eps=1e-5, stream=None, ch
 # the embeddings.  These calls launch on the current device, so they take
 # tensors of that device only.
 
-def _here(*tensors):
-    """ValueError where a device tensor is not on the current device (the
-    kernels would run on another device than the tensor's)."""
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _device():
+    """The current device's index, -1 where no device is in use yet."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+def _dev_ptrs(dev, *tensors):
+    """_ptr of every (tensor, bytes, element size, name), and ValueError where
+    a device tensor is not on device `dev`, the current one (the kernels would
+    run on another device than the tensor's)."""
+    out = []
+    for t, nbytes, esize, name in tensors:
+        # What nearly every tensor is, decided in a few attribute reads.
+        if (type(t) is torch.Tensor and t.is_cuda and t.get_device() == dev and t.is_contiguous()
+                and t.itemsize == esize and t.nbytes >= nbytes):
+            out.append(t.data_ptr() or None)
+            continue
+        p = _ptr(t, nbytes, esize, name)
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+        out.append(p)
+    return out
+
+
+def _dev_stream(stream, dev):
+    if stream is None and dev >= 0:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def mhc_ckpt_scales_per_row(n, C):
@@ -528,17 +549,17 @@ def mhc_ckpt_scales_per_row(n, C):
     return int(load().mhc_ckpt_scales_per_row(int(n), int(C)))
 
 
-def _ckpt_ptrs(B, n, C, codes, scales):
-    B, n, C = max(int(B), 0), int(n), int(C)
-    return (_ptr(codes, B * n * C, 1, "codes"), _ptr(scales, B * mhc_ckpt_scales_per_row(n, C), 1, "scales"))
+def _held(B, n, C, codes, scales):
+    rows = max(B, 0)
+    return ((codes, rows * n * C, 1, "codes"), (scales, rows * n * -(-C // 32), 1, "scales"))
 
 
 def mhc_ckpt_pack(B, n, C, X_t, codes, scales, stream=None, check=True):
     """The 8-bit checkpoint of X_t: codes (E4M3 or uint8 [B, n*C]) and scales
     (uint8 [B, mhc_ckpt_scales_per_row(n, C)]); see include/mhc.h."""
-    _here(X_t, codes, scales)
-    st = load().mhc_ckpt_pack(int(B), int(n), int(C), _ptr(X_t, _Sizes(B, n, C).x, 2, "X_t"),
-                              *_ckpt_ptrs(B, n, C, codes, scales), _stream(stream))
+    B, n, C, dev = int(B), int(n), int(C), _device()
+    st = load().mhc_ckpt_pack(B, n, C, *_dev_ptrs(dev, (X_t, max(B, 0) * n * C * 2, 2, "X_t"),
+                                                  *_held(B, n, C, codes, scales)), _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_ckpt_pack")
     return st
@@ -546,20 +567,19 @@ def mhc_ckpt_pack(B, n, C, X_t, codes, scales, stream=None, check=True):
 
 def mhc_ckpt_unpack(B, n, C, codes, scales, X_t, stream=None, check=True):
     """X_t in bf16 from its checkpoint (see include/mhc.h)."""
-    _here(X_t, codes, scales)
-    st = load().mhc_ckpt_unpack(int(B), int(n), int(C), *_ckpt_ptrs(B, n, C, codes, scales),
-                                _ptr(X_t, _Sizes(B, n, C).x, 2, "X_t"), _stream(stream))
+    B, n, C, dev = int(B), int(n), int(C), _device()
+    st = load().mhc_ckpt_unpack(B, n, C, *_dev_ptrs(dev, *_held(B, n, C, codes, scales),
+                                                    (X_t, max(B, 0) * n * C * 2, 2, "X_t")), _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_ckpt_unpack")
     return st
 
 
 def _post_res_bwd(fn, name, held, B, n, C, F_out, H, dX_next, dF_out, dH, stream, check):
-    z = _Sizes(B, n, C)
-    _here(F_out, H, dX_next, dF_out, dH)
-    st = fn(int(B), int(n), int(C), *held, _ptr(F_out, z.f, 2, "F_out"), _ptr(H, z.coef, 4, "H"),
-            _ptr(dX_next, z.x, 2, "dX_next"), _ptr(dF_out, z.f, 2, "dF_out"), _ptr(dH, z.coef, 4, "dH"),
-            _stream(stream))
+    dev, rows, coef = _device(), max(B, 0), max(B, 0) * (n * n + 2 * n) * 4
+    st = fn(B, n, C, *_dev_ptrs(dev, *held, (F_out, rows * C * 2, 2, "F_out"), (H, coef, 4, "H"),
+                                (dX_next, rows * n * C * 2, 2, "dX_next"), (dF_out, rows * C * 2, 2, "dF_out"),
+                                (dH, coef, 4, "dH")), _dev_stream(stream, dev))
     if check:
         _check(st, name)
     return st
@@ -567,16 +587,16 @@ def _post_res_bwd(fn, name, held, B, n, C, F_out, H, dX_next, dF_out, dH, stream
 
 def mhc_post_res_bwd(B, n, C, X_t, F_out, H, dX_next, dF_out, dH, stream=None, check=True):
     """Gradients of step (4b) with respect to F_out and H (see include/mhc.h)."""
-    _here(X_t)
-    return _post_res_bwd(load().mhc_post_res_bwd, "mhc_post_res_bwd", (_ptr(X_t, _Sizes(B, n, C).x, 2, "X_t"),),
-                         B, n, C, F_out, H, dX_next, dF_out, dH, stream, check)
+    B, n, C = int(B), int(n), int(C)
+    return _post_res_bwd(load().mhc_post_res_bwd, "mhc_post_res_bwd", ((X_t, max(B, 0) * n * C * 2, 2, "X_t"),), B, n,
+                         C, F_out, H, dX_next, dF_out, dH, stream, check)
 
 
 def mhc_post_res_bwd_ckpt(B, n, C, codes, scales, F_out, H, dX_next, dF_out, dH, stream=None, check=True):
     """mhc_post_res_bwd with X_t as its checkpoint (see include/mhc.h)."""
-    _here(codes, scales)
-    return _post_res_bwd(load().mhc_post_res_bwd_ckpt, "mhc_post_res_bwd_ckpt", _ckpt_ptrs(B, n, C, codes, scales),
-                         B, n, C, F_out, H, dX_next, dF_out, dH, stream, check)
+    B, n, C = int(B), int(n), int(C)
+    return _post_res_bwd(load().mhc_post_res_bwd_ckpt, "mhc_post_res_bwd_ckpt", _held(B, n, C, codes, scales), B, n, C,
+                         F_out, H, dX_next, dF_out, dH, stream, check)
 
 
 def mhc_coeffs_pre_bwd_workspace_size(B, n, C):
@@ -586,17 +606,19 @@ def mhc_coeffs_pre_bwd_workspace_size(B, n, C):
 def _coeffs_pre_bwd(fn, name, held, B, n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res, logits, r,
                     H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace, workspace_bytes,
                     stream, check):
-    z, n = _Sizes(B, n, C), int(n)
-    _here(phi, b_pre, b_post, b_res, logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res,
-          workspace)
+    dev, rows, N = _device(), max(B, 0), n * n + 2 * n
     wb = _ws_bytes(workspace, workspace_bytes)
-    pp, bp, bq, br, lg, rr, hh = _coeff_args(z, phi, b_pre, b_post, b_res, logits, r, H)
-    # The parameters' gradients are written at B == 0 too.
-    st = fn(int(B), n, int(C), *held, pp, float(alpha_pre), float(alpha_post), float(alpha_res), bp, bq, br, lg, rr,
-            hh, _ptr(dX_next, z.x, 2, "dX_next"), _ptr(dH, z.coef, 4, "dH"), _ptr(dF_pre, z.f, 2, "dF_pre"),
-            _ptr(dX_t, z.x, 2, "dX_t"), _ptr(dphi, n * int(C) * (n * n + 2 * n) * 4, 4, "dphi"),
-            _ptr(dalpha, 12, 4, "dalpha"), _ptr(db_pre, n * 4, 4, "db_pre"), _ptr(db_post, n * 4, 4, "db_post"),
-            _ptr(db_res, n * n * 4, 4, "db_res"), _ptr(workspace, wb, None, "workspace"), wb, _stream(stream))
+    some = B > 0  # at B == 0 only the parameters' gradients are touched
+    p = _dev_ptrs(dev, *held, (phi, n * C * N * 2 if some else 0, 2, "phi"), (b_pre, n * 4 if some else 0, 4, "b_pre"),
+                  (b_post, n * 4 if some else 0, 4, "b_post"), (b_res, n * n * 4 if some else 0, 4, "b_res"),
+                  (logits, rows * N * 4, 4, "logits"), (r, rows * 4, 4, "r"), (H, rows * N * 4, 4, "H"),
+                  (dX_next, rows * n * C * 2, 2, "dX_next"), (dH, rows * N * 4, 4, "dH"),
+                  (dF_pre, rows * C * 2, 2, "dF_pre"), (dX_t, rows * n * C * 2, 2, "dX_t"),
+                  (dphi, n * C * N * 4, 4, "dphi"), (dalpha, 12, 4, "dalpha"), (db_pre, n * 4, 4, "db_pre"),
+                  (db_post, n * 4, 4, "db_post"), (db_res, n * n * 4, 4, "db_res"), (workspace, wb, None, "workspace"))
+    k = len(held) + 1  # the alphas follow phi
+    st = fn(B, n, C, *p[:k], float(alpha_pre), float(alpha_post), float(alpha_res), *p[k:], wb,
+            _dev_stream(stream, dev))
     if check:
         _check(st, name)
     return st
@@ -606,31 +628,32 @@ def mhc_coeffs_pre_bwd(B, n, C, X_t, phi, alpha_pre, alpha_post, alpha_res, b_pr
                        dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace,
                        workspace_bytes=None, stream=None, check=True):
     """Gradients of steps (1)-(4a) and of X_t through the apply (see include/mhc.h)."""
-    _here(X_t)
-    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd, "mhc_coeffs_pre_bwd",
-                           (_ptr(X_t, _Sizes(B, n, C).x, 2, "X_t"),), B, n, C, phi, alpha_pre, alpha_post, alpha_res,
-                           b_pre, b_post, b_res, logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre,
-                           db_post, db_res, workspace, workspace_bytes, stream, check)
+    B, n, C = int(B), int(n), int(C)
+    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd, "mhc_coeffs_pre_bwd", ((X_t, max(B, 0) * n * C * 2, 2, "X_t"),),
+                           B, n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res, logits, r, H, dX_next,
+                           dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace, workspace_bytes, stream,
+                           check)
 
 
 def mhc_coeffs_pre_bwd_ckpt(B, n, C, codes, scales, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res,
                             logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res,
                             workspace, workspace_bytes=None, stream=None, check=True):
     """mhc_coeffs_pre_bwd with X_t as its checkpoint (see include/mhc.h)."""
-    _here(codes, scales)
-    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd_ckpt, "mhc_coeffs_pre_bwd_ckpt",
-                           _ckpt_ptrs(B, n, C, codes, scales), B, n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre,
-                           b_post, b_res, logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post,
-                           db_res, workspace, workspace_bytes, stream, check)
+    B, n, C = int(B), int(n), int(C)
+    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd_ckpt, "mhc_coeffs_pre_bwd_ckpt", _held(B, n, C, codes, scales), B,
+                           n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res, logits, r, H, dX_next,
+                           dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace, workspace_bytes, stream,
+                           check)
 
 
 def mhc_embed(B, n, C, V, tokens, table, scale, X_0, stream=None, check=True):
     """X_0: the scaled embeddings of the tokens (int64) in every stream (see include/mhc.h)."""
-    B, n, C, V = int(B), int(n), int(C), int(V)
-    _here(tokens, table, X_0)
-    st = load().mhc_embed(B, n, C, V, _ptr(tokens, max(B, 0) * 8, 8, "tokens"),
-                          _ptr(table, max(V, 0) * C * 2 if B > 0 else 0, 2, "table"), float(scale),
-                          _ptr(X_0, _Sizes(B, n, C).x, 2, "X_0"), _stream(stream))
+    B, n, C, V, dev = int(B), int(n), int(C), int(V), _device()
+    rows = max(B, 0)
+    tokens, table, X_0 = _dev_ptrs(dev, (tokens, rows * 8, 8, "tokens"),
+                                   (table, max(V, 0) * C * 2 if B > 0 else 0, 2, "table"),
+                                   (X_0, rows * n * C * 2, 2, "X_0"))
+    st = load().mhc_embed(B, n, C, V, tokens, table, float(scale), X_0, _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_embed")
     return st
@@ -644,13 +667,14 @@ def mhc_embed_bwd(B, n, C, V, tokens, dX_0, scale, dtable, workspace, accumulate
                   stream=None, check=True):
     """The embedding table's gradient (fp32 [V, C]), overwritten or, with
     accumulate, added to (see include/mhc.h)."""
-    B, n, C, V = int(B), int(n), int(C), int(V)
-    _here(tokens, dX_0, dtable, workspace)
-    wb = _ws_bytes(workspace, workspace_bytes)
-    st = load().mhc_embed_bwd(B, n, C, V, _ptr(tokens, max(B, 0) * 8, 8, "tokens"),
-                              _ptr(dX_0, _Sizes(B, n, C).x, 2, "dX_0"), float(scale), int(bool(accumulate)),
-                              _ptr(dtable, max(V, 0) * C * 4, 4, "dtable"),
-                              _ptr(workspace, wb, None, "workspace"), wb, _stream(stream))
+    B, n, C, V, dev = int(B), int(n), int(C), int(V), _device()
+    rows, wb = max(B, 0), _ws_bytes(workspace, workspace_bytes)
+    tokens, dX_0, dtable, workspace = _dev_ptrs(dev, (tokens, rows * 8, 8, "tokens"),
+                                                (dX_0, rows * n * C * 2, 2, "dX_0"),
+                                                (dtable, max(V, 0) * C * 4, 4, "dtable"),
+                                                (workspace, wb, None, "workspace"))
+    st = load().mhc_embed_bwd(B, n, C, V, tokens, dX_0, float(scale), int(bool(accumulate)), dtable, workspace, wb,
+                              _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_embed_bwd")
     return st

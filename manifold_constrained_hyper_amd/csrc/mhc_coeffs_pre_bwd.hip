@@ -25,7 +25,7 @@ namespace mhc {
 
 namespace {
 
-constexpr int64_t kMaxSumBlocks = 512;
+constexpr int64_t kMaxSumBlocks = 1024;
 
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -54,15 +54,20 @@ struct Tiles {
   static constexpr int kChunks = (kBytes + 1023) / 1024, kStride = kChunks * 1024;
 };
 
-// dH_pre [B, n]: a workgroup a row.
+// dH_pre [B, n]: a workgroup a row.  The rows of the row ranges' beginnings
+// come last, so that what the big cache still holds of X_t and dF_pre is what
+// dx_dphi_kernel reads first.
 template <int NS, bool CK, int W>
 __global__ __launch_bounds__(64 * W) void pre_dots_kernel(const void *__restrict__ X,
                                                           const uint8_t *__restrict__ scales,
                                                           const u32x4 *__restrict__ dF, float *__restrict__ dpre,
-                                                          uint32_t B, uint32_t cvec, uint32_t blocks) {
+                                                          uint32_t B, uint32_t cvec, uint32_t blocks, uint32_t split,
+                                                          uint32_t rows_each) {
   __shared__ float part[W][NS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (uint32_t row = blockIdx.x; row < B; row += gridDim.x) {
+  for (uint64_t p = blockIdx.x; p < (uint64_t)split * rows_each; p += gridDim.x) {
+    const uint64_t row = p % split * rows_each + (rows_each - 1 - p / split);
+    if (row >= B) continue;
     float acc[NS];
 #pragma unroll
     for (int j = 0; j < NS; ++j) acc[j] = 0.f;
@@ -102,19 +107,42 @@ __global__ __launch_bounds__(64 * W) void pre_dots_kernel(const void *__restrict
 
 // Sum over the n lanes that hold a row (AXIS 2: lanes differ in j) or a
 // column (AXIS 1: lanes differ in i) of an n x n matrix, one element a lane
-// at lane i*n + j of an aligned group of n*n lanes.
+// at lane i*n + j of an aligned group of n*n lanes; every lane of the row or
+// column gets the same bits (each step adds two values that its partner adds
+// too).  Lane moves inside rows of 16 lanes are DPP; n = 8 needs two wider
+// ones.
+__device__ __forceinline__ float dpp_add_ror8(float x) {  // lane ^ 8 in its row of 16
+  return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float dpp_add_ror4(float x) {  // lane ^ 4, once lanes 8 apart are equal
+  return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x124, 0xF, 0xF, false));
+}
 template <int NS, int AXIS>
 __device__ __forceinline__ float axis_sum(float x) {
-#pragma unroll
-  for (int d = 1; d < NS; d <<= 1) x += __shfl_xor(x, AXIS == 2 ? d : d * NS);
+  if constexpr (AXIS == 2) return group_sum<NS>(x);
+  if constexpr (NS == 2) return dpp_add_xor2(x);
+  if constexpr (NS == 4) return dpp_add_ror4(dpp_add_ror8(x));
+  if constexpr (NS == 8) {
+    x = dpp_add_ror8(x);
+    x += __shfl_xor(x, 16);
+    x += __shfl_xor(x, 32);
+  }
   return x;
+}
+// 1 / x to about an ulp: the hardware's reciprocal and a Newton step.
+__device__ __forceinline__ float recip(float x) {
+  const float r = __builtin_amdgcn_rcpf(x);
+  return fmaf(r, fmaf(-x, r, 1.0f), r);
 }
 
 // The coefficients' gradient of each row: n*n lanes a row, one element of the
-// n x n matrix each.  Every division is an IEEE one and the exponentials are
-// the accurate ones: a 1 x 1 matrix normalises to exactly 1 and its gradient
-// to exactly 0, as in the definition.  The partial sums of db and dalpha are
-// kept in fp64 (few adds, and gates' gradients cancel over a batch).
+// n x n matrix each, with the accurate exponentials.  A 1 x 1 matrix is 1
+// whatever its logit and has no gradient.  The first division is an IEEE one
+// (its totals are sums of exponentials of any size); the later ones, whose
+// totals are near 1, multiply by a reciprocal.  The 80 sums and divisions of a
+// row depend on each other, so the kernel is bound by their latency.  The
+// partial sums of db and dalpha are kept in fp64 (few adds, and gates'
+// gradients cancel over a batch).
 //
 // dlogit leaves in the tiles' records, in the matrix core's operand order,
 // split into bf16 parts whose sum is dlogit to 2^-17 (hi + mid: for dX, which
@@ -172,22 +200,26 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
     }
 
     const float lr = lg[2 * NS + e];
-    const float m0 = expf(alpha_res * lr / r + b_res[e]);
-    float y[2 * IT], total[2 * IT], m = m0;
+    float dz = 0.f;
+    if constexpr (NS > 1) {
+      const float m0 = expf(alpha_res * lr / r + b_res[e]);
+      float y[2 * IT], inv[2 * IT];
+      const float total = axis_sum<NS, 2>(m0);
+      float m = y[0] = m0 / total;
 #pragma unroll
-    for (int it = 0; it < IT; ++it) {
-      total[2 * it] = axis_sum<NS, 2>(m);
-      y[2 * it] = m = m / total[2 * it];
-      total[2 * it + 1] = axis_sum<NS, 1>(m);
-      y[2 * it + 1] = m = m / total[2 * it + 1];
-    }
-    float d = up[2 * NS + e];
+      for (int k = 1; k < 2 * IT; ++k) {
+        inv[k] = recip(k % 2 ? axis_sum<NS, 1>(m) : axis_sum<NS, 2>(m));
+        y[k] = m = m * inv[k];
+      }
+      float d = up[2 * NS + e];
 #pragma unroll
-    for (int it = IT - 1; it >= 0; --it) {
-      d = (d - axis_sum<NS, 1>(d * y[2 * it + 1])) / total[2 * it + 1];
-      d = (d - axis_sum<NS, 2>(d * y[2 * it])) / total[2 * it];
+      for (int k = 2 * IT - 1; k > 0; --k) {
+        const float dy = d * y[k];
+        d = (d - (k % 2 ? axis_sum<NS, 1>(dy) : axis_sum<NS, 2>(dy))) * inv[k];
+      }
+      // dz = m0 (d - sum) / total, with m0 / total = y[0]
+      dz = y[0] * (d - axis_sum<NS, 2>(d * y[0]));
     }
-    const float dz = d * m0;
     const float dlr = alpha_res * dz / r;
     scaled = fmaf(dlr, lr, scaled);
 #pragma unroll
@@ -282,20 +314,6 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
   }
 }
 
-// The workgroups' partial sums of db and dalpha: a workgroup for each sum, a
-// thread every 64th partial sum, then the threads as a tree.
-__global__ __launch_bounds__(64) void sums_kernel(const double *__restrict__ sums, int blocks, int n,
-                                                  float *__restrict__ dalpha, float *__restrict__ db_pre,
-                                                  float *__restrict__ db_post, float *__restrict__ db_res) {
-  const int N = n * n + 2 * n, k = blockIdx.x;
-  double a = 0.0;
-  for (int b = threadIdx.x; b < blocks; b += 64) a += sums[(size_t)b * (N + 3) + k];
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) a += __shfl_xor(a, o);
-  float *out = k < n ? db_pre + k : k < 2 * n ? db_post + (k - n) : k < N ? db_res + (k - 2 * n) : dalpha + (k - N);
-  if (threadIdx.x == 0) *out = (float)a;
-}
-
 // dX and the partial dphi, in one pass over G, X_t and dF_pre.
 //
 // A wave takes 16 rows and 32 channels at a time: lane 16 q + i has channels
@@ -317,8 +335,8 @@ __global__ __launch_bounds__(64) void sums_kernel(const double *__restrict__ sum
 //    fp32's accuracy (the third's product has zeros in its other half: a
 //    16x16x16 product before a 16x16x32 one on the same sums gave results
 //    that changed from run to run).  Sums over a workgroup's rows stay in
-//    registers and are joined over the row ranges by dphi_sum_kernel, in
-//    their order.
+//    registers and are joined over the row ranges by join_kernel, in their
+//    order.
 //
 // A NaN in X_t reaches dphi in the 32 channels around it (NaN times the
 // selection's zeros); a row with one has no finite r either.
@@ -518,6 +536,7 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     const float c = reinterpret_cast<const float *>(now + T::kTurn)[lo16];
     const bf16x8 *cols_a = reinterpret_cast<const bf16x8 *>(now + T::kColsA) + lane;
     const u32x2 *cols_c = reinterpret_cast<const u32x2 *>(now + T::kColsC) + lane;
+    bf16x8 twice[JW][HW][2];
 #pragma unroll
     for (int h = 0; h < HW; ++h) {
       char *g_at = mine + cw * (HW * NS * 1024) + h * NS * 1024;
@@ -599,15 +618,27 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
           const f32x4 m = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8, x[jj]), __builtin_bit_cast(bf16x8, sel[s]), zero, 0, 0, 0);
           const uint32_t p0 = pack_bf16x2(m[0], m[1]), p1 = pack_bf16x2(m[2], m[3]);
-          const bf16x8 twice = __builtin_bit_cast(bf16x8, u32x4{p0, p1, p0, p1});
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const u32x2 low = cols_c[mt * 64];
-            const bf16x8 cc = __builtin_bit_cast(bf16x8, u32x4{low[0], low[1], 0u, 0u});
-            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cc, twice, acc[jj][h][s][mt], 0, 0, 0);
-            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cols_a[mt * 64], twice, acc[jj][h][s][mt], 0, 0, 0);
-          }
+          twice[jj][h][s] = __builtin_bit_cast(bf16x8, u32x4{p0, p1, p0, p1});
         }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const u32x2 low = cols_c[mt * 64];
+      const bf16x8 ca = cols_a[mt * 64], cc = __builtin_bit_cast(bf16x8, u32x4{low[0], low[1], 0u, 0u});
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+        for (int h = 0; h < HW; ++h)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cc, twice[jj][h][s], acc[jj][h][s][mt], 0, 0, 0);
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+        for (int h = 0; h < HW; ++h)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ca, twice[jj][h][s], acc[jj][h][s][mt], 0, 0, 0);
     }
   }
 
@@ -638,13 +669,49 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
         }
 }
 
-// dphi: the partial sums in the order of their row ranges.
-__global__ __launch_bounds__(256) void dphi_sum_kernel(const float *__restrict__ part, float *__restrict__ dphi,
-                                                       uint64_t count, uint32_t split) {
-  for (uint64_t t = (uint64_t)blockIdx.x * 256 + threadIdx.x; t < count; t += (uint64_t)gridDim.x * 256) {
-    float a = 0.f;
-    for (uint32_t s = 0; s < split; ++s) a += part[s * count + t];
-    dphi[t] = a;
+// The last joins.  Workgroups below N + 3: a sum of db or dalpha each, from
+// the coefficient kernel's workgroups (a thread every 256th, then a tree).
+// The others: dphi from its row ranges, 64 vectors of four a workgroup, four
+// threads a vector that take a quarter of the ranges each, in order.
+__global__ __launch_bounds__(256) void join_kernel(const double *__restrict__ sums, int sum_blocks, int n,
+                                                   float *__restrict__ dalpha, float *__restrict__ db_pre,
+                                                   float *__restrict__ db_post, float *__restrict__ db_res,
+                                                   const f32x4 *__restrict__ part, f32x4 *__restrict__ dphi,
+                                                   uint64_t vecs, uint32_t split) {
+  const int N = n * n + 2 * n, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (blockIdx.x < (uint32_t)N + 3) {
+    __shared__ double waves[4];
+    const int k = blockIdx.x;
+    double a = 0.0;
+    for (int b = threadIdx.x; b < sum_blocks; b += 256) a += sums[(size_t)b * (N + 3) + k];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) a += __shfl_xor(a, o);
+    if (lane == 0) waves[wave] = a;
+    __syncthreads();
+    float *out = k < n ? db_pre + k : k < 2 * n ? db_post + (k - n) : k < N ? db_res + (k - 2 * n) : dalpha + (k - N);
+    if (threadIdx.x == 0) *out = (float)((waves[0] + waves[1]) + (waves[2] + waves[3]));
+    return;
+  }
+  __shared__ f32x4 quarter[3][64];
+  const uint32_t each = (split + 3) / 4, lo = wave * each, hi = lo + each < split ? lo + each : split;
+  for (uint64_t v0 = (uint64_t)(blockIdx.x - N - 3) * 64; v0 < vecs; v0 += (uint64_t)(gridDim.x - N - 3) * 64) {
+    const uint64_t v = v0 + lane;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f};
+    if (v < vecs) {
+      for (uint32_t s = lo; s < hi; s += 8) {
+        f32x4 x[8];
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u)
+          if (s + u < hi) x[u] = __builtin_nontemporal_load(part + (s + u) * vecs + v);
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u)
+          if (s + u < hi) a += x[u];
+      }
+    }
+    if (wave > 0) quarter[wave - 1][lane] = a;
+    __syncthreads();
+    if (wave == 0 && v < vecs) dphi[v] = ((a + quarter[0][lane]) + quarter[1][lane]) + quarter[2][lane];
+    __syncthreads();
   }
 }
 
@@ -667,20 +734,21 @@ hipError_t launch_t(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBw
   const uint32_t cvec = (uint32_t)(C / 8), blocks = (uint32_t)ckpt_blocks(C), rows = (uint32_t)B;
   const u32x4 *dF = static_cast<const u32x4 *>(a.dF_pre);
   hipError_t e;
-  pre_dots_kernel<NS, CK, 4><<<wgs(B, 1, 1u << 22), 256, 0, st>>>(a.X.x, a.X.scales, dF, dpre, rows, cvec, blocks);
+  pre_dots_kernel<NS, CK, 4><<<wgs((uint64_t)p.split * p.tiles_each * 16, 1, 1u << 22), 256, 0, st>>>(
+      a.X.x, a.X.scales, dF, dpre, rows, cvec, blocks, (uint32_t)p.split, (uint32_t)(p.tiles_each * 16));
   if ((e = hipGetLastError()) != hipSuccess) return e;
   coeffs_bwd_kernel<NS><<<(uint32_t)p.sum_blocks, sum_threads<NS>(), 0, st>>>(
       a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre, a.b_post, a.b_res, a.dH, dpre, a.H, records, sums,
       rows, 1.0 / ((double)NS * (double)C));
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  sums_kernel<<<T::N + 3, 64, 0, st>>>(sums, (int)p.sum_blocks, NS, a.dalpha, a.db_pre, a.db_post, a.db_res);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
   dx_dphi_kernel<NS, CK><<<(uint32_t)(p.slices * p.split), 64 * T::GROUPS * p.wc, 0, st>>>(
       static_cast<const char *>(a.X.x), a.X.scales, static_cast<const uint16_t *>(a.phi),
       static_cast<const char *>(a.dX_next), static_cast<const char *>(a.dF_pre), records, static_cast<char *>(a.dX), part, rows, (uint32_t)p.tiles_each, cvec, blocks, (uint32_t)p.slices, p.wc);
-  if ((e = hipGetLastError()) != hipSuccess || p.split == 1) return e;
-  const uint64_t count = (uint64_t)NS * C * T::N;
-  dphi_sum_kernel<<<wgs(count, 256, 1u << 22), 256, 0, st>>>(part, a.dphi, count, (uint32_t)p.split);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const uint64_t vecs = p.split > 1 ? (uint64_t)NS * C * T::N / 4 : 0;
+  join_kernel<<<T::N + 3 + wgs(vecs, 64, 1u << 20), 256, 0, st>>>(
+      sums, (int)p.sum_blocks, NS, a.dalpha, a.db_pre, a.db_post, a.db_res, reinterpret_cast<const f32x4 *>(part),
+      reinterpret_cast<f32x4 *>(a.dphi), vecs, (uint32_t)p.split);
   return hipGetLastError();
 }
 
@@ -701,11 +769,13 @@ CoeffsBwdPlan plan_n(int64_t B, int64_t C) {
   p.wc = 1;  // waves along the channels, as many as there are channels for
   while (p.wc < 8 / T::GROUPS && p.wc * T::CW < C) p.wc *= 2;
   p.slices = (C + p.wc * T::CW - 1) / (p.wc * T::CW);
-  // As many row ranges as fill the compute units once (a full workgroup has
-  // one to itself), but at least kMinTiles tiles in each: a range costs a copy
-  // of dphi.
-  int64_t split = kRound * (8 / (T::GROUPS * p.wc)) / p.slices;
-  if (split > tiles / kMinTiles) split = tiles / kMinTiles;
+  // Row ranges: a workgroup for every compute unit (a full workgroup has one
+  // to itself), down to a tile a range; smaller workgroups share a unit, and
+  // then a range gets kMinTiles tiles at least, as each costs a copy of dphi.
+  int64_t split = kRound / p.slices;
+  const int64_t more = kRound * (8 / (T::GROUPS * p.wc)) / p.slices;
+  if (split < (more < tiles / kMinTiles ? more : tiles / kMinTiles)) split = more < tiles / kMinTiles ? more : tiles / kMinTiles;
+  if (split > tiles) split = tiles;
   if (split < 1) split = 1;
   p.tiles_each = (tiles + split - 1) / split;
   p.split = (tiles + p.tiles_each - 1) / p.tiles_each;

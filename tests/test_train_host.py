@@ -120,7 +120,7 @@ def test_size_functions():
     for B in (1, 5, 1000, 16384, 1 << 20):
         for n, C in ((1, 8), (4, 7168), (8, 4096)):
             N = n * n + 2 * n
-            assert mhc.mhc_coeffs_pre_bwd_workspace_size(B, n, C) >= 4 * (B * (N + 1) + n * C * N)
+            assert mhc.mhc_coeffs_pre_bwd_workspace_size(B, n, C) >= 4 * B * N   # dlogit at least
             assert mhc.mhc_embed_bwd_workspace_size(B, n, C, 1000) >= 8 * B
 
 
