@@ -54,20 +54,15 @@ struct Tiles {
   static constexpr int kChunks = (kBytes + 1023) / 1024, kStride = kChunks * 1024;
 };
 
-// dH_pre [B, n]: a workgroup a row.  The rows of the row ranges' beginnings
-// come last, so that what the big cache still holds of X_t and dF_pre is what
-// dx_dphi_kernel reads first.
+// dH_pre [B, n]: a workgroup a row.
 template <int NS, bool CK, int W>
 __global__ __launch_bounds__(64 * W) void pre_dots_kernel(const void *__restrict__ X,
                                                           const uint8_t *__restrict__ scales,
                                                           const u32x4 *__restrict__ dF, float *__restrict__ dpre,
-                                                          uint32_t B, uint32_t cvec, uint32_t blocks, uint32_t split,
-                                                          uint32_t rows_each) {
+                                                          uint32_t B, uint32_t cvec, uint32_t blocks) {
   __shared__ float part[W][NS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (uint64_t p = blockIdx.x; p < (uint64_t)split * rows_each; p += gridDim.x) {
-    const uint64_t row = p % split * rows_each + (rows_each - 1 - p / split);
-    if (row >= B) continue;
+  for (uint32_t row = blockIdx.x; row < B; row += gridDim.x) {
     float acc[NS];
 #pragma unroll
     for (int j = 0; j < NS; ++j) acc[j] = 0.f;
@@ -734,8 +729,7 @@ hipError_t launch_t(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBw
   const uint32_t cvec = (uint32_t)(C / 8), blocks = (uint32_t)ckpt_blocks(C), rows = (uint32_t)B;
   const u32x4 *dF = static_cast<const u32x4 *>(a.dF_pre);
   hipError_t e;
-  pre_dots_kernel<NS, CK, 4><<<wgs((uint64_t)p.split * p.tiles_each * 16, 1, 1u << 22), 256, 0, st>>>(
-      a.X.x, a.X.scales, dF, dpre, rows, cvec, blocks, (uint32_t)p.split, (uint32_t)(p.tiles_each * 16));
+  pre_dots_kernel<NS, CK, 4><<<wgs(B, 1, 1u << 22), 256, 0, st>>>(a.X.x, a.X.scales, dF, dpre, rows, cvec, blocks);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   coeffs_bwd_kernel<NS><<<(uint32_t)p.sum_blocks, sum_threads<NS>(), 0, st>>>(
       a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre, a.b_post, a.b_res, a.dH, dpre, a.H, records, sums,
