@@ -338,16 +338,22 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
 //
 // Memory: in that layout the lanes of a quad have four different rows, so
 // loads straight into it touch 64 separate 16-byte pieces each (measured 915
-// us at n=4, C=7168, B=16384 from the checkpoint).  Direct-to-LDS loads take
-// the data in memory order instead (lanes 4 r .. 4 r + 3: 64 bytes of row r),
-// one tile ahead, without registers; a row's four pieces are rotated by its
-// row / 4 (xor), so that the reads in the matrix layout meet no bank twice.
-// dX goes back through LDS the same way and is stored in memory order.  The
-// tile's record is staged the same way, shared by the workgroup's waves.
+// us at n=4, C=7168, B=16384 from the checkpoint).  Direct-to-LDS loads take a
+// tile of the workgroup's channels in memory order instead (512 bytes of a row
+// at a time at n = 4, 128 at n = 8), one or two tiles ahead, without
+// registers; a row's 16-byte pieces are exchanged by an xor with the row, so
+// that the reads in the matrix layout meet no bank twice.  dX takes G's or
+// X_t's place in LDS and is stored from there, four or eight lanes a row.  A
+// tile's record is staged the same way.
 //
-// Waits: a tile's loads are issued a whole tile before they are waited for,
-// and vmcnt counts in order; only the dX stores of the tile in between are
-// younger, so "at most that many outstanding" means the loads have landed.
+// Measured at n=4, C=7168, B=16384 from the checkpoint: 500 us for 2.6 GB
+// (5.2 TB/s); without any arithmetic the same loads and stores take 490.
+//
+// Waits: vmcnt counts in order, and between a tile's loads and their use the
+// wave issues the loads and dX stores of the tiles in between and no other
+// memory access (Stage::kYounger of them at least), so "at most that many
+// outstanding" means that the tile has landed.  Where fewer may be issued (the
+// first and last tiles, waves past the channels) the wait is for all.
 __device__ __attribute__((aligned(256))) uint32_t g_train_zero[64];  // what loads past the edges read
 
 template <int BYTES>
@@ -366,91 +372,113 @@ __device__ __forceinline__ uint32_t lds_addr_of(const char *p) { return (uint32_
 template <int NS, bool CK>
 struct Stage {
   using T = Tiles<NS>;
-  // Bytes of a stage: G (a KiB a stream and step), X_t, dF_pre, scale bytes
-  // (a dword each).  With one stream a wave (n = 8) dX leaves through the
-  // wave's X slots, else through its G slots, which nobody else reads.
   static constexpr int kWaves = 8, kAlong = kWaves / T::GROUPS;
-  static constexpr bool kShared = T::GROUPS > 1;
+  static constexpr bool kShared = T::GROUPS > 1;  // G is read by waves of other streams
+  // Stages of LDS; loads are issued kStages - 1 tiles ahead.
+  static constexpr int kStages = NS == 4 ? 2 : 3;
+  static constexpr int kDist = kStages - 1;
+  // Bytes of a stage: G, X_t, dF_pre, scale bytes (a dword each).
   static constexpr int kG = kAlong * T::HW * NS * 1024;
-  static constexpr int kXWave = T::JW * T::HW * (CK && !kShared ? 512 : 1024);
-  static constexpr int kX = kWaves * kXWave;
+  static constexpr int kX = kWaves * T::JW * T::HW * (CK ? 512 : 1024);
   static constexpr int kF = kAlong * T::HW * 1024;
   static constexpr int kS = CK ? kWaves * 256 : 0;
   static constexpr int kBytes = kG + kX + kF + kS;
-  // Codes of a wave: [JW][16 rows][32] bytes, or at n = 8 [16 rows][64] in the
-  // second KiB (dX of the first step goes to the first).
-  static constexpr int kCodes = kShared ? 1024 : 0;
+  // dX takes the place of G in LDS (a wave's own columns of it), or where G is
+  // shared that of X_t, or (from codes) a place of its own.
+  static constexpr bool kOwnOut = kShared && CK;
+  static constexpr int kOutBytes = kOwnOut ? kWaves * T::HW * 1024 : 16;
+  // Loads a wave issues for a tile at least (without its share of the record),
+  // and its stores of a tile: what may be younger than a tile's loads.
+  static constexpr int kLoads = kShared ? T::HW + (CK ? 1 + 1 : T::HW)
+                                        : NS + 1 + (CK ? T::JW / 2 + 1 : T::JW);
+  static constexpr int kStores = T::JW * T::HW;
+  static constexpr int kYounger = kDist == 1 ? kStores : 2 * kStores + kLoads;
 };
 
 template <int NS, bool CK>
 __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     const char *__restrict__ X, const uint8_t *__restrict__ scales, const uint16_t *__restrict__ phi,
     const char *__restrict__ G, const char *__restrict__ dF, const char *__restrict__ records, char *__restrict__ dX,
-    float *__restrict__ out, uint32_t B, uint32_t tiles_each, uint32_t cvec, uint32_t blocks, uint32_t slices,
-    int wc) {
+    float *__restrict__ out, uint32_t B, uint32_t cvec, uint32_t blocks, uint32_t slices, int wc) {
   using T = Tiles<NS>;
   using S = Stage<NS, CK>;
   constexpr int N = T::N, KS = T::KS, MT = T::MT, JW = T::JW, GROUPS = T::GROUPS, HW = T::HW;
-  __shared__ __attribute__((aligned(1024))) char stage[2][S::kBytes];
-  __shared__ __attribute__((aligned(1024))) char record[2][T::kStride];
+  __shared__ __attribute__((aligned(1024))) char stage[S::kStages][S::kBytes];
+  __shared__ __attribute__((aligned(1024))) char record[S::kStages][T::kStride];
+  __shared__ __attribute__((aligned(1024))) char own_out[S::kOutBytes];
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
   // wc waves along the channels, GROUPS along the streams.
   const int cw = wave / GROUPS, group = wave % GROUPS, waves = wc * GROUPS;
-  const uint32_t slice = blockIdx.x % slices, range = blockIdx.x / slices;
-  const uint32_t v_wave = (slice * (uint32_t)wc + cw) * (HW * 4);  // the wave's first vector of eight channels
+  const uint32_t slice = blockIdx.x % slices, range = blockIdx.x / slices, split = gridDim.x / slices;
+  const uint32_t v_wg = slice * (uint32_t)wc * (HW * 4);  // the workgroup's first vector of eight channels
+  const uint32_t v_wave = v_wg + cw * (HW * 4);
   const int lo16 = lane & 15, q = lane >> 4, j0 = group * JW;
-  const uint32_t tiles = (B + 15) / 16, first = range * tiles_each;
-  const uint32_t last = tiles - first < tiles_each ? tiles : first + tiles_each;
+  // Its tiles: every `split`th, from `range` on, so that all workgroups move
+  // through the rows together (with a run of rows each, 14 us slower at n=4,
+  // C=7168, B=16384).
+  const uint32_t count = ((B + 15) / 16 - range + split - 1) / split;
+  const auto tile_at = [&](uint32_t k) { return range + k * split; };
   const size_t row_bytes = (size_t)cvec * 16;  // a stream of a row
 
-  // The 16-byte piece a lane takes in memory order, and its place in the
-  // matrix layout.
-  const int mrow = lane >> 2, mq = (lane & 3) ^ ((lane >> 4) & 3);
-  const int slot16 = (lo16 * 4 + (q ^ ((lo16 >> 2) & 3))) * 16;
+  // A stream's tile in LDS: 16 rows of 1 << lg 16-byte pieces, piece p of row
+  // r at p ^ turn(r, lg): reads of one piece of every row meet 16 different
+  // places of the 256 bytes that the banks span.
+  const int lg = __builtin_ctz(wc) + (HW == 2 ? 3 : 2);
+  const auto turn = [](int row, int l) { return l >= 4 ? row : (row >> (4 - l)) & ((1 << l) - 1); };
+  const auto piece_of = [&](int row, int p, int l) { return ((row << l) + (p ^ turn(row, l))) * 16; };
 
   const auto issue = [&](uint32_t tile, int st) {
     const char *zero = reinterpret_cast<const char *>(g_train_zero);
     const uint32_t at = lds_addr_of(stage[st]), row0 = tile * 16;
-    const uint32_t g_at = at + (uint32_t)cw * (HW * NS * 1024), x_at = at + S::kG + (uint32_t)wave * S::kXWave;
+    // bf16 tiles: KiB `part` of a stream's
+    const auto offset = [&](int part, bool &in) -> size_t {
+      const int at_lane = part * 64 + lane, r = at_lane >> lg, p = (at_lane & ((1 << lg) - 1)) ^ turn(r, lg);
+      const uint32_t row = row0 + r, v = v_wg + p;
+      in = row < B && v < cvec;
+      return ((size_t)row * NS * cvec + v) * 16;
+    };
+    const int kib = 256 << lg;  // bytes of a stream's tile
 #pragma unroll
     for (int h = 0; h < HW; ++h) {
-      const uint32_t row = row0 + mrow, v = v_wave + h * 4 + mq;
-      const bool in = row < B && v < cvec;
-      const size_t at_row = (size_t)row * NS * row_bytes + (size_t)v * 16;
+      const int part = S::kShared ? h : cw;
+      bool in;
+      const size_t o = offset(part, in);
       if constexpr (!S::kShared) {
 #pragma unroll
         for (int i = 0; i < NS; ++i)
-          dma<16>(in ? G + at_row + (size_t)i * row_bytes : zero, g_at + (h * NS + i) * 1024);
+          dma<16>(in ? G + o + (size_t)i * row_bytes : zero, at + i * kib + part * 1024);
       } else {
-        dma<16>(in ? G + at_row + (size_t)group * row_bytes : zero, g_at + (h * NS + group) * 1024);
+        dma<16>(in ? G + o + (size_t)group * row_bytes : zero, at + group * kib + part * 1024);
       }
-      if (!S::kShared || group == h)
-        dma<16>(in ? dF + (size_t)row * row_bytes + (size_t)v * 16 : zero, at + S::kG + S::kX + (cw * HW + h) * 1024);
+      if (!S::kShared || group == h) {
+        const int at_lane = part * 64 + lane, r = at_lane >> lg, p = (at_lane & ((1 << lg) - 1)) ^ turn(r, lg);
+        dma<16>(in ? dF + (size_t)(row0 + r) * row_bytes + (size_t)(v_wg + p) * 16 : zero,
+                at + S::kG + S::kX + part * 1024);
+      }
       if constexpr (!CK) {
 #pragma unroll
         for (int jj = 0; jj < JW; ++jj)
-          dma<16>(in ? X + at_row + (size_t)(j0 + jj) * row_bytes : zero, x_at + (h * JW + jj) * 1024);
+          dma<16>(in ? X + o + (size_t)(j0 + jj) * row_bytes : zero, at + S::kG + (j0 + jj) * kib + part * 1024);
       }
     }
     if constexpr (CK) {
-      // Rows of 32 HW codes, linear; 16 bytes a lane where a stream's codes
-      // are that aligned, else four.
-      constexpr int kRow = 32 * HW;
+      // Codes: the same with rows of half as many pieces; 16 bytes a lane
+      // where a stream's codes are that aligned, else four.
       const size_t stream = (size_t)cvec * 8;
-      const auto code = [&](int byte, int width) -> const char * {  // of [JW][16][kRow]
-        const int jj = byte / (16 * kRow), r = byte / kRow % 16, c = byte % kRow;
-        const uint32_t row = row0 + r, ch = v_wave * 8 + c;
-        return jj < JW && row < B && ch < cvec * 8 ? X + ((size_t)row * NS + j0 + jj) * stream + ch : zero;
+      const int lc = lg - 1, bytes = 256 << lc, all = S::kShared ? bytes : JW * bytes;
+      const uint32_t x_at = at + S::kG + (S::kShared ? group * bytes : 0);
+      const auto code = [&](int byte) -> const char * {
+        const int jj = byte >> (8 + lc), r = (byte >> (4 + lc)) & 15;
+        const int p = ((byte >> 4) & ((1 << lc) - 1)) ^ turn(r, lc);
+        const uint32_t row = row0 + r, ch = v_wg * 8 + p * 16 + (byte & 15);
+        return row < B && ch < cvec * 8 ? X + ((size_t)row * NS + j0 + jj) * stream + ch : zero;
       };
       if (cvec % 2 == 0) {
-#pragma unroll
-        for (int k = 0; k < (JW * 16 * kRow + 1023) / 1024; ++k)
-          if (JW * 16 * kRow >= 1024 || lane < JW * 16 * kRow / 16)
-            dma<16>(code(k * 1024 + lane * 16, 16), x_at + S::kCodes + k * 1024);
+        for (int b = (S::kShared ? 0 : cw) * 1024; b < all; b += (S::kShared ? 1 : wc) * 1024)
+          if (b + lane * 16 < all) dma<16>(code(b + lane * 16), x_at + b);
       } else {
-#pragma unroll
-        for (int k = 0; k < JW * 16 * kRow / 256; ++k)
-          dma<4>(code(k * 256 + lane * 4, 4), x_at + S::kCodes + k * 256);
+        for (int b = (S::kShared ? 0 : cw) * 256; b < all; b += (S::kShared ? 1 : wc) * 256)
+          dma<4>(code(b + lane * 4), x_at + b);
       }
       // One scale byte for each row and stream (n = 8: row and step).
       const uint32_t row = row0 + lo16, v = v_wave + (S::kShared ? q * 4 : 0);
@@ -462,7 +490,9 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     for (int k = wave; k < T::kChunks; k += waves)
       dma<16>(records + (size_t)tile * T::kStride + k * 1024 + lane * 16, lds_addr_of(record[st]) + k * 1024);
   };
-  issue(first, 0);
+#pragma unroll
+  for (int k = 0; k < S::kDist; ++k)
+    if ((uint32_t)k < count) issue(tile_at(k), k);
 
   // phi: operand (stream, step h, t, ks), lane 16 q + m: coefficients
   // 32 ks + 8 q .. + 7 of channel 32 h + 8 (m / 4) + 4 t + m % 4 of the wave.
@@ -507,20 +537,36 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
         for (int mt = 0; mt < MT; ++mt) acc[jj][h][s][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  // Every step of the wave has channels: its stores are issued each tile.
-  const bool full = v_wave + (HW - 1) * 4 < cvec;
-  for (uint32_t tile = first; tile < last; ++tile) {
-    const int st = (int)(tile - first) & 1;
-    if (tile == first || !full)
+  // Where all of the wave's pieces have channels, every store is issued each
+  // tile.
+  const bool full = v_wave + HW * 4 <= cvec;
+  int st = 0;  // the tile's stage
+  for (uint32_t k = 0; k < count; ++k) {
+    const uint32_t tile = tile_at(k);
+    if (k < S::kDist || k + S::kDist > count || !full)
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     else
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(JW * HW) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::kYounger) : "memory");
     // The other waves' share of the tile has landed, and everybody has read
     // the last of the stage that the next loads fill.
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (tile + 1 < last) issue(tile + 1, st ^ 1);
+    if (k + S::kDist < count) issue(tile_at(k + S::kDist), st == 0 ? S::kStages - 1 : st - 1);
     char *mine = stage[st];
     const char *now = record[st];
+    char *const o_at = S::kOwnOut ? own_out + wave * (HW * 1024) : S::kShared ? mine + S::kG + (j0 * 256 << lg) : mine;
+    st = st + 1 == S::kStages ? 0 : st + 1;
+    const char *const f_at = mine + S::kG + S::kX, *const s_at = f_at + S::kF + wave * 256;
+    const auto x_of = [&](int h, int jj) -> u32x4 {
+      if constexpr (CK) {
+        const int lc = lg - 1, p = (cw * HW + h) * 2 + (q >> 1);
+        const char *x = mine + S::kG + ((j0 + jj) * 256 << lc) + piece_of(lo16, p, lc) + (q & 1) * 8;
+        return held_bf16(*reinterpret_cast<const u32x2 *>(x),
+                         (int)reinterpret_cast<const uint32_t *>(s_at)[(S::kShared ? h : jj) * 16 + lo16]);
+      } else {
+        return *reinterpret_cast<const u32x4 *>(mine + S::kG + ((j0 + jj) * 256 << lg) +
+                                                piece_of(lo16, (cw * HW + h) * 4 + q, lg));
+      }
+    };
     bf16x8 bh[KS], bm[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -534,19 +580,10 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     bf16x8 twice[JW][HW][2];
 #pragma unroll
     for (int h = 0; h < HW; ++h) {
-      char *g_at = mine + cw * (HW * NS * 1024) + h * NS * 1024;
-      char *x_at = mine + S::kG + wave * S::kXWave;
       u32x4 x[JW];
 #pragma unroll
-      for (int jj = 0; jj < JW; ++jj) {
-        if constexpr (CK) {
-          const u32x2 code = *reinterpret_cast<const u32x2 *>(x_at + S::kCodes + (jj * 16 + lo16) * (32 * HW) + h * 32 + q * 8);
-          const uint32_t s = reinterpret_cast<const uint32_t *>(mine + S::kG + S::kX + S::kF + wave * 256)[(S::kShared ? h : jj) * 16 + lo16];
-          x[jj] = held_bf16(code, (int)s);
-        } else {
-          x[jj] = *reinterpret_cast<const u32x4 *>(x_at + (h * JW + jj) * 1024 + slot16);
-        }
-      }
+      for (int jj = 0; jj < JW; ++jj) x[jj] = x_of(h, jj);
+      const int at = piece_of(lo16, (cw * HW + h) * 4 + q, lg);
       float o[JW][8];
 #pragma unroll
       for (int jj = 0; jj < JW; ++jj) {
@@ -566,7 +603,7 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
       }
       {
         float fw[8];
-        widen8(*reinterpret_cast<const u32x4 *>(mine + S::kG + S::kX + (cw * HW + h) * 1024 + slot16), fw);
+        widen8(*reinterpret_cast<const u32x4 *>(f_at + at), fw);
 #pragma unroll
         for (int jj = 0; jj < JW; ++jj) {
           const float hpre = mix[(j0 + jj) * 16];
@@ -577,7 +614,7 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         float gw[8];
-        widen8(*reinterpret_cast<const u32x4 *>(g_at + i * 1024 + slot16), gw);
+        widen8(*reinterpret_cast<const u32x4 *>(mine + (i * 256 << lg) + at), gw);
 #pragma unroll
         for (int jj = 0; jj < JW; ++jj) {
           const float hres = mix[(NS + i * NS + j0 + jj) * 16];
@@ -585,27 +622,11 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
           for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hres, gw[e], o[jj][e]);
         }
       }
-      // Out in memory order: over the wave's own G (or X) pieces of this step.
-      char *o_at = S::kShared ? x_at + h * 1024 : g_at;
-      __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int jj = 0; jj < JW; ++jj)
-        *reinterpret_cast<u32x4 *>(o_at + jj * 1024 + slot16) =
+        *reinterpret_cast<u32x4 *>(o_at + (jj * 256 << lg) + at) =
             u32x4{pack_bf16x2(o[jj][0], o[jj][1]), pack_bf16x2(o[jj][2], o[jj][3]), pack_bf16x2(o[jj][4], o[jj][5]),
                   pack_bf16x2(o[jj][6], o[jj][7])};
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_wave_barrier();
-      {
-        const uint32_t row = tile * 16 + mrow, v = v_wave + h * 4 + mq;
-        char *dst = dX + ((size_t)row * NS + j0) * row_bytes + (size_t)v * 16;
-        u32x4 y[JW];
-#pragma unroll
-        for (int jj = 0; jj < JW; ++jj) y[jj] = *reinterpret_cast<const u32x4 *>(o_at + jj * 1024 + lane * 16);
-        if (row < B && v < cvec) {
-#pragma unroll
-          for (int jj = 0; jj < JW; ++jj) *reinterpret_cast<u32x4 *>(dst + (size_t)jj * row_bytes) = y[jj];
-        }
-      }
 #pragma unroll
       for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
@@ -615,6 +636,25 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
           const uint32_t p0 = pack_bf16x2(m[0], m[1]), p1 = pack_bf16x2(m[2], m[3]);
           twice[jj][h][s] = __builtin_bit_cast(bf16x8, u32x4{p0, p1, p0, p1});
         }
+    }
+    // dX in memory order.  The wave's own pieces only: 64 bytes a row (128 at
+    // n = 8); storing whole rows of the workgroup's after another barrier
+    // measured 15 us slower at n=4, C=7168, B=16384.
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int h = 0; h < HW; ++h) {
+      constexpr int kRow = 4 * HW;  // the wave's pieces of a row
+      const int r = (h * 64 + lane) / kRow, p = cw * kRow + ((lane & (kRow - 1)) ^ (turn(r, lg) & (kRow - 1)));
+      const uint32_t row = tile * 16 + r, v = v_wg + p;
+      char *const dst = dX + ((size_t)row * NS + j0) * row_bytes + (size_t)v * 16;
+      u32x4 y[JW];
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj) y[jj] = *reinterpret_cast<const u32x4 *>(o_at + (jj * 256 << lg) + piece_of(r, p, lg));
+      if (row < B && v < cvec) {
+#pragma unroll
+        for (int jj = 0; jj < JW; ++jj) *reinterpret_cast<u32x4 *>(dst + (size_t)jj * row_bytes) = y[jj];
+      }
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -737,7 +777,7 @@ hipError_t launch_t(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBw
   if ((e = hipGetLastError()) != hipSuccess) return e;
   dx_dphi_kernel<NS, CK><<<(uint32_t)(p.slices * p.split), 64 * T::GROUPS * p.wc, 0, st>>>(
       static_cast<const char *>(a.X.x), a.X.scales, static_cast<const uint16_t *>(a.phi),
-      static_cast<const char *>(a.dX_next), static_cast<const char *>(a.dF_pre), records, static_cast<char *>(a.dX), part, rows, (uint32_t)p.tiles_each, cvec, blocks, (uint32_t)p.slices, p.wc);
+      static_cast<const char *>(a.dX_next), static_cast<const char *>(a.dF_pre), records, static_cast<char *>(a.dX), part, rows, cvec, blocks, (uint32_t)p.slices, p.wc);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const uint64_t vecs = p.split > 1 ? (uint64_t)NS * C * T::N / 4 : 0;
   join_kernel<<<T::N + 3 + wgs(vecs, 64, 1u << 20), 256, 0, st>>>(
@@ -763,16 +803,16 @@ CoeffsBwdPlan plan_n(int64_t B, int64_t C) {
   p.wc = 1;  // waves along the channels, as many as there are channels for
   while (p.wc < 8 / T::GROUPS && p.wc * T::CW < C) p.wc *= 2;
   p.slices = (C + p.wc * T::CW - 1) / (p.wc * T::CW);
-  // Row ranges: a workgroup for every compute unit (a full workgroup has one
-  // to itself), down to a tile a range; smaller workgroups share a unit, and
-  // then a range gets kMinTiles tiles at least, as each costs a copy of dphi.
+  // Row ranges: as many workgroups as the compute units hold of full ones
+  // (eight waves on each), down to a tile a range; smaller workgroups share a
+  // unit, and then a range gets kMinTiles tiles at least, as each costs a copy
+  // of dphi.
+  const int64_t room = kRound * (8 / (T::GROUPS * p.wc)) / p.slices;
   int64_t split = kRound / p.slices;
-  const int64_t more = kRound * (8 / (T::GROUPS * p.wc)) / p.slices;
-  if (split < (more < tiles / kMinTiles ? more : tiles / kMinTiles)) split = more < tiles / kMinTiles ? more : tiles / kMinTiles;
+  if (split < (room < tiles / kMinTiles ? room : tiles / kMinTiles)) split = room < tiles / kMinTiles ? room : tiles / kMinTiles;
   if (split > tiles) split = tiles;
   if (split < 1) split = 1;
-  p.tiles_each = (tiles + split - 1) / split;
-  p.split = (tiles + p.tiles_each - 1) / p.tiles_each;
+  p.split = split;
   const int64_t per = sum_threads<NS>() / (NS * NS), groups = (B + per - 1) / per;
   p.sum_blocks = groups < kMaxSumBlocks ? groups : kMaxSumBlocks;
   p.records = 0;

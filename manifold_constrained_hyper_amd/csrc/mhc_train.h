@@ -38,8 +38,7 @@ hipError_t launch_post_res_bwd(int n, int64_t B, int64_t C, HeldX X, const void 
 struct CoeffsBwdPlan {
   int wc;              // waves along the channels in a workgroup
   int64_t slices;      // workgroups along the channels
-  int64_t split;       // row ranges
-  int64_t tiles_each;  // tiles of 16 rows in each
+  int64_t split;       // row ranges (every split-th tile of 16 rows)
   int64_t sum_blocks;  // workgroups of the coefficient kernel
   size_t records, dpre, sums, dphi, total_bytes;
 };
