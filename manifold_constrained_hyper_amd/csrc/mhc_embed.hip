@@ -10,6 +10,7 @@
 #include "mhc_device.h"
 #include "mhc_train.h"
 
+#include <type_traits>
 #include <utility>
 
 namespace mhc {
@@ -52,8 +53,54 @@ constexpr uint32_t kTile = 1024, kJoin = 16;
 
 __device__ __forceinline__ uint32_t token_of(u64 key) { return (uint32_t)(key >> 32); }
 
-// Bitonic sort, one key a thread: partners inside a wave trade by lane moves,
-// others through LDS (10 of the 55 steps).
+// The value of lane ^ D, without LDS: DPP inside rows of 16 lanes, row and
+// half swaps beyond.
+template <int D>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
+  const auto dpp = [](uint32_t v, auto ctrl) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, decltype(ctrl)::value, 0xF, 0xF, false);
+  };
+  if constexpr (D == 1) return dpp(x, std::integral_constant<int, 0xB1>{});
+  if constexpr (D == 2) return dpp(x, std::integral_constant<int, 0x4E>{});
+  // 7 - lane in its eight, then 3 - lane in its four
+  if constexpr (D == 4) return dpp(dpp(x, std::integral_constant<int, 0x141>{}), std::integral_constant<int, 0x1B>{});
+  if constexpr (D == 8) return dpp(x, std::integral_constant<int, 0x128>{});  // lane + 8 in its row
+  if constexpr (D == 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return threadIdx.x & 16 ? s[0] : s[1];
+  }
+  if constexpr (D == 32) {
+    const auto s = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return threadIdx.x & 32 ? s[0] : s[1];
+  }
+}
+template <int D>
+__device__ __forceinline__ u64 lane_xor64(u64 x) {
+  return ((u64)lane_xor<D>((uint32_t)(x >> 32)) << 32) | lane_xor<D>((uint32_t)x);
+}
+
+// Bitonic sort, one key a thread: a step's partners are D apart.
+template <int SIZE, int D>
+__device__ __forceinline__ void sort_steps(u64 &key, u64 *swap, uint32_t t) {
+  u64 other;
+  if constexpr (D >= 64) {
+    __syncthreads();
+    swap[t] = key;
+    __syncthreads();
+    other = swap[t ^ D];
+  } else {
+    other = lane_xor64<D>(key);
+  }
+  const bool up = (t & SIZE) == 0, low = (t & D) == 0;
+  key = (up == low) == (key < other) ? key : other;
+  if constexpr (D > 1) sort_steps<SIZE, D / 2>(key, swap, t);
+}
+template <int SIZE>
+__device__ __forceinline__ void sort_tile(u64 &key, u64 *swap, uint32_t t) {
+  sort_steps<SIZE, SIZE / 2>(key, swap, t);
+  if constexpr (SIZE < (int)kTile) sort_tile<2 * SIZE>(key, swap, t);
+}
+
 __global__ __launch_bounds__(kTile) void sort_tiles_kernel(const int64_t *__restrict__ tokens, uint32_t B, int64_t V,
                                                            u64 *__restrict__ keys) {
   __shared__ u64 swap[kTile];
@@ -64,59 +111,79 @@ __global__ __launch_bounds__(kTile) void sort_tiles_kernel(const int64_t *__rest
     const int64_t id = tokens[row];
     key = ((u64)(id >= 0 && id < V ? (uint32_t)id : kNoToken) << 32) | row;
   }
-  for (uint32_t size = 2; size <= kTile; size <<= 1)
-    for (uint32_t d = size >> 1; d > 0; d >>= 1) {
-      u64 other;
-      if (d >= 64) {
-        __syncthreads();
-        swap[t] = key;
-        __syncthreads();
-        other = swap[t ^ d];
-      } else {
-        other = __shfl_xor(key, (int)d);
-      }
-      const bool up = (t & size) == 0, low = (t & d) == 0;
-      const bool less = key < other;
-      key = (up == low) == less ? key : other;
-    }
+  sort_tile<2>(key, swap, t);
   if (row < B) keys[row] = key;
 }
 
-// Runs of `run` sorted keys -> runs of kJoin times that.
+// Runs of `run` sorted keys (a power of two) -> runs of kJoin times that.  The
+// searches of a key in the other runs go side by side, as each is a chain of
+// dependent loads.
 __global__ __launch_bounds__(kThreads) void join_runs_kernel(const u64 *__restrict__ in, u64 *__restrict__ out,
-                                                             uint32_t B, uint64_t run) {
+                                                             uint32_t B, uint64_t run, int log_run) {
   const uint64_t p = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
   if (p >= B) return;
   const u64 key = in[p];
-  const uint64_t mine = p / run, first = mine / kJoin * kJoin;
-  uint64_t at = p - mine * run;
-  for (uint64_t q0 = first; q0 < first + kJoin; q0 += 4) {
-    uint64_t lo[4], len[4];
+  const uint64_t mine = p >> log_run, first = mine / kJoin * kJoin;
+  uint64_t less[kJoin];  // keys of each run found to be smaller
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint64_t q = q0 + u;
-      lo[u] = q * run;
-      len[u] = q == mine || lo[u] >= B ? 0 : (B - lo[u] < run ? B - lo[u] : run);
+  for (uint32_t u = 0; u < kJoin; ++u) less[u] = 0;
+  for (uint64_t step = run; step > 0; step >>= 1) {
+#pragma unroll
+    for (uint32_t u = 0; u < kJoin; ++u) {
+      // the first less[u] keys are smaller; are the next `step` ones too?
+      const uint64_t upto = less[u] + step, at = ((first + u) << log_run) + upto - 1;
+      const bool there = upto <= run && at < B;
+      const u64 other = in[there ? at : p];
+      less[u] = there && other < key ? upto : less[u];
     }
-    // Four searches side by side; [lo, lo + len) holds the first key that is not smaller.
-    for (uint64_t left = run; left > 0; left >>= 1) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (len[u] == 0) continue;
-        const uint64_t half = len[u] >> 1;
-        if (in[lo[u] + half] < key) {
-          lo[u] += half + 1;
-          len[u] -= half + 1;
-        } else {
-          len[u] = half;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (q0 + u != mine && (q0 + u) * run < B) at += lo[u] - (q0 + u) * run;
   }
-  out[first * run + at] = key;
+  uint64_t place = first << log_run;
+#pragma unroll
+  for (uint32_t u = 0; u < kJoin; ++u) place += less[u];  // its own run counts the keys before it
+  out[place] = key;
+}
+
+// The same for the first level, whose runs are the tiles: their tokens fit
+// LDS (64 KiB), where a step of the searches costs a tenth of what it does in
+// the cache.  Of equal tokens the rows of an earlier tile come first.
+constexpr uint32_t kJoinThreads = 512;  // a workgroup's keys are of one tile
+__global__ __launch_bounds__(kJoinThreads) void join_tiles_kernel(const u64 *__restrict__ in, u64 *__restrict__ out,
+                                                                  uint32_t B) {
+  constexpr uint32_t kAll = kJoin * kTile, kLoads = kAll / 2 / kJoinThreads;
+  __shared__ uint32_t tok[kAll];
+  const uint32_t p = blockIdx.x * kJoinThreads + threadIdx.x;
+  const uint32_t first = p / kAll * kAll, count = B - first < kAll ? B - first : kAll;
+  // Two keys a load, all of a thread's loads in flight at once.
+  ulonglong2 two[kLoads];
+#pragma unroll
+  for (uint32_t k = 0; k < kLoads; ++k) {
+    const uint32_t at = 2 * (threadIdx.x + k * kJoinThreads);
+    two[k] = at + 1 < count ? *reinterpret_cast<const ulonglong2 *>(in + first + at)
+                            : ulonglong2{at < count ? in[first + at] : ~0ull, ~0ull};
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kLoads; ++k)
+    *reinterpret_cast<uint2 *>(tok + 2 * (threadIdx.x + k * kJoinThreads)) = uint2{token_of(two[k].x), token_of(two[k].y)};
+  __syncthreads();
+  if (p >= B) return;
+  const u64 key = in[p];
+  const uint32_t mine = (p - first) / kTile, token = token_of(key);
+  uint32_t less[kJoin];
+#pragma unroll
+  for (uint32_t u = 0; u < kJoin; ++u) less[u] = 0;
+  for (uint32_t step = kTile; step > 0; step >>= 1) {
+#pragma unroll
+    for (uint32_t u = 0; u < kJoin; ++u) {
+      // (places past the last key hold ~0, which no token exceeds)
+      const uint32_t upto = less[u] + step, there = tok[u * kTile + (upto <= kTile ? upto : kTile) - 1];
+      const bool before = there < token || (there == token && u < mine);
+      less[u] = before && upto <= kTile ? upto : less[u];
+    }
+  }
+  uint32_t place = first;
+#pragma unroll
+  for (uint32_t u = 0; u < kJoin; ++u) place += u == mine ? p - first - mine * kTile : less[u];
+  out[place] = key;
 }
 
 // First place whose token is not below `token`.
@@ -141,7 +208,7 @@ __device__ __forceinline__ void write_row(f32x4 *o, const float (&acc)[8], float
   for (int h = 0; h < 2; ++h) {
     f32x4 x = f32x4{acc[4 * h], acc[4 * h + 1], acc[4 * h + 2], acc[4 * h + 3]} * scale;
     if (accumulate) x += o[h];
-    __builtin_nontemporal_store(x, o + h);
+    o[h] = x;  // half of every 32 bytes: the cache joins the two (streaming stores cost 45 us more)
   }
 }
 
@@ -154,17 +221,26 @@ __device__ __forceinline__ void write_row(f32x4 *o, const float (&acc)[8], float
 constexpr int kAhead = 16;  // 16-byte loads a lane has in flight
 constexpr uint32_t kZeroRows = 8;
 
+// Eight lanes search for a row's token together, nine parts a step.
 __device__ __forceinline__ void zero_rows(const u64 *keys, uint32_t B, uint64_t v0, uint32_t V, uint32_t cvec,
                                           f32x4 *dtable) {
-  const uint32_t lane = threadIdx.x & 63;
-  bool absent = false;
-  if (lane < kZeroRows && v0 + lane < V) {
-    const uint32_t at = first_place(keys, B, v0 + lane);
-    absent = at >= B || token_of(keys[at]) != v0 + lane;
+  static_assert(kZeroRows == 8, "eight lanes of a wave for each row");
+  const uint32_t lane = threadIdx.x & 63, s = lane & 7, shift = lane & 56;
+  const u64 token = v0 + (lane >> 3);
+  uint32_t lo = 0, len = B;  // [lo, lo + len] holds the first place not below the token
+  while (__any(len > 0)) {
+    const uint32_t part = (len + 8) / 9, at = lo + s * part + part - 1;
+    const bool probe = len > 0 && s * part + part <= len;
+    const uint32_t probes = (uint32_t)__builtin_popcountll((__ballot(probe) >> shift) & 0xff);
+    const bool below = probe && (keys[at] >> 32) < token;
+    const uint32_t found = (uint32_t)__builtin_popcountll((__ballot(below) >> shift) & 0xff);
+    lo += found * part;
+    len = len == 0 ? 0 : found == probes ? len - found * part : part - 1;
   }
-  uint32_t rows = (uint32_t)__ballot(absent);
+  const bool absent = s == 0 && token < V && (lo >= B || token_of(keys[lo]) != token);
+  u64 rows = __ballot(absent);
   while (rows) {
-    const uint64_t v = v0 + (uint32_t)__builtin_ctz(rows);
+    const uint64_t v = v0 + ((uint32_t)__builtin_ctzll(rows) >> 3);
     rows &= rows - 1;
     for (uint32_t c = threadIdx.x; c < 2 * cvec; c += kThreads)
       __builtin_nontemporal_store(f32x4{0.f, 0.f, 0.f, 0.f}, dtable + v * 2 * cvec + c);
@@ -345,8 +421,12 @@ hipError_t table_n(const EmbedBwdPlan &p, int64_t B, int64_t C, int64_t V, const
   hipError_t e;
   sort_tiles_kernel<<<(uint32_t)((B + kTile - 1) / kTile), kTile, 0, st>>>(tokens, rows, V, keys);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  for (uint64_t run = kTile; run < (uint64_t)B; run *= kJoin) {
-    join_runs_kernel<<<(uint32_t)((B + kThreads - 1) / kThreads), kThreads, 0, st>>>(keys, other, rows, run);
+  int log_run = 10;
+  for (uint64_t run = kTile; run < (uint64_t)B; run *= kJoin, log_run += 4) {
+    if (run == kTile)
+      join_tiles_kernel<<<(uint32_t)((B + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, st>>>(keys, other, rows);
+    else
+      join_runs_kernel<<<(uint32_t)((B + kThreads - 1) / kThreads), kThreads, 0, st>>>(keys, other, rows, run, log_run);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     std::swap(keys, other);
   }
@@ -379,7 +459,12 @@ hipError_t launch_embed(int n, int64_t B, int64_t C, int64_t V, const int64_t *t
 EmbedBwdPlan plan_embed_bwd(int64_t B, int64_t C) {
   EmbedBwdPlan p;
   const int64_t slices = (C + 511) / 512;
-  p.rb = B * slices >= 32 * 4096 ? 32 : 8;
+  // Long blocks where there are rows enough for one round of waves (4 on each
+  // SIMD of the 256 compute units), short ones for latency otherwise: at n=4,
+  // C=7168, B=16384 64 rows a block take 380 us, 32 397; 1001 rows of C=1000
+  // take 21 us with 8.
+  p.rb = 8;
+  while (p.rb < 64 && B * slices / p.rb > 4096) p.rb *= 2;
   const size_t list = ((size_t)B * 8 + 15) / 16 * 16;
   p.keys = 0;
   p.other = list;
