@@ -35,10 +35,9 @@ struct Tiles {
   static constexpr int N = NS * NS + 2 * NS;
   static constexpr int KS = (N + 31) / 32;      // 32-wide steps over the coefficients (dlogit . phi^T)
   static constexpr int MT = (N + 15) / 16;      // 16-row tiles of dphi^T
-  static constexpr int JW = NS == 8 ? 1 : NS;   // streams a wave forms dX and dphi of
+  static constexpr int JW = NS == 8 ? 2 : NS;   // streams a wave forms dX and dphi of
   static constexpr int GROUPS = NS / JW;        // waves that share a tile of rows and channels
-  static constexpr int HW = NS == 8 ? 2 : 1;    // 32-channel steps a wave
-  static constexpr int CW = 32 * HW;            // channels a wave
+  static constexpr int CW = 32;                 // channels a wave
   // What dx_dphi_kernel needs of a tile of 16 rows, written by coeffs_bwd_kernel
   // (byte offsets in the tile's record; every part is a multiple of 16):
   //   rows_b  [hi, mid][KS][lane][8] bf16  B operand of dlogit . phi^T: lane
@@ -104,8 +103,8 @@ __global__ __launch_bounds__(64 * W) void pre_dots_kernel(const void *__restrict
 // column (AXIS 1: lanes differ in i) of an n x n matrix, one element a lane
 // at lane i*n + j of an aligned group of n*n lanes; every lane of the row or
 // column gets the same bits (each step adds two values that its partner adds
-// too).  Lane moves inside rows of 16 lanes are DPP; n = 8 needs two wider
-// ones.
+// too).  Lane moves inside rows of 16 lanes are DPP; n = 8 swaps rows and
+// halves of the wave beside.
 __device__ __forceinline__ float dpp_add_ror8(float x) {  // lane ^ 8 in its row of 16
   return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xF, 0xF, false));
 }
@@ -119,8 +118,10 @@ __device__ __forceinline__ float axis_sum(float x) {
   if constexpr (NS == 4) return dpp_add_ror4(dpp_add_ror8(x));
   if constexpr (NS == 8) {
     x = dpp_add_ror8(x);
-    x += __shfl_xor(x, 16);
-    x += __shfl_xor(x, 32);
+    const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
+    const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
   }
   return x;
 }
@@ -378,20 +379,19 @@ struct Stage {
   static constexpr int kStages = NS == 4 ? 2 : 3;
   static constexpr int kDist = kStages - 1;
   // Bytes of a stage: G, X_t, dF_pre, scale bytes (a dword each).
-  static constexpr int kG = kAlong * T::HW * NS * 1024;
-  static constexpr int kX = kWaves * T::JW * T::HW * (CK ? 512 : 1024);
-  static constexpr int kF = kAlong * T::HW * 1024;
+  static constexpr int kG = kAlong * NS * 1024;
+  static constexpr int kX = kWaves * T::JW * (CK ? 512 : 1024);
+  static constexpr int kF = kAlong * 1024;
   static constexpr int kS = CK ? kWaves * 256 : 0;
   static constexpr int kBytes = kG + kX + kF + kS;
   // dX takes the place of G in LDS (a wave's own columns of it), or where G is
   // shared that of X_t, or (from codes) a place of its own.
   static constexpr bool kOwnOut = kShared && CK;
-  static constexpr int kOutBytes = kOwnOut ? kWaves * T::HW * 1024 : 16;
+  static constexpr int kOutBytes = kOwnOut ? kWaves * T::JW * 1024 : 16;
   // Loads a wave issues for a tile at least (without its share of the record),
   // and its stores of a tile: what may be younger than a tile's loads.
-  static constexpr int kLoads = kShared ? T::HW + (CK ? 1 + 1 : T::HW)
-                                        : NS + 1 + (CK ? T::JW / 2 + 1 : T::JW);
-  static constexpr int kStores = T::JW * T::HW;
+  static constexpr int kLoads = (kShared ? T::JW : NS + 1) + (CK ? T::JW / 2 + 1 : T::JW);
+  static constexpr int kStores = T::JW;
   static constexpr int kYounger = kDist == 1 ? kStores : 2 * kStores + kLoads;
 };
 
@@ -402,7 +402,7 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     float *__restrict__ out, uint32_t B, uint32_t cvec, uint32_t blocks, uint32_t slices, int wc) {
   using T = Tiles<NS>;
   using S = Stage<NS, CK>;
-  constexpr int N = T::N, KS = T::KS, MT = T::MT, JW = T::JW, GROUPS = T::GROUPS, HW = T::HW;
+  constexpr int N = T::N, KS = T::KS, MT = T::MT, JW = T::JW, GROUPS = T::GROUPS;
   __shared__ __attribute__((aligned(1024))) char stage[S::kStages][S::kBytes];
   __shared__ __attribute__((aligned(1024))) char record[S::kStages][T::kStride];
   __shared__ __attribute__((aligned(1024))) char own_out[S::kOutBytes];
@@ -410,8 +410,8 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
   // wc waves along the channels, GROUPS along the streams.
   const int cw = wave / GROUPS, group = wave % GROUPS, waves = wc * GROUPS;
   const uint32_t slice = blockIdx.x % slices, range = blockIdx.x / slices, split = gridDim.x / slices;
-  const uint32_t v_wg = slice * (uint32_t)wc * (HW * 4);  // the workgroup's first vector of eight channels
-  const uint32_t v_wave = v_wg + cw * (HW * 4);
+  const uint32_t v_wg = slice * (uint32_t)wc * 4;  // the workgroup's first vector of eight channels
+  const uint32_t v_wave = v_wg + cw * 4;
   const int lo16 = lane & 15, q = lane >> 4, j0 = group * JW;
   // Its tiles: every `split`th, from `range` on, so that all workgroups move
   // through the rows together (with a run of rows each, 14 us slower at n=4,
@@ -423,68 +423,52 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
   // A stream's tile in LDS: 16 rows of 1 << lg 16-byte pieces, piece p of row
   // r at p ^ turn(r, lg): reads of one piece of every row meet 16 different
   // places of the 256 bytes that the banks span.
-  const int lg = __builtin_ctz(wc) + (HW == 2 ? 3 : 2);
+  const int lg = __builtin_ctz(wc) + 2;
   const auto turn = [](int row, int l) { return l >= 4 ? row : (row >> (4 - l)) & ((1 << l) - 1); };
   const auto piece_of = [&](int row, int p, int l) { return ((row << l) + (p ^ turn(row, l))) * 16; };
 
   const auto issue = [&](uint32_t tile, int st) {
     const char *zero = reinterpret_cast<const char *>(g_train_zero);
     const uint32_t at = lds_addr_of(stage[st]), row0 = tile * 16;
-    // bf16 tiles: KiB `part` of a stream's
-    const auto offset = [&](int part, bool &in) -> size_t {
-      const int at_lane = part * 64 + lane, r = at_lane >> lg, p = (at_lane & ((1 << lg) - 1)) ^ turn(r, lg);
-      const uint32_t row = row0 + r, v = v_wg + p;
-      in = row < B && v < cvec;
-      return ((size_t)row * NS * cvec + v) * 16;
-    };
-    const int kib = 256 << lg;  // bytes of a stream's tile
+    // bf16 tiles: KiB cw of a stream's.
+    const int at_lane = cw * 64 + lane, r = at_lane >> lg, p = (at_lane & ((1 << lg) - 1)) ^ turn(r, lg);
+    const uint32_t row = row0 + r, v = v_wg + p, kib = 256u << lg;  // (bytes of a stream's tile)
+    const bool in = row < B && v < cvec;
+    const size_t o = ((size_t)row * NS * cvec + v) * 16;
 #pragma unroll
-    for (int h = 0; h < HW; ++h) {
-      const int part = S::kShared ? h : cw;
-      bool in;
-      const size_t o = offset(part, in);
-      if constexpr (!S::kShared) {
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-          dma<16>(in ? G + o + (size_t)i * row_bytes : zero, at + i * kib + part * 1024);
-      } else {
-        dma<16>(in ? G + o + (size_t)group * row_bytes : zero, at + group * kib + part * 1024);
-      }
-      if (!S::kShared || group == h) {
-        const int at_lane = part * 64 + lane, r = at_lane >> lg, p = (at_lane & ((1 << lg) - 1)) ^ turn(r, lg);
-        dma<16>(in ? dF + (size_t)(row0 + r) * row_bytes + (size_t)(v_wg + p) * 16 : zero,
-                at + S::kG + S::kX + part * 1024);
-      }
-      if constexpr (!CK) {
-#pragma unroll
-        for (int jj = 0; jj < JW; ++jj)
-          dma<16>(in ? X + o + (size_t)(j0 + jj) * row_bytes : zero, at + S::kG + (j0 + jj) * kib + part * 1024);
-      }
+    for (int k = 0; k < (S::kShared ? JW : NS); ++k) {
+      const int i = S::kShared ? j0 + k : k;
+      dma<16>(in ? G + o + (size_t)i * row_bytes : zero, at + i * kib + cw * 1024);
     }
-    if constexpr (CK) {
+    if (!S::kShared || group == 0)
+      dma<16>(in ? dF + (size_t)row * row_bytes + (size_t)v * 16 : zero, at + S::kG + S::kX + cw * 1024);
+    if constexpr (!CK) {
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj)
+        dma<16>(in ? X + o + (size_t)(j0 + jj) * row_bytes : zero, at + S::kG + (j0 + jj) * kib + cw * 1024);
+    } else {
       // Codes: the same with rows of half as many pieces; 16 bytes a lane
       // where a stream's codes are that aligned, else four.
       const size_t stream = (size_t)cvec * 8;
-      const int lc = lg - 1, bytes = 256 << lc, all = S::kShared ? bytes : JW * bytes;
-      const uint32_t x_at = at + S::kG + (S::kShared ? group * bytes : 0);
+      const int lc = lg - 1, all = JW * 256 << lc;
+      const uint32_t x_at = at + S::kG + (j0 * 256 << lc);
       const auto code = [&](int byte) -> const char * {
-        const int jj = byte >> (8 + lc), r = (byte >> (4 + lc)) & 15;
-        const int p = ((byte >> 4) & ((1 << lc) - 1)) ^ turn(r, lc);
-        const uint32_t row = row0 + r, ch = v_wg * 8 + p * 16 + (byte & 15);
-        return row < B && ch < cvec * 8 ? X + ((size_t)row * NS + j0 + jj) * stream + ch : zero;
+        const int jj = byte >> (8 + lc), cr = (byte >> (4 + lc)) & 15;
+        const int cp = ((byte >> 4) & ((1 << lc) - 1)) ^ turn(cr, lc);
+        const uint32_t code_row = row0 + cr, ch = v_wg * 8 + cp * 16 + (byte & 15);
+        return code_row < B && ch < cvec * 8 ? X + ((size_t)code_row * NS + j0 + jj) * stream + ch : zero;
       };
       if (cvec % 2 == 0) {
-        for (int b = (S::kShared ? 0 : cw) * 1024; b < all; b += (S::kShared ? 1 : wc) * 1024)
+        for (int b = cw * 1024; b < all; b += wc * 1024)
           if (b + lane * 16 < all) dma<16>(code(b + lane * 16), x_at + b);
       } else {
-        for (int b = (S::kShared ? 0 : cw) * 256; b < all; b += (S::kShared ? 1 : wc) * 256)
-          dma<4>(code(b + lane * 4), x_at + b);
+        for (int b = cw * 256; b < all; b += wc * 256) dma<4>(code(b + lane * 4), x_at + b);
       }
-      // One scale byte for each row and stream (n = 8: row and step).
-      const uint32_t row = row0 + lo16, v = v_wave + (S::kShared ? q * 4 : 0);
-      const int j = S::kShared ? j0 : q;
-      const bool in = row < B && v < cvec && (S::kShared ? q < HW : q < JW);
-      dma<1>(in ? reinterpret_cast<const char *>(scales) + ((size_t)row * NS + j) * blocks + (v >> 2) : zero,
+      // One scale byte for each row and stream.
+      const uint32_t s_row = row0 + lo16;
+      dma<1>(s_row < B && v_wave < cvec && q < JW
+                 ? reinterpret_cast<const char *>(scales) + ((size_t)s_row * NS + j0 + q) * blocks + (v_wave >> 2)
+                 : zero,
              at + S::kG + S::kX + S::kF + (uint32_t)wave * 256);
     }
     for (int k = wave; k < T::kChunks; k += waves)
@@ -494,52 +478,48 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
   for (int k = 0; k < S::kDist; ++k)
     if ((uint32_t)k < count) issue(tile_at(k), k);
 
-  // phi: operand (stream, step h, t, ks), lane 16 q + m: coefficients
-  // 32 ks + 8 q .. + 7 of channel 32 h + 8 (m / 4) + 4 t + m % 4 of the wave.
-  bf16x8 pa[JW][HW][2][KS];
+  // phi: operand (stream, t, ks), lane 16 q + m: coefficients 32 ks + 8 q .. + 7
+  // of the wave's channel 8 (m / 4) + 4 t + m % 4.
+  bf16x8 pa[JW][2][KS];
 #pragma unroll
   for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
-    for (int h = 0; h < HW; ++h)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t v = v_wave + (lo16 >> 2);
+        const int k0 = 32 * ks + 8 * q;
+        u32x4 a = {0u, 0u, 0u, 0u};
+        if (v < cvec && k0 < N) {
+          const size_t at = ((size_t)(j0 + jj) * cvec * 8 + (size_t)v * 8 + 4 * t + (lo16 & 3)) * N + k0;
+          if constexpr (N % 8 == 0) {
+            a = load16(phi + at);
+          } else {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t v = v_wave + h * 4 + (lo16 >> 2);
-          const int k0 = 32 * ks + 8 * q;
-          u32x4 a = {0u, 0u, 0u, 0u};
-          if (v < cvec && k0 < N) {
-            const size_t at = ((size_t)(j0 + jj) * cvec * 8 + (size_t)v * 8 + 4 * t + (lo16 & 3)) * N + k0;
-            if constexpr (N % 8 == 0) {
-              a = load16(phi + at);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (k0 + k < N) a[k / 2] |= (uint32_t)phi[at + k] << (16 * (k & 1));
-            }
+            for (int k = 0; k < 8; ++k)
+              if (k0 + k < N) a[k / 2] |= (uint32_t)phi[at + k] << (16 * (k & 1));
           }
-          pa[jj][h][t][ks] = __builtin_bit_cast(bf16x8, a);
         }
+        pa[jj][t][ks] = __builtin_bit_cast(bf16x8, a);
+      }
   // Selections: channels 16 s .. 16 s + 15 of the 32.
   s16x8 sel[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sel[s][j] = 8 * q + j == 16 * s + lo16 ? (short)0x3f80 : (short)0;
-  f32x4 acc[JW][HW][2][MT];
+  f32x4 acc[JW][2][MT];
 #pragma unroll
   for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
-    for (int h = 0; h < HW; ++h)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) acc[jj][h][s][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int mt = 0; mt < MT; ++mt) acc[jj][s][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   // Where all of the wave's pieces have channels, every store is issued each
   // tile.
-  const bool full = v_wave + HW * 4 <= cvec;
+  const bool full = v_wave + 4 <= cvec;
   int st = 0;  // the tile's stage
   for (uint32_t k = 0; k < count; ++k) {
     const uint32_t tile = tile_at(k);
@@ -553,20 +533,9 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     if (k + S::kDist < count) issue(tile_at(k + S::kDist), st == 0 ? S::kStages - 1 : st - 1);
     char *mine = stage[st];
     const char *now = record[st];
-    char *const o_at = S::kOwnOut ? own_out + wave * (HW * 1024) : S::kShared ? mine + S::kG + (j0 * 256 << lg) : mine;
     st = st + 1 == S::kStages ? 0 : st + 1;
-    const char *const f_at = mine + S::kG + S::kX, *const s_at = f_at + S::kF + wave * 256;
-    const auto x_of = [&](int h, int jj) -> u32x4 {
-      if constexpr (CK) {
-        const int lc = lg - 1, p = (cw * HW + h) * 2 + (q >> 1);
-        const char *x = mine + S::kG + ((j0 + jj) * 256 << lc) + piece_of(lo16, p, lc) + (q & 1) * 8;
-        return held_bf16(*reinterpret_cast<const u32x2 *>(x),
-                         (int)reinterpret_cast<const uint32_t *>(s_at)[(S::kShared ? h : jj) * 16 + lo16]);
-      } else {
-        return *reinterpret_cast<const u32x4 *>(mine + S::kG + ((j0 + jj) * 256 << lg) +
-                                                piece_of(lo16, (cw * HW + h) * 4 + q, lg));
-      }
-    };
+    const char *const f_at = mine + S::kG + S::kX;
+    const uint32_t *const s_at = reinterpret_cast<const uint32_t *>(f_at + S::kF + wave * 256);
     bf16x8 bh[KS], bm[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -577,85 +546,90 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     const float c = reinterpret_cast<const float *>(now + T::kTurn)[lo16];
     const bf16x8 *cols_a = reinterpret_cast<const bf16x8 *>(now + T::kColsA) + lane;
     const u32x2 *cols_c = reinterpret_cast<const u32x2 *>(now + T::kColsC) + lane;
-    bf16x8 twice[JW][HW][2];
+    const int at = piece_of(lo16, cw * 4 + q, lg);
+    u32x4 x[JW];
 #pragma unroll
-    for (int h = 0; h < HW; ++h) {
-      u32x4 x[JW];
+    for (int jj = 0; jj < JW; ++jj) {
+      if constexpr (CK) {
+        const char *codes = mine + S::kG + ((j0 + jj) * 256 << (lg - 1)) + piece_of(lo16, cw * 2 + (q >> 1), lg - 1);
+        x[jj] = held_bf16(*reinterpret_cast<const u32x2 *>(codes + (q & 1) * 8), (int)s_at[jj * 16 + lo16]);
+      } else {
+        x[jj] = *reinterpret_cast<const u32x4 *>(mine + S::kG + ((j0 + jj) * 256 << lg) + at);
+      }
+    }
+    float o[JW][8];
 #pragma unroll
-      for (int jj = 0; jj < JW; ++jj) x[jj] = x_of(h, jj);
-      const int at = piece_of(lo16, (cw * HW + h) * 4 + q, lg);
-      float o[JW][8];
+    for (int jj = 0; jj < JW; ++jj) {
+      f32x4 d[2] = {zero, zero};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pa[jj][t][ks], bm[ks], d[t], 0, 0, 0);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pa[jj][t][ks], bh[ks], d[t], 0, 0, 0);
+      float xw[8];
+      widen8(x[jj], xw);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(c, xw[e], d[e >> 2][e & 3]);
+    }
+    {
+      float fw[8];
+      widen8(*reinterpret_cast<const u32x4 *>(f_at + at), fw);
 #pragma unroll
       for (int jj = 0; jj < JW; ++jj) {
-        f32x4 d[2] = {zero, zero};
+        const float hpre = mix[(j0 + jj) * 16];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pa[jj][h][t][ks], bm[ks], d[t], 0, 0, 0);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pa[jj][h][t][ks], bh[ks], d[t], 0, 0, 0);
-        float xw[8];
-        widen8(x[jj], xw);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(c, xw[e], d[e >> 2][e & 3]);
+        for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hpre, fw[e], o[jj][e]);
       }
-      {
-        float fw[8];
-        widen8(*reinterpret_cast<const u32x4 *>(f_at + at), fw);
-#pragma unroll
-        for (int jj = 0; jj < JW; ++jj) {
-          const float hpre = mix[(j0 + jj) * 16];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hpre, fw[e], o[jj][e]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        float gw[8];
-        widen8(*reinterpret_cast<const u32x4 *>(mine + (i * 256 << lg) + at), gw);
-#pragma unroll
-        for (int jj = 0; jj < JW; ++jj) {
-          const float hres = mix[(NS + i * NS + j0 + jj) * 16];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hres, gw[e], o[jj][e]);
-        }
-      }
-#pragma unroll
-      for (int jj = 0; jj < JW; ++jj)
-        *reinterpret_cast<u32x4 *>(o_at + (jj * 256 << lg) + at) =
-            u32x4{pack_bf16x2(o[jj][0], o[jj][1]), pack_bf16x2(o[jj][2], o[jj][3]), pack_bf16x2(o[jj][4], o[jj][5]),
-                  pack_bf16x2(o[jj][6], o[jj][7])};
-#pragma unroll
-      for (int jj = 0; jj < JW; ++jj)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const f32x4 m = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, x[jj]), __builtin_bit_cast(bf16x8, sel[s]), zero, 0, 0, 0);
-          const uint32_t p0 = pack_bf16x2(m[0], m[1]), p1 = pack_bf16x2(m[2], m[3]);
-          twice[jj][h][s] = __builtin_bit_cast(bf16x8, u32x4{p0, p1, p0, p1});
-        }
     }
-    // dX in memory order.  The wave's own pieces only: 64 bytes a row (128 at
-    // n = 8); storing whole rows of the workgroup's after another barrier
-    // measured 15 us slower at n=4, C=7168, B=16384.
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      float gw[8];
+      widen8(*reinterpret_cast<const u32x4 *>(mine + (i * 256 << lg) + at), gw);
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj) {
+        const float hres = mix[(NS + i * NS + j0 + jj) * 16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[jj][e] = fmaf(hres, gw[e], o[jj][e]);
+      }
+    }
+    // dX out in memory order, the wave's own pieces: 64 bytes of a row a store
+    // (whole rows of the workgroup's, after another barrier, measured 15 us
+    // slower at n=4, C=7168, B=16384).
+    char *const o_at = S::kOwnOut ? own_out + wave * (JW * 1024) : S::kShared ? mine + S::kG + (j0 * 256 << lg) : mine;
+    const int ol = S::kOwnOut ? 2 : lg, ow = S::kOwnOut ? 0 : cw * 4;  // pieces of a row there, the wave's first
+    const int o_write = S::kOwnOut ? piece_of(lo16, q, 2) : at;
+    const int mr = lane >> 2, mp = (lane & 3) ^ (turn(mr, ol) & 3), o_read = piece_of(mr, ow + mp, ol);
+#pragma unroll
+    for (int jj = 0; jj < JW; ++jj)
+      *reinterpret_cast<u32x4 *>(o_at + (jj * 256 << ol) + o_write) =
+          u32x4{pack_bf16x2(o[jj][0], o[jj][1]), pack_bf16x2(o[jj][2], o[jj][3]), pack_bf16x2(o[jj][4], o[jj][5]),
+                pack_bf16x2(o[jj][6], o[jj][7])};
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int h = 0; h < HW; ++h) {
-      constexpr int kRow = 4 * HW;  // the wave's pieces of a row
-      const int r = (h * 64 + lane) / kRow, p = cw * kRow + ((lane & (kRow - 1)) ^ (turn(r, lg) & (kRow - 1)));
-      const uint32_t row = tile * 16 + r, v = v_wg + p;
+    {
+      const uint32_t row = tile * 16 + mr, v = v_wave + mp;
       char *const dst = dX + ((size_t)row * NS + j0) * row_bytes + (size_t)v * 16;
       u32x4 y[JW];
 #pragma unroll
-      for (int jj = 0; jj < JW; ++jj) y[jj] = *reinterpret_cast<const u32x4 *>(o_at + (jj * 256 << lg) + piece_of(r, p, lg));
+      for (int jj = 0; jj < JW; ++jj) y[jj] = *reinterpret_cast<const u32x4 *>(o_at + (jj * 256 << ol) + o_read);
       if (row < B && v < cvec) {
 #pragma unroll
         for (int jj = 0; jj < JW; ++jj) *reinterpret_cast<u32x4 *>(dst + (size_t)jj * row_bytes) = y[jj];
       }
     }
+    bf16x8 twice[JW][2];
+#pragma unroll
+    for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const f32x4 m = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, x[jj]), __builtin_bit_cast(bf16x8, sel[s]), zero, 0, 0, 0);
+        const uint32_t p0 = pack_bf16x2(m[0], m[1]), p1 = pack_bf16x2(m[2], m[3]);
+        twice[jj][s] = __builtin_bit_cast(bf16x8, u32x4{p0, p1, p0, p1});
+      }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const u32x2 low = cols_c[mt * 64];
@@ -663,45 +637,39 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
 #pragma unroll
       for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
-        for (int h = 0; h < HW; ++h)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cc, twice[jj][h][s], acc[jj][h][s][mt], 0, 0, 0);
+        for (int s = 0; s < 2; ++s)
+          acc[jj][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cc, twice[jj][s], acc[jj][s][mt], 0, 0, 0);
 #pragma unroll
       for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
-        for (int h = 0; h < HW; ++h)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            acc[jj][h][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ca, twice[jj][h][s], acc[jj][h][s][mt], 0, 0, 0);
+        for (int s = 0; s < 2; ++s)
+          acc[jj][s][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ca, twice[jj][s], acc[jj][s][mt], 0, 0, 0);
     }
   }
 
-  // Lane 16 q + c of acc[jj][h][s][mt]: coefficients 16 mt + 4 q .. + 3 of
-  // the wave's channel 32 h + 16 s + c.
+  // Lane 16 q + c of acc[jj][s][mt]: coefficients 16 mt + 4 q .. + 3 of the
+  // wave's channel 16 s + c.
   float *po = out + (size_t)range * NS * cvec * 8 * N;
 #pragma unroll
-  for (int h = 0; h < HW; ++h)
+  for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
-    for (int jj = 0; jj < JW; ++jj)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int mt = 0; mt < MT; ++mt) {
+        const f32x4 a = acc[jj][s][mt];
+        const uint32_t ch = v_wave * 8 + 16 * s + lo16;
+        const int k = 16 * mt + 4 * q;
+        if (ch < cvec * 8 && k < N) {
+          float *p = po + ((size_t)(j0 + jj) * cvec * 8 + ch) * N + k;
+          if constexpr (N % 4 == 0) {
+            *reinterpret_cast<f32x4 *>(p) = a;
+          } else {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const f32x4 a = acc[jj][h][s][mt];
-          const uint32_t ch = v_wave * 8 + 32 * h + 16 * s + lo16;
-          const int k = 16 * mt + 4 * q;
-          if (ch < cvec * 8 && k < N) {
-            float *p = po + ((size_t)(j0 + jj) * cvec * 8 + ch) * N + k;
-            if constexpr (N % 4 == 0) {
-              *reinterpret_cast<f32x4 *>(p) = a;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (k + e < N) p[e] = a[e];
-            }
+            for (int e = 0; e < 4; ++e)
+              if (k + e < N) p[e] = a[e];
           }
         }
+      }
 }
 
 // The last joins.  Workgroups below N + 3: a sum of db or dalpha each, from
