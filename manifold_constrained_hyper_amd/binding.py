@@ -7,6 +7,7 @@ fallback: if the library is missing or fails to load, every call raises.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -520,15 +521,15 @@ def _device():
     return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
 
 
-def _dev_ptrs(dev, *tensors):
-    """_ptr of every (tensor, bytes, element size, name), and ValueError where
-    a device tensor is not on device `dev`, the current one (the kernels would
-    run on another device than the tensor's)."""
+def _dev_ptrs(dev, tensors, sizes):
+    """_ptr of every tensor with its (bytes, element size, name), and
+    ValueError where a device tensor is not on device `dev`, the current one
+    (the kernels would run on another device than the tensor's)."""
     out = []
-    for t, nbytes, esize, name in tensors:
+    for t, (nbytes, esize, name) in zip(tensors, sizes):
         # What nearly every tensor is, decided in a few attribute reads.
-        if (type(t) is torch.Tensor and t.is_cuda and t.get_device() == dev and t.is_contiguous()
-                and t.itemsize == esize and t.nbytes >= nbytes):
+        if (type(t) is torch.Tensor and t.get_device() == dev and dev >= 0 and t.is_contiguous()
+                and (t.itemsize == esize or esize is None) and t.nbytes >= nbytes):
             out.append(t.data_ptr() or None)
             continue
         p = _ptr(t, nbytes, esize, name)
@@ -549,17 +550,45 @@ def mhc_ckpt_scales_per_row(n, C):
     return int(load().mhc_ckpt_scales_per_row(int(n), int(C)))
 
 
-def _held(B, n, C, codes, scales):
-    rows = max(B, 0)
-    return ((codes, rows * n * C, 1, "codes"), (scales, rows * n * -(-C // 32), 1, "scales"))
+# What each call's tensors have to be, in their order: (bytes, element size,
+# name).  They depend on the sizes alone and are worked out once for each.
+
+def _x_sizes(B, n, C, ckpt):
+    return (((B * n * C, 1, "codes"), (B * n * -(-C // 32), 1, "scales")) if ckpt else ((B * n * C * 2, 2, "X_t"),))
+
+
+@functools.lru_cache(maxsize=256)
+def _ckpt_sizes(B, n, C, pack):
+    x, held = (_x_sizes(max(B, 0), n, C, ckpt) for ckpt in (False, True))
+    return x + held if pack else held + x
+
+
+@functools.lru_cache(maxsize=256)
+def _post_res_bwd_sizes(B, n, C, ckpt):
+    B, N = max(B, 0), n * n + 2 * n
+    return _x_sizes(B, n, C, ckpt) + (
+        (B * C * 2, 2, "F_out"), (B * N * 4, 4, "H"), (B * n * C * 2, 2, "dX_next"), (B * C * 2, 2, "dF_out"),
+        (B * N * 4, 4, "dH"))
+
+
+@functools.lru_cache(maxsize=256)
+def _coeffs_pre_bwd_sizes(B, n, C, ckpt):
+    B, N = max(B, 0), n * n + 2 * n
+    some = 1 if B > 0 else 0  # at B == 0 only the parameters' gradients are touched
+    return _x_sizes(B, n, C, ckpt) + (
+        (some * n * C * N * 2, 2, "phi"), (some * n * 4, 4, "b_pre"), (some * n * 4, 4, "b_post"),
+        (some * n * n * 4, 4, "b_res"), (B * N * 4, 4, "logits"), (B * 4, 4, "r"), (B * N * 4, 4, "H"),
+        (B * n * C * 2, 2, "dX_next"), (B * N * 4, 4, "dH"), (B * C * 2, 2, "dF_pre"), (B * n * C * 2, 2, "dX_t"),
+        (n * C * N * 4, 4, "dphi"), (12, 4, "dalpha"), (n * 4, 4, "db_pre"), (n * 4, 4, "db_post"),
+        (n * n * 4, 4, "db_res"))
 
 
 def mhc_ckpt_pack(B, n, C, X_t, codes, scales, stream=None, check=True):
     """The 8-bit checkpoint of X_t: codes (E4M3 or uint8 [B, n*C]) and scales
     (uint8 [B, mhc_ckpt_scales_per_row(n, C)]); see include/mhc.h."""
     B, n, C, dev = int(B), int(n), int(C), _device()
-    st = load().mhc_ckpt_pack(B, n, C, *_dev_ptrs(dev, (X_t, max(B, 0) * n * C * 2, 2, "X_t"),
-                                                  *_held(B, n, C, codes, scales)), _dev_stream(stream, dev))
+    st = load().mhc_ckpt_pack(B, n, C, *_dev_ptrs(dev, (X_t, codes, scales), _ckpt_sizes(B, n, C, True)),
+                              _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_ckpt_pack")
     return st
@@ -568,18 +597,17 @@ def mhc_ckpt_pack(B, n, C, X_t, codes, scales, stream=None, check=True):
 def mhc_ckpt_unpack(B, n, C, codes, scales, X_t, stream=None, check=True):
     """X_t in bf16 from its checkpoint (see include/mhc.h)."""
     B, n, C, dev = int(B), int(n), int(C), _device()
-    st = load().mhc_ckpt_unpack(B, n, C, *_dev_ptrs(dev, *_held(B, n, C, codes, scales),
-                                                    (X_t, max(B, 0) * n * C * 2, 2, "X_t")), _dev_stream(stream, dev))
+    st = load().mhc_ckpt_unpack(B, n, C, *_dev_ptrs(dev, (codes, scales, X_t), _ckpt_sizes(B, n, C, False)),
+                                _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_ckpt_unpack")
     return st
 
 
 def _post_res_bwd(fn, name, held, B, n, C, F_out, H, dX_next, dF_out, dH, stream, check):
-    dev, rows, coef = _device(), max(B, 0), max(B, 0) * (n * n + 2 * n) * 4
-    st = fn(B, n, C, *_dev_ptrs(dev, *held, (F_out, rows * C * 2, 2, "F_out"), (H, coef, 4, "H"),
-                                (dX_next, rows * n * C * 2, 2, "dX_next"), (dF_out, rows * C * 2, 2, "dF_out"),
-                                (dH, coef, 4, "dH")), _dev_stream(stream, dev))
+    B, n, C, dev = int(B), int(n), int(C), _device()
+    st = fn(B, n, C, *_dev_ptrs(dev, (*held, F_out, H, dX_next, dF_out, dH),
+                                _post_res_bwd_sizes(B, n, C, len(held) == 2)), _dev_stream(stream, dev))
     if check:
         _check(st, name)
     return st
@@ -587,38 +615,27 @@ def _post_res_bwd(fn, name, held, B, n, C, F_out, H, dX_next, dF_out, dH, stream
 
 def mhc_post_res_bwd(B, n, C, X_t, F_out, H, dX_next, dF_out, dH, stream=None, check=True):
     """Gradients of step (4b) with respect to F_out and H (see include/mhc.h)."""
-    B, n, C = int(B), int(n), int(C)
-    return _post_res_bwd(load().mhc_post_res_bwd, "mhc_post_res_bwd", ((X_t, max(B, 0) * n * C * 2, 2, "X_t"),), B, n,
-                         C, F_out, H, dX_next, dF_out, dH, stream, check)
+    return _post_res_bwd(load().mhc_post_res_bwd, "mhc_post_res_bwd", (X_t,), B, n, C, F_out, H, dX_next, dF_out, dH,
+                         stream, check)
 
 
 def mhc_post_res_bwd_ckpt(B, n, C, codes, scales, F_out, H, dX_next, dF_out, dH, stream=None, check=True):
     """mhc_post_res_bwd with X_t as its checkpoint (see include/mhc.h)."""
-    B, n, C = int(B), int(n), int(C)
-    return _post_res_bwd(load().mhc_post_res_bwd_ckpt, "mhc_post_res_bwd_ckpt", _held(B, n, C, codes, scales), B, n, C,
-                         F_out, H, dX_next, dF_out, dH, stream, check)
+    return _post_res_bwd(load().mhc_post_res_bwd_ckpt, "mhc_post_res_bwd_ckpt", (codes, scales), B, n, C, F_out, H,
+                         dX_next, dF_out, dH, stream, check)
 
 
 def mhc_coeffs_pre_bwd_workspace_size(B, n, C):
     return int(load().mhc_coeffs_pre_bwd_workspace_size(int(B), int(n), int(C)))
 
 
-def _coeffs_pre_bwd(fn, name, held, B, n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res, logits, r,
-                    H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace, workspace_bytes,
-                    stream, check):
-    dev, rows, N = _device(), max(B, 0), n * n + 2 * n
+def _coeffs_pre_bwd(fn, name, held, B, n, C, alphas, tensors, workspace, workspace_bytes, stream, check):
+    B, n, C, dev = int(B), int(n), int(C), _device()
+    p = _dev_ptrs(dev, (*held, *tensors), _coeffs_pre_bwd_sizes(B, n, C, len(held) == 2))
     wb = _ws_bytes(workspace, workspace_bytes)
-    some = B > 0  # at B == 0 only the parameters' gradients are touched
-    p = _dev_ptrs(dev, *held, (phi, n * C * N * 2 if some else 0, 2, "phi"), (b_pre, n * 4 if some else 0, 4, "b_pre"),
-                  (b_post, n * 4 if some else 0, 4, "b_post"), (b_res, n * n * 4 if some else 0, 4, "b_res"),
-                  (logits, rows * N * 4, 4, "logits"), (r, rows * 4, 4, "r"), (H, rows * N * 4, 4, "H"),
-                  (dX_next, rows * n * C * 2, 2, "dX_next"), (dH, rows * N * 4, 4, "dH"),
-                  (dF_pre, rows * C * 2, 2, "dF_pre"), (dX_t, rows * n * C * 2, 2, "dX_t"),
-                  (dphi, n * C * N * 4, 4, "dphi"), (dalpha, 12, 4, "dalpha"), (db_pre, n * 4, 4, "db_pre"),
-                  (db_post, n * 4, 4, "db_post"), (db_res, n * n * 4, 4, "db_res"), (workspace, wb, None, "workspace"))
+    p += _dev_ptrs(dev, (workspace,), ((wb, None, "workspace"),))
     k = len(held) + 1  # the alphas follow phi
-    st = fn(B, n, C, *p[:k], float(alpha_pre), float(alpha_post), float(alpha_res), *p[k:], wb,
-            _dev_stream(stream, dev))
+    st = fn(B, n, C, *p[:k], *alphas, *p[k:], wb, _dev_stream(stream, dev))
     if check:
         _check(st, name)
     return st
@@ -628,31 +645,28 @@ def mhc_coeffs_pre_bwd(B, n, C, X_t, phi, alpha_pre, alpha_post, alpha_res, b_pr
                        dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace,
                        workspace_bytes=None, stream=None, check=True):
     """Gradients of steps (1)-(4a) and of X_t through the apply (see include/mhc.h)."""
-    B, n, C = int(B), int(n), int(C)
-    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd, "mhc_coeffs_pre_bwd", ((X_t, max(B, 0) * n * C * 2, 2, "X_t"),),
-                           B, n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res, logits, r, H, dX_next,
-                           dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace, workspace_bytes, stream,
-                           check)
+    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd, "mhc_coeffs_pre_bwd", (X_t,), B, n, C,
+                           (float(alpha_pre), float(alpha_post), float(alpha_res)),
+                           (phi, b_pre, b_post, b_res, logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre,
+                            db_post, db_res), workspace, workspace_bytes, stream, check)
 
 
 def mhc_coeffs_pre_bwd_ckpt(B, n, C, codes, scales, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res,
                             logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res,
                             workspace, workspace_bytes=None, stream=None, check=True):
     """mhc_coeffs_pre_bwd with X_t as its checkpoint (see include/mhc.h)."""
-    B, n, C = int(B), int(n), int(C)
-    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd_ckpt, "mhc_coeffs_pre_bwd_ckpt", _held(B, n, C, codes, scales), B,
-                           n, C, phi, alpha_pre, alpha_post, alpha_res, b_pre, b_post, b_res, logits, r, H, dX_next,
-                           dH, dF_pre, dX_t, dphi, dalpha, db_pre, db_post, db_res, workspace, workspace_bytes, stream,
-                           check)
+    return _coeffs_pre_bwd(load().mhc_coeffs_pre_bwd_ckpt, "mhc_coeffs_pre_bwd_ckpt", (codes, scales), B, n, C,
+                           (float(alpha_pre), float(alpha_post), float(alpha_res)),
+                           (phi, b_pre, b_post, b_res, logits, r, H, dX_next, dH, dF_pre, dX_t, dphi, dalpha, db_pre,
+                            db_post, db_res), workspace, workspace_bytes, stream, check)
 
 
 def mhc_embed(B, n, C, V, tokens, table, scale, X_0, stream=None, check=True):
     """X_0: the scaled embeddings of the tokens (int64) in every stream (see include/mhc.h)."""
     B, n, C, V, dev = int(B), int(n), int(C), int(V), _device()
     rows = max(B, 0)
-    tokens, table, X_0 = _dev_ptrs(dev, (tokens, rows * 8, 8, "tokens"),
-                                   (table, max(V, 0) * C * 2 if B > 0 else 0, 2, "table"),
-                                   (X_0, rows * n * C * 2, 2, "X_0"))
+    tokens, table, X_0 = _dev_ptrs(dev, (tokens, table, X_0), (
+        (rows * 8, 8, "tokens"), (max(V, 0) * C * 2 if B > 0 else 0, 2, "table"), (rows * n * C * 2, 2, "X_0")))
     st = load().mhc_embed(B, n, C, V, tokens, table, float(scale), X_0, _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_embed")
@@ -669,10 +683,9 @@ def mhc_embed_bwd(B, n, C, V, tokens, dX_0, scale, dtable, workspace, accumulate
     accumulate, added to (see include/mhc.h)."""
     B, n, C, V, dev = int(B), int(n), int(C), int(V), _device()
     rows, wb = max(B, 0), _ws_bytes(workspace, workspace_bytes)
-    tokens, dX_0, dtable, workspace = _dev_ptrs(dev, (tokens, rows * 8, 8, "tokens"),
-                                                (dX_0, rows * n * C * 2, 2, "dX_0"),
-                                                (dtable, max(V, 0) * C * 4, 4, "dtable"),
-                                                (workspace, wb, None, "workspace"))
+    tokens, dX_0, dtable, workspace = _dev_ptrs(dev, (tokens, dX_0, dtable, workspace), (
+        (rows * 8, 8, "tokens"), (rows * n * C * 2, 2, "dX_0"), (max(V, 0) * C * 4, 4, "dtable"),
+        (wb, None, "workspace")))
     st = load().mhc_embed_bwd(B, n, C, V, tokens, dX_0, float(scale), int(bool(accumulate)), dtable, workspace, wb,
                               _dev_stream(stream, dev))
     if check:
