@@ -21,6 +21,8 @@
 #include "mhc_finish.h"
 #include "mhc_train.h"
 
+#include <type_traits>
+
 namespace mhc {
 
 namespace {
@@ -125,20 +127,34 @@ __device__ __forceinline__ float axis_sum(float x) {
   }
   return x;
 }
+template <int NS, int AXIS>
+__device__ __forceinline__ double axis_sum(double x) {  // n = 2: lane ^ 1 or lane ^ 2
+  static_assert(NS == 2, "");
+  constexpr int kCtrl = AXIS == 2 ? 0xB1 : 0x4E;
+  const int lo = __builtin_amdgcn_mov_dpp(__double2loint(x), kCtrl, 0xF, 0xF, false);
+  const int hi = __builtin_amdgcn_mov_dpp(__double2hiint(x), kCtrl, 0xF, 0xF, false);
+  return x + __hiloint2double(hi, lo);
+}
 // 1 / x to about an ulp: the hardware's reciprocal and a Newton step.
 __device__ __forceinline__ float recip(float x) {
   const float r = __builtin_amdgcn_rcpf(x);
   return fmaf(r, fmaf(-x, r, 1.0f), r);
 }
+__device__ __forceinline__ double recip(double x) { return 1.0 / x; }
 
 // The coefficients' gradient of each row: n*n lanes a row, one element of the
 // n x n matrix each, with the accurate exponentials.  A 1 x 1 matrix is 1
 // whatever its logit and has no gradient.  The first division is an IEEE one
 // (its totals are sums of exponentials of any size); the later ones, whose
 // totals are near 1, multiply by a reciprocal.  The 80 sums and divisions of a
-// row depend on each other, so the kernel is bound by their latency.  The
-// partial sums of db and dalpha are kept in fp64 (few adds, and gates'
-// gradients cancel over a batch).
+// row depend on each other, so the kernel is bound by their latency (and at
+// n = 8, 64 lanes a row, by their number).
+//
+// What is summed over a batch cancels, so the partial sums of db and dalpha
+// and the gates' derivatives are fp64 (a few operations a row).  So is the
+// whole of a 2 x 2 matrix: its gradient has one degree of freedom, all of
+// dH_res's other three cancel, and fp32 left errors of 1e-6 of the sum (n = 4
+// and 8, with 9 and 49, stay under 4e-7).
 //
 // dlogit leaves in the tiles' records, in the matrix core's operand order,
 // split into bf16 parts whose sum is dlogit to 2^-17 (hi + mid: for dX, which
@@ -158,86 +174,75 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
   using T = Tiles<NS>;
   constexpr int TH = sum_threads<NS>();
   constexpr int NN = NS * NS, N = NN + 2 * NS, R = TH / NN;
-  constexpr int GATES = (2 * NS + NN - 1) / NN;  // gates a lane: 2 at n = 1, else 1
   constexpr int IT = kSinkhornIters;
   constexpr int NP = N | 1;  // odd: rows start in different LDS banks
-  __shared__ float turn[R];
+  __shared__ float along[R];  // a row's sum of dlogit * logit over the res block
   __shared__ union {
     float dl[R][NP];
     double part[R][N + 3];
   } sh;
-  const int e = threadIdx.x % NN, slot = threadIdx.x / NN;
-  double sum_res = 0.0, sum_gate[GATES] = {}, sum_a[3] = {};
+  const int e = threadIdx.x % NN, slot = threadIdx.x / NN;  // the thread's element of a row's matrix
+  const int gk = threadIdx.x % (2 * NS);                    // and its gate, of any row
+  const bool post = gk >= NS;
+  const float alpha_gate = post ? alpha_post : alpha_pre, b_gate = post ? b_post[gk - NS] : b_pre[gk];
+  double sum_res = 0.0, sum_gate = 0.0, sum_a_res = 0.0, sum_a_gate = 0.0;
   const uint32_t stride = gridDim.x * R;
   for (uint32_t row0 = blockIdx.x * R; row0 < B; row0 += stride) {
+    for (int w = threadIdx.x; w < R * 2 * NS; w += TH) {
+      const int gs = w / (2 * NS);
+      const size_t row = row0 + gs;
+      float dl = 0.f;
+      if (row < B) {
+        const float l = logits[row * N + gk], r = r_in[row];
+        const double z = (double)alpha_gate * l / r + b_gate;
+        const double t = exp(-fabs(z));  // s(z) s(-z) = t / (1 + t)^2
+        const double dz = (post ? 2.0f * dH[row * N + gk] : dpre[row * NS + gk]) * t / ((1.0 + t) * (1.0 + t));
+        dl = (float)(alpha_gate * dz / r);
+        sum_gate += dz;
+        sum_a_gate += dz * l / r;
+      }
+      sh.dl[gs][gk] = dl;
+    }
+
     const uint32_t at = row0 + slot;
     const bool in = at < B;
     const uint32_t row = in ? at : B - 1;  // lanes past the end redo the last row and write nothing
-    const float *lg = logits + (size_t)row * N;
-    const float *up = dH + (size_t)row * N;
-    const float r = r_in[row];
-    float scaled = 0.f;  // sum of dlogit * logit over the lane's coefficients
-
-    float dz_gate[GATES], dl_gate[GATES];
-#pragma unroll
-    for (int q = 0; q < GATES; ++q) {
-      const int k = e + q * NN;
-      dz_gate[q] = dl_gate[q] = 0.f;
-      if (k < 2 * NS) {
-        const bool post = k >= NS;
-        const float a = post ? alpha_post : alpha_pre;
-        const float z = a * lg[k] / r + (post ? b_post[k - NS] : b_pre[k]);
-        const float s0 = 1.0f / (1.0f + expf(-z)), s1 = 1.0f / (1.0f + expf(z));
-        const float g = post ? 2.0f * up[k] : dpre[(size_t)row * NS + k];
-        dz_gate[q] = g * s0 * s1;
-        dl_gate[q] = a * dz_gate[q] / r;
-        scaled = fmaf(dl_gate[q], lg[k], scaled);
-      }
-    }
-
-    const float lr = lg[2 * NS + e];
-    float dz = 0.f;
+    const float r = r_in[row], lr = logits[(size_t)row * N + 2 * NS + e];
+    typedef typename std::conditional<NS == 2, double, float>::type real;
+    real dz = 0;
     if constexpr (NS > 1) {
-      const float m0 = expf(alpha_res * lr / r + b_res[e]);
-      float y[2 * IT], inv[2 * IT];
-      const float total = axis_sum<NS, 2>(m0);
-      float m = y[0] = m0 / total;
+      const real z = (real)alpha_res * lr / r + b_res[e];
+      real m0;
+      if constexpr (NS == 2)
+        m0 = exp(z);
+      else
+        m0 = expf(z);
+      real y[2 * IT], inv[2 * IT];
+      const real total = axis_sum<NS, 2>(m0);
+      real m = y[0] = m0 / total;
 #pragma unroll
       for (int k = 1; k < 2 * IT; ++k) {
         inv[k] = recip(k % 2 ? axis_sum<NS, 1>(m) : axis_sum<NS, 2>(m));
         y[k] = m = m * inv[k];
       }
-      float d = up[2 * NS + e];
+      real d = dH[(size_t)row * N + 2 * NS + e];
 #pragma unroll
       for (int k = 2 * IT - 1; k > 0; --k) {
-        const float dy = d * y[k];
+        const real dy = d * y[k];
         d = (d - (k % 2 ? axis_sum<NS, 1>(dy) : axis_sum<NS, 2>(dy))) * inv[k];
       }
       // dz = m0 (d - sum) / total, with m0 / total = y[0]
       dz = y[0] * (d - axis_sum<NS, 2>(d * y[0]));
     }
-    const float dlr = alpha_res * dz / r;
-    scaled = fmaf(dlr, lr, scaled);
+    const float dlr = (float)(alpha_res * dz / r);
+    float res = dlr * lr;
 #pragma unroll
-    for (int o = 1; o < NN; o <<= 1) scaled += __shfl_xor(scaled, o);
-
-    float *out = sh.dl[slot];
-    out[2 * NS + e] = in ? dlr : 0.f;
-#pragma unroll
-    for (int q = 0; q < GATES; ++q)
-      if (e + q * NN < 2 * NS) out[e + q * NN] = in ? dl_gate[q] : 0.f;
-    if (e == 0) turn[slot] = in ? (float)(-(double)scaled * inv_k / ((double)r * r)) : 0.f;
+    for (int o = 1; o < NN; o <<= 1) res += __shfl_xor(res, o);
+    sh.dl[slot][2 * NS + e] = in ? dlr : 0.f;
+    if (e == 0) along[slot] = res;
     if (in) {
       sum_res += dz;
-      sum_a[2] += (double)dz * lr / r;
-#pragma unroll
-      for (int q = 0; q < GATES; ++q) {
-        const int k = e + q * NN;
-        if (k < 2 * NS) {
-          sum_gate[q] += dz_gate[q];
-          sum_a[k >= NS ? 1 : 0] += (double)dz_gate[q] * lg[k] / r;
-        }
-      }
+      sum_a_res += (double)dz * lr / r;
     }
     __syncthreads();
     const auto at_row = [&](int i, int k) { return k < N ? sh.dl[i][k] : 0.f; };
@@ -283,24 +288,32 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
       const size_t tile = row0 / 16 + tl, row = tile * 16 + i;
       if (tile >= tiles) continue;
       float x = 0.f;
-      if (k == T::KH)
-        x = turn[tl * 16 + i];
-      else if (row < B)
+      if (k == T::KH && row < B) {
+        const double r = r_in[row];
+        double all = along[tl * 16 + i];
+#pragma unroll
+        for (int g = 0; g < 2 * NS; ++g) all += (double)sh.dl[tl * 16 + i][g] * logits[row * N + g];
+        x = (float)(-all * inv_k / (r * r));
+      } else if (row < B) {
         x = H[row * N + (k < NS ? k : k + NS)];  // the post block is not needed
+      }
       reinterpret_cast<float *>(records + tile * T::kStride + T::kMix)[k * 16 + i] = x;
     }
     __syncthreads();
   }
   // [db_pre | db_post | db_res | dalpha_pre, _post, _res] of this workgroup
+  for (int w = threadIdx.x; w < R * (N + 3); w += TH) (&sh.part[0][0])[w] = 0.0;
+  __syncthreads();
   sh.part[slot][2 * NS + e] = sum_res;
 #pragma unroll
-  for (int q = 0; q < GATES; ++q)
-    if (e + q * NN < 2 * NS) sh.part[slot][e + q * NN] = sum_gate[q];
+  for (int o = 1; o < NN; o <<= 1) sum_a_res += __shfl_xor(sum_a_res, o);
+  if (e == 0) sh.part[slot][N + 2] = sum_a_res;
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-#pragma unroll
-    for (int o = 1; o < NN; o <<= 1) sum_a[k] += __shfl_xor(sum_a[k], o);
-    if (e == 0) sh.part[slot][N + k] = sum_a[k];
+  for (int o = 1; o < NS; o <<= 1) sum_a_gate += __shfl_xor(sum_a_gate, o);
+  if (threadIdx.x < R * 2 * NS) {
+    const int gs = threadIdx.x / (2 * NS);
+    sh.part[gs][gk] = sum_gate;
+    if (gk % NS == 0) sh.part[gs][N + (post ? 1 : 0)] = sum_a_gate;
   }
   __syncthreads();
   for (int k = threadIdx.x; k < N + 3; k += TH) {
