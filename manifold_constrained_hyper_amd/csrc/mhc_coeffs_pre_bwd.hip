@@ -110,37 +110,39 @@ __global__ __launch_bounds__(64 * W) void pre_dots_kernel(const void *__restrict
 __device__ __forceinline__ float dpp_add_ror8(float x) {  // lane ^ 8 in its row of 16
   return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x128, 0xF, 0xF, false));
 }
-__device__ __forceinline__ float dpp_add_ror4(float x) {  // lane ^ 4, once lanes 8 apart are equal
-  return x + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x124, 0xF, 0xF, false));
-}
 template <int NS, int AXIS>
 __device__ __forceinline__ float axis_sum(float x) {
+  static_assert(NS == 8, "");
   if constexpr (AXIS == 2) return group_sum<NS>(x);
-  if constexpr (NS == 2) return dpp_add_xor2(x);
-  if constexpr (NS == 4) return dpp_add_ror4(dpp_add_ror8(x));
-  if constexpr (NS == 8) {
-    x = dpp_add_ror8(x);
-    const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
-    const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
-  }
-  return x;
+  x = dpp_add_ror8(x);
+  const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
+  const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double x) {
+  const int lo = __builtin_amdgcn_mov_dpp(__double2loint(x), CTRL, 0xF, 0xF, false);
+  const int hi = __builtin_amdgcn_mov_dpp(__double2hiint(x), CTRL, 0xF, 0xF, false);
+  return x + __hiloint2double(hi, lo);
 }
 template <int NS, int AXIS>
-__device__ __forceinline__ double axis_sum(double x) {  // n = 2: lane ^ 1 or lane ^ 2
-  static_assert(NS == 2, "");
-  constexpr int kCtrl = AXIS == 2 ? 0xB1 : 0x4E;
-  const int lo = __builtin_amdgcn_mov_dpp(__double2loint(x), kCtrl, 0xF, 0xF, false);
-  const int hi = __builtin_amdgcn_mov_dpp(__double2hiint(x), kCtrl, 0xF, 0xF, false);
-  return x + __hiloint2double(hi, lo);
+__device__ __forceinline__ double axis_sum(double x) {
+  static_assert(NS == 2 || NS == 4, "");
+  if constexpr (NS == 2) return dpp_add<AXIS == 2 ? 0xB1 : 0x4E>(x);  // lane ^ 1, lane ^ 2
+  if constexpr (AXIS == 2) return dpp_add<0x4E>(dpp_add<0xB1>(x));
+  return dpp_add<0x124>(dpp_add<0x128>(x));  // lane ^ 8, then lane ^ 4 (lane + 4, as lanes 8 apart are equal)
 }
 // 1 / x to about an ulp: the hardware's reciprocal and a Newton step.
 __device__ __forceinline__ float recip(float x) {
   const float r = __builtin_amdgcn_rcpf(x);
   return fmaf(r, fmaf(-x, r, 1.0f), r);
 }
-__device__ __forceinline__ double recip(double x) { return 1.0 / x; }
+__device__ __forceinline__ double recip(double x) {  // two steps: 2^-23, 2^-46, 2^-52
+  double r = __builtin_amdgcn_rcp(x);
+  r = fma(r, fma(-x, r, 1.0), r);
+  return fma(r, fma(-x, r, 1.0), r);
+}
 
 // The coefficients' gradient of each row: n*n lanes a row, one element of the
 // n x n matrix each, with the accurate exponentials.  A 1 x 1 matrix is 1
@@ -151,10 +153,12 @@ __device__ __forceinline__ double recip(double x) { return 1.0 / x; }
 // n = 8, 64 lanes a row, by their number).
 //
 // What is summed over a batch cancels, so the partial sums of db and dalpha
-// and the gates' derivatives are fp64 (a few operations a row).  So is the
-// whole of a 2 x 2 matrix: its gradient has one degree of freedom, all of
-// dH_res's other three cancel, and fp32 left errors of 1e-6 of the sum (n = 4
-// and 8, with 9 and 49, stay under 4e-7).
+// and the gates' derivatives are fp64 (a few operations a row), and up to
+// n = 4 so are the normalisations: most of dH_res cancels in them (at n = 2
+// all but one degree of freedom), and fp32 left errors of 1e-6 of small
+// batches' sums.  That costs 5 us at n=4, B=16384 (19 against 14).  At n = 8,
+// with 49 degrees of freedom, fp32's errors stay under 4e-7 of the sums, and
+// 64 bits would not fit the registers of 1024 threads.
 //
 // dlogit leaves in the tiles' records, in the matrix core's operand order,
 // split into bf16 parts whose sum is dlogit to 2^-17 (hi + mid: for dX, which
@@ -208,12 +212,12 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
     const bool in = at < B;
     const uint32_t row = in ? at : B - 1;  // lanes past the end redo the last row and write nothing
     const float r = r_in[row], lr = logits[(size_t)row * N + 2 * NS + e];
-    typedef typename std::conditional<NS == 2, double, float>::type real;
+    typedef typename std::conditional<NS <= 4, double, float>::type real;
     real dz = 0;
     if constexpr (NS > 1) {
       const real z = (real)alpha_res * lr / r + b_res[e];
       real m0;
-      if constexpr (NS == 2)
+      if constexpr (NS <= 4)
         m0 = exp(z);
       else
         m0 = expf(z);
