@@ -217,17 +217,22 @@ __device__ __forceinline__ void write_row(f32x4 *o, const float (&acc)[8], float
 // the block is written to the table; a block's first token that began before
 // it, and its last that goes on after it, are left in `part` ([blocks][2][C]:
 // from the left, to the right) for the join below.  Workgroups from sum_wgs
-// on write zeros to the table rows that have no token, kZeroRows each.
+// on write zeros to the table rows that have no token: kZeroBytes or a row each,
+// kZeroRows at most (with 8 rows each the table of n=4, C=7168, B=16384,
+// V=32768 took 405 us, not 396, and V=65536, C=64 with 300 rows 30, not 18).
 constexpr int kAhead = 16;  // 16-byte loads a lane has in flight
-constexpr uint32_t kZeroRows = 8;
+constexpr uint32_t kZeroRows = 32, kZeroBytes = 1 << 14;
 
-// Eight lanes search for a row's token together, nine parts a step.
-__device__ __forceinline__ void zero_rows(const u64 *keys, uint32_t B, uint64_t v0, uint32_t V, uint32_t cvec,
+// Eight lanes search for a row's token together, nine parts a step; a wave
+// searches for eight rows.  All threads then write the absent ones, whatever
+// their width.
+__device__ __forceinline__ void zero_rows(const u64 *keys, uint32_t B, uint64_t v0, uint32_t rows, uint32_t V, uint32_t cvec,
                                           f32x4 *dtable) {
-  static_assert(kZeroRows == 8, "eight lanes of a wave for each row");
+  static_assert(kZeroRows == kThreads / 8, "eight lanes for each row");
+  __shared__ uint8_t absent[kZeroRows];
   const uint32_t lane = threadIdx.x & 63, s = lane & 7, shift = lane & 56;
-  const u64 token = v0 + (lane >> 3);
-  uint32_t lo = 0, len = B;  // [lo, lo + len] holds the first place not below the token
+  const u64 token = v0 + (threadIdx.x >> 3);
+  uint32_t lo = 0, len = (threadIdx.x >> 3) < rows ? B : 0;  // [lo, lo + len] holds the first place not below the token
   while (__any(len > 0)) {
     const uint32_t part = (len + 8) / 9, at = lo + s * part + part - 1;
     const bool probe = len > 0 && s * part + part <= len;
@@ -237,14 +242,17 @@ __device__ __forceinline__ void zero_rows(const u64 *keys, uint32_t B, uint64_t 
     lo += found * part;
     len = len == 0 ? 0 : found == probes ? len - found * part : part - 1;
   }
-  const bool absent = s == 0 && token < V && (lo >= B || token_of(keys[lo]) != token);
-  u64 rows = __ballot(absent);
-  while (rows) {
-    const uint64_t v = v0 + ((uint32_t)__builtin_ctzll(rows) >> 3);
-    rows &= rows - 1;
-    for (uint32_t c = threadIdx.x; c < 2 * cvec; c += kThreads)
-      __builtin_nontemporal_store(f32x4{0.f, 0.f, 0.f, 0.f}, dtable + v * 2 * cvec + c);
+  if (s == 0 && (threadIdx.x >> 3) < rows) absent[threadIdx.x >> 3] = token < V && (lo >= B || token_of(keys[lo]) != token);
+  __syncthreads();
+  const uint32_t width = 2 * cvec, down = kThreads / width, along = kThreads % width;
+  uint32_t row = threadIdx.x / width, c = threadIdx.x % width;
+  while (row < rows) {
+    if (absent[row]) __builtin_nontemporal_store(f32x4{0.f, 0.f, 0.f, 0.f}, dtable + (v0 + row) * width + c);
+    row += down;
+    c += along;
+    if (c >= width) c -= width, ++row;
   }
+  __syncthreads();
 }
 
 template <int NS>
@@ -311,10 +319,10 @@ __global__ __launch_bounds__(kThreads) void table_kernel(const u64 *__restrict__
                                                          float scale, bool accumulate, f32x4 *__restrict__ dtable,
                                                          float *__restrict__ part, uint32_t B, uint32_t cvec,
                                                          uint32_t slices, uint32_t rb, uint64_t items,
-                                                         uint64_t sum_wgs, uint64_t all_wgs, uint32_t V) {
+                                                         uint64_t sum_wgs, uint64_t all_wgs, uint32_t zero, uint32_t V) {
   for (uint64_t wg = blockIdx.x; wg < all_wgs; wg += gridDim.x) {
     if (wg >= sum_wgs) {
-      zero_rows(keys, B, (wg - sum_wgs) * kZeroRows, V, cvec, dtable);
+      zero_rows(keys, B, (wg - sum_wgs) * zero, zero, V, cvec, dtable);
       continue;
     }
     const uint64_t item = (uint64_t)uniform((int64_t)(wg * (kThreads / 64) + (threadIdx.x >> 6)));
@@ -432,10 +440,12 @@ hipError_t table_n(const EmbedBwdPlan &p, int64_t B, int64_t C, int64_t V, const
   }
   const uint64_t blocks = (B + rb - 1) / rb, items = blocks * slices;
   const uint64_t sum_wgs = (items + kThreads / 64 - 1) / (kThreads / 64);
-  const uint64_t all_wgs = sum_wgs + (accumulate ? 0 : (uint64_t)(V + kZeroRows - 1) / kZeroRows);
+  uint32_t zero = kZeroRows;
+  while (zero > 1 && (uint64_t)zero * C * 4 > kZeroBytes) zero /= 2;
+  const uint64_t all_wgs = sum_wgs + (accumulate ? 0 : (uint64_t)(V + zero - 1) / zero);
   table_kernel<NS><<<wgs(all_wgs, 1, 1u << 22), kThreads, 0, st>>>(keys, static_cast<const u32x4 *>(G), scale,
                                                                    accumulate, out, part, rows, cvec, slices, rb,
-                                                                   items, sum_wgs, all_wgs, (uint32_t)V);
+                                                                   items, sum_wgs, all_wgs, zero, (uint32_t)V);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (blocks > 1)
     join_parts_kernel<<<wgs(items, 1, 1u << 22), kThreads, 0, st>>>(keys, part, scale, accumulate, out, rows, cvec,

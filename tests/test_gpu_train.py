@@ -483,6 +483,27 @@ def test_embedding_gradient_of_many_rows(B, n, C, V, how):
     assert bool(((d.t.double() - want).abs() <= (count * n + 2) * U * total).all())
 
 
+@pytest.mark.parametrize("B,n,C,V", [(5, 2, 8, 70001), (700, 1, 56, 4999), (9, 1, 2056, 333), (3, 4, 8192, 7)])
+def test_embedding_gradient_of_few_rows(B, n, C, V):
+    """Most of the table has no token: narrow rows, of which a workgroup writes
+    many zeros, and wide ones, the last of them at the table's end.  Every
+    element is B n values of either sign, a product and B n + 1 roundings."""
+    _say(f"embedding gradient of few rows B={B} n={n} C={C} V={V}")
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    tokens = torch.randint(0, V, (B,), generator=gen, device="cuda")
+    tokens[0], tokens[B // 2] = V - 1, 0
+    G = torch.randn(B, n * C, generator=gen, device="cuda").to(torch.bfloat16)
+    ws = Guarded(mhc.mhc_embed_bwd_workspace_size(B, n, C, V), dtype=torch.uint8, fill=0xFF)
+    d = Guarded(V, C)
+    mhc.mhc_embed_bwd(B, n, C, V, tokens, G, 0.75, d.t, ws.t)
+    torch.cuda.synchronize()
+    assert d.check() and ws.check()
+    g = G.double().view(B, n, C)
+    want = torch.zeros(V, C, dtype=torch.float64, device="cuda").index_add_(0, tokens, 0.75 * g.sum(1))
+    total = torch.zeros_like(want).index_add_(0, tokens, 0.75 * g.abs().sum(1))
+    assert bool(((d.t.double() - want).abs() <= (B * n + 2) * U * total).all())
+
+
 # -- a training step --------------------------------------------------------------------------------
 
 class Model:
