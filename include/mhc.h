@@ -1,6 +1,6 @@
 /*
  * mhc.h -- C ABI of libmhc: the mHC (manifold-constrained hyper-connections)
- * residual-stream forward on one AMD Instinct MI355X (gfx950).
+ * residual stream, forward and backward, on one AMD Instinct MI355X (gfx950).
  *
  * The method is the one stated in section 2 of the blog page
  * "mHC 算法分析 & cutile 高效实现" (edward-lyz, 2026-02-10), cited below as
@@ -530,13 +530,17 @@ int mhc_lazy_prenorm_gemm(int64_t M, int64_t N, int64_t K, const void *A, const 
  * dX_t is the G of the layer before.  The calls take what the forward calls
  * returned (logits, r, H) and X_t either as the bf16 stream or, in the *_ckpt
  * calls, as its checkpoint (mhc_ckpt_pack).  The forward calls on a bf16
- * stream with a bf16 phi are the ones they belong to.
+ * stream are the ones they belong to.  After a *_phi32 call pass phi rounded
+ * to bf16: only dX_t's term dlogits . phi^T reads it.
  *
  * Gradients of the stream and of F are bf16, rounded once (nearest even);
  * gradients of parameters and coefficients are fp32.  Sums are fp32 or wider
  * and run in a fixed order (no atomics on values): equal inputs give equal
- * bits.  A row with r = 0 has no gradient (NaN), as it has no logits in the
- * forward.  Conventions, checks and errors are those at the top of this file;
+ * bits.  A row with r = 0 (all zeros) has no gradient, as it has no gates in
+ * the forward: its NaN reaches the parameters' gradients, which are sums over
+ * the rows, so such rows must not be among those passed here.  A workspace
+ * belongs to one call at a time: calls on different streams, and graphs that
+ * may run side by side, need one each.  Conventions, checks and errors are those at the top of this file;
  * beyond them the gradients of parameters of no rows (B == 0) are zeros, so
  * those calls fill their parameter outputs at B == 0 and then need those
  * pointers.
@@ -636,7 +640,8 @@ int mhc_coeffs_pre_bwd_ckpt(int64_t B, int32_t n, int64_t C, const void *codes,
 
 /* The first layer's stream from token embeddings: X_0[b, i*C + c] =
  * bf16(scale * table[tokens[b], c]) for every stream i.  A token outside
- * [0, V) (padding) gives a row of zeros.
+ * [0, V) gives a row of zeros; such a row has r = 0 and no gates, so padding
+ * that goes through the layers needs a token of the table.
  *
  *   tokens  in  int64 [B], 8-byte aligned
  *   table   in  bf16 [V, C]
