@@ -55,7 +55,8 @@ struct Tiles {
   static constexpr int kChunks = (kBytes + 1023) / 1024, kStride = kChunks * 1024;
 };
 
-// dH_pre [B, n]: a workgroup a row.
+// dH_pre [B, n]: a workgroup a row (103 us at n=4, C=7168, B=16384 from the
+// checkpoint: 0.72 GB at 7.0 TB/s).
 template <int NS, bool CK, int W>
 __global__ __launch_bounds__(64 * W) void pre_dots_kernel(const void *__restrict__ X,
                                                           const uint8_t *__restrict__ scales,
@@ -169,29 +170,97 @@ constexpr int sum_threads() { return NS == 8 ? 1024 : 256; }  // a multiple of 1
 
 __device__ __forceinline__ float bf16_round(float x) { return bf16_lo(pack_bf16x2(x, 0.f)); }
 
+// With Dots (where X_t is), the row dot products are formed here too, by eight
+// waves, rather than in a launch of their own.
+struct NoDots {};
+template <bool CK>
+struct Dots {
+  const void *X;
+  const uint8_t *scales;
+  const u32x4 *dF;
+  uint32_t cvec, blocks;
+};
+template <class D>
+constexpr bool kFused = !std::is_same<D, NoDots>::value;
+template <int NS, bool FUSED>
+constexpr int coeff_threads() { return FUSED ? 512 : sum_threads<NS>(); }
 template <int NS>
-__global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
-    const float *__restrict__ logits, const float *__restrict__ r_in, float alpha_pre, float alpha_post,
+constexpr int kDotRows = NS == 4 ? 2 : 8 / NS;  // rows a wave has under way
+
+template <int NS, bool CK>
+__device__ __forceinline__ void row_dots(const Dots<CK> &d, uint32_t row0, uint32_t rows, uint32_t B, float (*out)[NS]) {
+  constexpr int U = kDotRows<NS>;
+  const uint32_t lane = threadIdx.x & 63, wave = (uint32_t)uniform((int)(threadIdx.x >> 6)), W = blockDim.x >> 6;
+  for (uint32_t base = wave * U; base < rows && row0 + base < B; base += W * U) {
+    float acc[U][NS];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NS; ++j) acc[u][j] = 0.f;
+    for (uint32_t v = lane; v < d.cvec; v += 64) {
+      Held8<CK> x[U][NS];
+      u32x4 f[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t row = row0 + base + u < B ? row0 + base + u : B - 1;
+        f[u] = __builtin_nontemporal_load(d.dF + (size_t)row * d.cvec + v);
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+          x[u][j].load(d.X, d.scales, ((size_t)row * NS + j) * d.cvec + v, ((size_t)row * NS + j) * d.blocks + (v >> 2));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float fw[8];
+        widen8(f[u], fw);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          float xw[8];
+          x[u][j].widen(xw);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[u][j] = fmaf(fw[e], xw[e], acc[u][j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) acc[u][j] += __shfl_xor(acc[u][j], o);
+        if (lane == 0) out[base + u][j] = acc[u][j];
+      }
+  }
+}
+
+template <int NS, class D>
+__global__ __launch_bounds__((coeff_threads<NS, kFused<D>>())) void coeffs_bwd_kernel(
+    D dots, const float *__restrict__ logits, const float *__restrict__ r_in, float alpha_pre, float alpha_post,
     float alpha_res, const float *__restrict__ b_pre, const float *__restrict__ b_post,
     const float *__restrict__ b_res, const float *__restrict__ dH, const float *__restrict__ dpre,
     const float *__restrict__ H, char *__restrict__ records, double *__restrict__ sums, uint32_t B, double inv_k) {
   using T = Tiles<NS>;
-  constexpr int TH = sum_threads<NS>();
-  constexpr int NN = NS * NS, N = NN + 2 * NS, R = TH / NN;
+  constexpr int TH = coeff_threads<NS, kFused<D>>();
+  constexpr int NN = NS * NS, N = NN + 2 * NS, R = sum_threads<NS>() / NN;
   constexpr int IT = kSinkhornIters;
   constexpr int NP = N | 1;  // odd: rows start in different LDS banks
+  __shared__ float row_dot[kFused<D> ? R : 1][NS];
   __shared__ float along[R];  // a row's sum of dlogit * logit over the res block
   __shared__ union {
     float dl[R][NP];
     double part[R][N + 3];
   } sh;
   const int e = threadIdx.x % NN, slot = threadIdx.x / NN;  // the thread's element of a row's matrix
+  const bool mine = slot < R;  // (whole waves: the other waves have no element)
   const int gk = threadIdx.x % (2 * NS);                    // and its gate, of any row
   const bool post = gk >= NS;
   const float alpha_gate = post ? alpha_post : alpha_pre, b_gate = post ? b_post[gk - NS] : b_pre[gk];
   double sum_res = 0.0, sum_gate = 0.0, sum_a_res = 0.0, sum_a_gate = 0.0;
   const uint32_t stride = gridDim.x * R;
   for (uint32_t row0 = blockIdx.x * R; row0 < B; row0 += stride) {
+    if constexpr (kFused<D>) {
+      row_dots<NS>(dots, row0, R, B, row_dot);
+      __syncthreads();
+    }
     for (int w = threadIdx.x; w < R * 2 * NS; w += TH) {
       const int gs = w / (2 * NS);
       const size_t row = row0 + gs;
@@ -200,7 +269,7 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
         const float l = logits[row * N + gk], r = r_in[row];
         const double z = (double)alpha_gate * l / r + b_gate;
         const double t = exp(-fabs(z));  // s(z) s(-z) = t / (1 + t)^2
-        const double dz = (post ? 2.0f * dH[row * N + gk] : dpre[row * NS + gk]) * t / ((1.0 + t) * (1.0 + t));
+        const double dz = (post ? 2.0f * dH[row * N + gk] : kFused<D> ? row_dot[kFused<D> ? gs : 0][gk] : dpre[row * NS + gk]) * t / ((1.0 + t) * (1.0 + t));
         dl = (float)(alpha_gate * dz / r);
         sum_gate += dz;
         sum_a_gate += dz * l / r;
@@ -208,45 +277,47 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
       sh.dl[gs][gk] = dl;
     }
 
-    const uint32_t at = row0 + slot;
-    const bool in = at < B;
-    const uint32_t row = in ? at : B - 1;  // lanes past the end redo the last row and write nothing
-    const float r = r_in[row], lr = logits[(size_t)row * N + 2 * NS + e];
-    typedef typename std::conditional<NS <= 4, double, float>::type real;
-    real dz = 0;
-    if constexpr (NS > 1) {
-      const real z = (real)alpha_res * lr / r + b_res[e];
-      real m0;
-      if constexpr (NS <= 4)
-        m0 = exp(z);
-      else
-        m0 = expf(z);
-      real y[2 * IT], inv[2 * IT];
-      const real total = axis_sum<NS, 2>(m0);
-      real m = y[0] = m0 / total;
+    if (mine) {
+      const uint32_t at = row0 + slot;
+      const bool in = at < B;
+      const uint32_t row = in ? at : B - 1;  // lanes past the end redo the last row and write nothing
+      const float r = r_in[row], lr = logits[(size_t)row * N + 2 * NS + e];
+      typedef typename std::conditional<NS <= 4, double, float>::type real;
+      real dz = 0;
+      if constexpr (NS > 1) {
+        const real z = (real)alpha_res * lr / r + b_res[e];
+        real m0;
+        if constexpr (NS <= 4)
+          m0 = exp(z);
+        else
+          m0 = expf(z);
+        real y[2 * IT], inv[2 * IT];
+        const real total = axis_sum<NS, 2>(m0);
+        real m = y[0] = m0 / total;
 #pragma unroll
-      for (int k = 1; k < 2 * IT; ++k) {
-        inv[k] = recip(k % 2 ? axis_sum<NS, 1>(m) : axis_sum<NS, 2>(m));
-        y[k] = m = m * inv[k];
+        for (int k = 1; k < 2 * IT; ++k) {
+          inv[k] = recip(k % 2 ? axis_sum<NS, 1>(m) : axis_sum<NS, 2>(m));
+          y[k] = m = m * inv[k];
+        }
+        real d = dH[(size_t)row * N + 2 * NS + e];
+#pragma unroll
+        for (int k = 2 * IT - 1; k > 0; --k) {
+          const real dy = d * y[k];
+          d = (d - (k % 2 ? axis_sum<NS, 1>(dy) : axis_sum<NS, 2>(dy))) * inv[k];
+        }
+        // dz = m0 (d - sum) / total, with m0 / total = y[0]
+        dz = y[0] * (d - axis_sum<NS, 2>(d * y[0]));
       }
-      real d = dH[(size_t)row * N + 2 * NS + e];
+      const float dlr = (float)(alpha_res * dz / r);
+      float res = dlr * lr;
 #pragma unroll
-      for (int k = 2 * IT - 1; k > 0; --k) {
-        const real dy = d * y[k];
-        d = (d - (k % 2 ? axis_sum<NS, 1>(dy) : axis_sum<NS, 2>(dy))) * inv[k];
+      for (int o = 1; o < NN; o <<= 1) res += __shfl_xor(res, o);
+      sh.dl[slot][2 * NS + e] = in ? dlr : 0.f;
+      if (e == 0) along[slot] = res;
+      if (in) {
+        sum_res += dz;
+        sum_a_res += (double)dz * lr / r;
       }
-      // dz = m0 (d - sum) / total, with m0 / total = y[0]
-      dz = y[0] * (d - axis_sum<NS, 2>(d * y[0]));
-    }
-    const float dlr = (float)(alpha_res * dz / r);
-    float res = dlr * lr;
-#pragma unroll
-    for (int o = 1; o < NN; o <<= 1) res += __shfl_xor(res, o);
-    sh.dl[slot][2 * NS + e] = in ? dlr : 0.f;
-    if (e == 0) along[slot] = res;
-    if (in) {
-      sum_res += dz;
-      sum_a_res += (double)dz * lr / r;
     }
     __syncthreads();
     const auto at_row = [&](int i, int k) { return k < N ? sh.dl[i][k] : 0.f; };
@@ -308,10 +379,10 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
   // [db_pre | db_post | db_res | dalpha_pre, _post, _res] of this workgroup
   for (int w = threadIdx.x; w < R * (N + 3); w += TH) (&sh.part[0][0])[w] = 0.0;
   __syncthreads();
-  sh.part[slot][2 * NS + e] = sum_res;
+  if (mine) sh.part[slot][2 * NS + e] = sum_res;
 #pragma unroll
   for (int o = 1; o < NN; o <<= 1) sum_a_res += __shfl_xor(sum_a_res, o);
-  if (e == 0) sh.part[slot][N + 2] = sum_a_res;
+  if (mine && e == 0) sh.part[slot][N + 2] = sum_a_res;
 #pragma unroll
   for (int o = 1; o < NS; o <<= 1) sum_a_gate += __shfl_xor(sum_a_gate, o);
   if (threadIdx.x < R * 2 * NS) {
@@ -326,6 +397,19 @@ __global__ __launch_bounds__(sum_threads<NS>()) void coeffs_bwd_kernel(
     sums[(size_t)blockIdx.x * (N + 3) + k] = a;
   }
 }
+
+// The sums over the rows besides dphi: the coefficient kernel's workgroups'
+// parts, and where they go.
+struct Sums {
+  const double *part;
+  int blocks;
+  float *dalpha, *db_pre, *db_post, *db_res;
+  template <int NS>
+  __device__ __forceinline__ float *out(int k) const {
+    constexpr int N = NS * NS + 2 * NS;
+    return k < NS ? db_pre + k : k < 2 * NS ? db_post + (k - NS) : k < N ? db_res + (k - 2 * NS) : dalpha + (k - N);
+  }
+};
 
 // dX and the partial dphi, in one pass over G, X_t and dF_pre.
 //
@@ -416,17 +500,27 @@ template <int NS, bool CK>
 __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     const char *__restrict__ X, const uint8_t *__restrict__ scales, const uint16_t *__restrict__ phi,
     const char *__restrict__ G, const char *__restrict__ dF, const char *__restrict__ records, char *__restrict__ dX,
-    float *__restrict__ out, uint32_t B, uint32_t cvec, uint32_t blocks, uint32_t slices, int wc) {
+    float *__restrict__ out, uint32_t B, uint32_t cvec, uint32_t blocks, uint32_t slices, uint32_t split, int wc,
+    Sums sums) {
   using T = Tiles<NS>;
   using S = Stage<NS, CK>;
   constexpr int N = T::N, KS = T::KS, MT = T::MT, JW = T::JW, GROUPS = T::GROUPS;
   __shared__ __attribute__((aligned(1024))) char stage[S::kStages][S::kBytes];
   __shared__ __attribute__((aligned(1024))) char record[S::kStages][T::kStride];
   __shared__ __attribute__((aligned(1024))) char own_out[S::kOutBytes];
+  if (blockIdx.x == slices * split) {  // with one row range there is no join_kernel
+    for (int k = threadIdx.x; k < N + 3; k += blockDim.x) {
+      double a = 0.0;
+#pragma unroll 8
+      for (int b = 0; b < sums.blocks; ++b) a += sums.part[(size_t)b * (N + 3) + k];
+      *sums.out<NS>(k) = (float)a;
+    }
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
   // wc waves along the channels, GROUPS along the streams.
   const int cw = wave / GROUPS, group = wave % GROUPS, waves = wc * GROUPS;
-  const uint32_t slice = blockIdx.x % slices, range = blockIdx.x / slices, split = gridDim.x / slices;
+  const uint32_t slice = blockIdx.x % slices, range = blockIdx.x / slices;
   const uint32_t v_wg = slice * (uint32_t)wc * 4;  // the workgroup's first vector of eight channels
   const uint32_t v_wave = v_wg + cw * 4;
   const int lo16 = lane & 15, q = lane >> 4, j0 = group * JW;
@@ -693,23 +787,21 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
 // the coefficient kernel's workgroups (a thread every 256th, then a tree).
 // The others: dphi from its row ranges, 64 vectors of four a workgroup, four
 // threads a vector that take a quarter of the ranges each, in order.
-__global__ __launch_bounds__(256) void join_kernel(const double *__restrict__ sums, int sum_blocks, int n,
-                                                   float *__restrict__ dalpha, float *__restrict__ db_pre,
-                                                   float *__restrict__ db_post, float *__restrict__ db_res,
-                                                   const f32x4 *__restrict__ part, f32x4 *__restrict__ dphi,
-                                                   uint64_t vecs, uint32_t split) {
-  const int N = n * n + 2 * n, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int NS>
+__global__ __launch_bounds__(256) void join_kernel(Sums sums, const f32x4 *__restrict__ part,
+                                                   f32x4 *__restrict__ dphi, uint64_t vecs, uint32_t split) {
+  constexpr int N = NS * NS + 2 * NS;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (blockIdx.x < (uint32_t)N + 3) {
     __shared__ double waves[4];
     const int k = blockIdx.x;
     double a = 0.0;
-    for (int b = threadIdx.x; b < sum_blocks; b += 256) a += sums[(size_t)b * (N + 3) + k];
+    for (int b = threadIdx.x; b < sums.blocks; b += 256) a += sums.part[(size_t)b * (N + 3) + k];
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) a += __shfl_xor(a, o);
     if (lane == 0) waves[wave] = a;
     __syncthreads();
-    float *out = k < n ? db_pre + k : k < 2 * n ? db_post + (k - n) : k < N ? db_res + (k - 2 * n) : dalpha + (k - N);
-    if (threadIdx.x == 0) *out = (float)((waves[0] + waves[1]) + (waves[2] + waves[3]));
+    if (threadIdx.x == 0) *sums.out<NS>(k) = (float)((waves[0] + waves[1]) + (waves[2] + waves[3]));
     return;
   }
   __shared__ f32x4 quarter[3][64];
@@ -744,6 +836,19 @@ uint32_t wgs(uint64_t work, uint64_t per, uint64_t most) {
   return (uint32_t)(g < most ? g : most);
 }
 
+// Few steps of the row dot products a wave cost less than a launch (2.7 us):
+// with up to two, n=4, B=16, C=512 takes 15.6 us, not 18.1, and with four
+// (C=2048) 18.4, not 18.0.  At n = 8 the kernel's 1024 threads have no
+// registers for it (1 us slower).
+constexpr int64_t kFusedSteps = 2;
+template <int NS>
+bool fused_dots(int64_t B, int64_t C) {
+  if (NS == 8) return false;
+  constexpr int R = sum_threads<NS>() / (NS * NS), at_once = coeff_threads<NS, true>() / 64 * kDotRows<NS>;
+  const int64_t rows = B < R ? B : R;
+  return (rows + at_once - 1) / at_once * ((C + 511) / 512) <= kFusedSteps && (B + R - 1) / R <= 256;
+}
+
 template <int NS, bool CK>
 hipError_t launch_t(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBwdArgs &a, char *ws, hipStream_t st) {
   using T = Tiles<NS>;
@@ -754,20 +859,30 @@ hipError_t launch_t(const CoeffsBwdPlan &p, int64_t B, int64_t C, const CoeffsBw
   const uint32_t cvec = (uint32_t)(C / 8), blocks = (uint32_t)ckpt_blocks(C), rows = (uint32_t)B;
   const u32x4 *dF = static_cast<const u32x4 *>(a.dF_pre);
   hipError_t e;
-  pre_dots_kernel<NS, CK, 4><<<wgs(B, 1, 1u << 22), 256, 0, st>>>(a.X.x, a.X.scales, dF, dpre, rows, cvec, blocks);
+  const double inv_k = 1.0 / ((double)NS * (double)C);
+  if (fused_dots<NS>(B, C)) {
+    if constexpr (NS < 8)
+      coeffs_bwd_kernel<NS><<<(uint32_t)p.sum_blocks, coeff_threads<NS, true>(), 0, st>>>(
+          Dots<CK>{a.X.x, a.X.scales, dF, cvec, blocks}, a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre,
+          a.b_post, a.b_res, a.dH, dpre, a.H, records, sums, rows, inv_k);
+  } else {
+    pre_dots_kernel<NS, CK, 4><<<wgs(B, 1, 1u << 22), 256, 0, st>>>(a.X.x, a.X.scales, dF, dpre, rows, cvec, blocks);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    coeffs_bwd_kernel<NS><<<(uint32_t)p.sum_blocks, coeff_threads<NS, false>(), 0, st>>>(
+        NoDots{}, a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre, a.b_post, a.b_res, a.dH, dpre, a.H,
+        records, sums, rows, inv_k);
+  }
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  coeffs_bwd_kernel<NS><<<(uint32_t)p.sum_blocks, sum_threads<NS>(), 0, st>>>(
-      a.logits, a.r, a.alpha[0], a.alpha[1], a.alpha[2], a.b_pre, a.b_post, a.b_res, a.dH, dpre, a.H, records, sums,
-      rows, 1.0 / ((double)NS * (double)C));
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  dx_dphi_kernel<NS, CK><<<(uint32_t)(p.slices * p.split), 64 * T::GROUPS * p.wc, 0, st>>>(
+  const uint32_t slices = (uint32_t)p.slices, split = (uint32_t)p.split;
+  const Sums join{sums, (int)p.sum_blocks, a.dalpha, a.db_pre, a.db_post, a.db_res};
+  dx_dphi_kernel<NS, CK><<<slices * split + (split == 1 ? 1 : 0), 64 * T::GROUPS * p.wc, 0, st>>>(
       static_cast<const char *>(a.X.x), a.X.scales, static_cast<const uint16_t *>(a.phi),
-      static_cast<const char *>(a.dX_next), static_cast<const char *>(a.dF_pre), records, static_cast<char *>(a.dX), part, rows, cvec, blocks, (uint32_t)p.slices, p.wc);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const uint64_t vecs = p.split > 1 ? (uint64_t)NS * C * T::N / 4 : 0;
-  join_kernel<<<T::N + 3 + wgs(vecs, 64, 1u << 20), 256, 0, st>>>(
-      sums, (int)p.sum_blocks, NS, a.dalpha, a.db_pre, a.db_post, a.db_res, reinterpret_cast<const f32x4 *>(part),
-      reinterpret_cast<f32x4 *>(a.dphi), vecs, (uint32_t)p.split);
+      static_cast<const char *>(a.dX_next), static_cast<const char *>(a.dF_pre), records, static_cast<char *>(a.dX),
+      part, rows, cvec, blocks, slices, split, p.wc, join);
+  if ((e = hipGetLastError()) != hipSuccess || split == 1) return e;
+  const uint64_t vecs = (uint64_t)NS * C * T::N / 4;
+  join_kernel<NS><<<T::N + 3 + wgs(vecs, 64, 1u << 20), 256, 0, st>>>(
+      join, reinterpret_cast<const f32x4 *>(part), reinterpret_cast<f32x4 *>(a.dphi), vecs, split);
   return hipGetLastError();
 }
 
@@ -797,6 +912,14 @@ CoeffsBwdPlan plan_n(int64_t B, int64_t C) {
   if (split < (room < tiles / kMinTiles ? room : tiles / kMinTiles)) split = room < tiles / kMinTiles ? room : tiles / kMinTiles;
   if (split > tiles) split = tiles;
   if (split < 1) split = 1;
+  // One range, which needs no join, where its further tiles cost less than the
+  // join's launch and the copies of dphi, written and read (in us, measured:
+  // 2 a tile at n = 4 and 8, 0.7 and 0.3 at n = 2 and 1; 2.7 a launch; 6 TB/s.
+  // 16 rows of n=4, C=512: 18.1 us with one range or several, 20.7 with the
+  // join; 60 rows of n=8, C=7168: 40 with one range, 53 with two; 120 rows of
+  // n=4, C=512: 34 with one range, 20 with eight).
+  const double tile_us = T::JW * (T::MT + 1) / 6.0, copy_us = (double)K * T::N * 8 / 6e6;
+  if ((double)(tiles - (tiles + split - 1) / split) * tile_us <= 2.7 + (double)split * copy_us) split = 1;
   p.split = split;
   const int64_t per = sum_threads<NS>() / (NS * NS), groups = (B + per - 1) / per;
   p.sum_blocks = groups < kMaxSumBlocks ? groups : kMaxSumBlocks;

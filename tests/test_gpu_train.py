@@ -299,6 +299,19 @@ def test_layer_gradients_match_oracle(B, n, C, x):
     _check_coeffs_pre(inp, held, xv, dH, B, n, C)
 
 
+@pytest.mark.parametrize("x", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,n,C", [(30, 4, 512), (16, 4, 1024), (34, 4, 1032), (250, 4, 40), (64, 2, 512), (31, 2, 1024),
+                                   (200, 2, 264), (61, 1, 1024), (259, 1, 512), (118, 1, 2048), (30, 8, 2056),
+                                   (55, 8, 1160)])
+def test_layer_gradients_of_few_rows(B, n, C, x):
+    """Both sides of the choices by size: row dot products in the coefficient
+    kernel or before it, dphi from one range of rows or from several."""
+    _say(f"layer gradients of few rows B={B} n={n} C={C} x={x}")
+    inp = _inputs(B, n, C, seed=B + 7 * C + n)
+    held, xv = _held(inp, x, n, C)
+    _check_coeffs_pre(inp, held, xv, _check_post_res(inp, held, xv, B, n, C), B, n, C)
+
+
 def test_one_stream_has_no_res_gradient():
     """n = 1: H_res is 1 exactly, so its bias gets exactly nothing."""
     inp = _inputs(50, 1, 64, seed=3)
