@@ -145,11 +145,13 @@ __global__ __launch_bounds__(kThreads) void join_runs_kernel(const u64 *__restri
 
 // The same for the first level, whose runs are the tiles: their tokens fit
 // LDS (64 KiB), where a step of the searches costs a tenth of what it does in
-// the cache.  Of equal tokens the rows of an earlier tile come first.
+// the cache.  Of equal tokens the rows of an earlier tile come first.  TILES:
+// kJoin, or fewer where there are no more.
 constexpr uint32_t kJoinThreads = 512;  // a workgroup's keys are of one tile
+template <uint32_t TILES>
 __global__ __launch_bounds__(kJoinThreads) void join_tiles_kernel(const u64 *__restrict__ in, u64 *__restrict__ out,
                                                                   uint32_t B) {
-  constexpr uint32_t kAll = kJoin * kTile, kLoads = kAll / 2 / kJoinThreads;
+  constexpr uint32_t kAll = TILES * kTile, kLoads = kAll / 2 / kJoinThreads;
   __shared__ uint32_t tok[kAll];
   const uint32_t p = blockIdx.x * kJoinThreads + threadIdx.x;
   const uint32_t first = p / kAll * kAll, count = B - first < kAll ? B - first : kAll;
@@ -168,12 +170,12 @@ __global__ __launch_bounds__(kJoinThreads) void join_tiles_kernel(const u64 *__r
   if (p >= B) return;
   const u64 key = in[p];
   const uint32_t mine = (p - first) / kTile, token = token_of(key);
-  uint32_t less[kJoin];
+  uint32_t less[TILES];
 #pragma unroll
-  for (uint32_t u = 0; u < kJoin; ++u) less[u] = 0;
+  for (uint32_t u = 0; u < TILES; ++u) less[u] = 0;
   for (uint32_t step = kTile; step > 0; step >>= 1) {
 #pragma unroll
-    for (uint32_t u = 0; u < kJoin; ++u) {
+    for (uint32_t u = 0; u < TILES; ++u) {
       // (places past the last key hold ~0, which no token exceeds)
       const uint32_t upto = less[u] + step, there = tok[u * kTile + (upto <= kTile ? upto : kTile) - 1];
       const bool before = there < token || (there == token && u < mine);
@@ -182,7 +184,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_tiles_kernel(const u64 *__r
   }
   uint32_t place = first;
 #pragma unroll
-  for (uint32_t u = 0; u < kJoin; ++u) place += u == mine ? p - first - mine * kTile : less[u];
+  for (uint32_t u = 0; u < TILES; ++u) place += u == mine ? p - first - mine * kTile : less[u];
   out[place] = key;
 }
 
@@ -431,10 +433,19 @@ hipError_t table_n(const EmbedBwdPlan &p, int64_t B, int64_t C, int64_t V, const
   if ((e = hipGetLastError()) != hipSuccess) return e;
   int log_run = 10;
   for (uint64_t run = kTile; run < (uint64_t)B; run *= kJoin, log_run += 4) {
-    if (run == kTile)
-      join_tiles_kernel<<<(uint32_t)((B + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, st>>>(keys, other, rows);
-    else
+    if (run == kTile) {  // (a call of 1100 rows: 21 us with two tiles, 28 with kJoin)
+      const uint32_t grid = (uint32_t)((B + kJoinThreads - 1) / kJoinThreads);
+      if (B <= 2 * kTile)
+        join_tiles_kernel<2><<<grid, kJoinThreads, 0, st>>>(keys, other, rows);
+      else if (B <= 4 * kTile)
+        join_tiles_kernel<4><<<grid, kJoinThreads, 0, st>>>(keys, other, rows);
+      else if (B <= 8 * kTile)
+        join_tiles_kernel<8><<<grid, kJoinThreads, 0, st>>>(keys, other, rows);
+      else
+        join_tiles_kernel<kJoin><<<grid, kJoinThreads, 0, st>>>(keys, other, rows);
+    } else {
       join_runs_kernel<<<(uint32_t)((B + kThreads - 1) / kThreads), kThreads, 0, st>>>(keys, other, rows, run, log_run);
+    }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     std::swap(keys, other);
   }

@@ -475,7 +475,7 @@ def test_embedding_matches_oracle(B, n, C, V, how):
 
 
 @pytest.mark.parametrize("how", ["any", "padded", "one"])
-@pytest.mark.parametrize("B,n,C,V", [(17001, 2, 4104, 900), (40000, 1, 8, 70000), (16384, 1, 520, 2)])
+@pytest.mark.parametrize("B,n,C,V", [(17001, 2, 4104, 900), (40000, 1, 8, 70000), (16384, 1, 520, 2), (2048, 2, 16, 300), (6001, 1, 16, 900)])
 def test_embedding_gradient_of_many_rows(B, n, C, V, how):
     """More rows than one joining pass sorts, long blocks, and tokens whose
     rows span hundreds of blocks (64-bit sums by torch)."""
