@@ -482,10 +482,11 @@ EmbedBwdPlan plan_embed_bwd(int64_t B, int64_t C) {
   const int64_t slices = (C + 511) / 512;
   // Long blocks where there are rows enough for one round of waves (4 on each
   // SIMD of the 256 compute units), short ones for latency otherwise: at n=4,
-  // C=7168, B=16384 64 rows a block take 380 us, 32 397; 1001 rows of C=1000
-  // take 21 us with 8.
-  p.rb = 8;
-  while (p.rb < 64 && B * slices / p.rb > 4096) p.rb *= 2;
+  // C=7168, B=16384 64 rows a block take 380 us, 32 397; with few waves n=4,
+  // C=256, B=3000 takes 21.5 us with 4, 24 with 8, n=2, C=1000, B=1001 17.5
+  // with 4, 18.5 with 8.
+  p.rb = 4;
+  while (p.rb < 64 && B * slices / p.rb > (p.rb == 4 ? 1024 : 4096)) p.rb *= 2;
   const size_t list = ((size_t)B * 8 + 15) / 16 * 16;
   p.keys = 0;
   p.other = list;
