@@ -448,8 +448,13 @@ struct Sums {
 // X_t's place in LDS and is stored from there, four or eight lanes a row.  A
 // tile's record is staged the same way.
 //
-// Measured at n=4, C=7168, B=16384 from the checkpoint: 500 us for 2.6 GB
-// (5.2 TB/s); without any arithmetic the same loads and stores take 490.
+// Measured at n=4, C=7168, B=16384 from the checkpoint: 495 us for 2.6 GB of
+// tensors (5.3 TB/s; with the records, read once a slice, 5.6).  The same
+// loads and stores without the arithmetic took 490 (with a run of rows a
+// range): bound by HBM and the order in which it is reached.  At n=8, C=4096,
+// B=8192 from the stream 410 us for 1.7 GB (4.1 TB/s): the registers of a
+// compute unit hold phi and dphi of 64 channels, so rows are read 128 bytes at
+// a time.
 //
 // Waits: vmcnt counts in order, and between a tile's loads and their use the
 // wave issues the loads and dX stores of the tiles in between and no other

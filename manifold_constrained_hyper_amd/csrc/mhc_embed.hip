@@ -19,6 +19,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// A lane reads eight channels of the table's row and writes them to every
+// stream.  Bound by the writes: 184 us at n=4, C=7168, B=16384 (1.01 GB, of
+// which 0.94 are X_0; 5.5 TB/s); one token takes a launch (6.3 us).
 template <int NS>
 __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t *__restrict__ tokens,
                                                          const u32x4 *__restrict__ table, float scale,
@@ -46,7 +49,9 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t *__restri
 // order.  Tiles of 1024 keys are sorted in one workgroup each; then runs are
 // joined 16 at a time: a key's place in the joined run is its place in its
 // own run plus, for each other run, the number of smaller keys there (a
-// binary search).  One launch for up to 1024 rows, two for up to 16384.
+// binary search).  One launch for up to 1024 rows (5.5 us), two for up to
+// 16384 (20 us: the tiles' bitonic sort and the join are chains of lane moves
+// and LDS reads).
 typedef unsigned long long u64;
 constexpr uint32_t kNoToken = 0xffffffffu;
 constexpr uint32_t kTile = 1024, kJoin = 16;
@@ -222,6 +227,10 @@ __device__ __forceinline__ void write_row(f32x4 *o, const float (&acc)[8], float
 // on write zeros to the table rows that have no token: kZeroBytes or a row each,
 // kZeroRows at most (with 8 rows each the table of n=4, C=7168, B=16384,
 // V=32768 took 405 us, not 396, and V=65536, C=64 with 300 rows 30, not 18).
+//
+// Bound by HBM where there are many rows: 326 us of the call's 398 at n=4,
+// C=7168, B=16384, V=32768, for 0.94 GB of dX_0 and 0.94 of the table (5.7
+// TB/s); by latency where there are few (7 us at n=2, C=1000, B=1001).
 constexpr int kAhead = 16;  // 16-byte loads a lane has in flight
 constexpr uint32_t kZeroRows = 32, kZeroBytes = 1 << 14;
 
