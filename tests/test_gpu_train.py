@@ -517,6 +517,56 @@ def test_embedding_gradient_of_few_rows(B, n, C, V):
     assert bool(((d.t.double() - want).abs() <= (B * n + 2) * U * total).all())
 
 
+def test_offsets_past_32_bits():
+    """A stream of more than 2^32 values and a table of more than 2^31: the last
+    rows come out as they do in a call of their own."""
+    B, n, C, last = 66000, 8, 8192, 2048
+    _say(f"offsets past 32 bits B={B} n={n} C={C}")
+    N, e = n * n + 2 * n, lambda *s, d=torch.float32: torch.empty(*s, dtype=d, device="cuda")
+    b = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    X, G = (e(B, n * C, d=b).normal_(generator=gen) for _ in range(2))
+    F, dFp = (e(B, C, d=b).normal_(generator=gen) for _ in range(2))
+    phi = (torch.randn(n * C, N, generator=gen, device="cuda") / 256).to(b)
+    logits, H = torch.randn(B, N, generator=gen, device="cuda"), torch.rand(B, N, generator=gen, device="cuda")
+    r = torch.rand(B, generator=gen, device="cuda") + 0.5
+    bias = [torch.randn(k, generator=gen, device="cuda") for k in (n, n, n * n)]
+
+    def calls(lo, hi):
+        m, s = hi - lo, slice(lo, hi)
+        codes, scales = e(m, n * C, d=torch.uint8), e(m, mhc.mhc_ckpt_scales_per_row(n, C), d=torch.uint8)
+        mhc.mhc_ckpt_pack(m, n, C, X[s], codes, scales)
+        dF, dH, dX = e(m, C, d=b), e(m, N), e(m, n * C, d=b)
+        mhc.mhc_post_res_bwd_ckpt(m, n, C, codes, scales, F[s], H[s], G[s], dF, dH)
+        ws = e(mhc.mhc_coeffs_pre_bwd_workspace_size(m, n, C), d=torch.uint8)
+        grads = [e(n * C, N), e(3), e(n), e(n), e(n * n)]
+        mhc.mhc_coeffs_pre_bwd_ckpt(m, n, C, codes, scales, phi, 0.5, 0.5, 0.5, *bias, logits[s], r[s], H[s], G[s], dH,
+                                    dFp[s], dX, *grads, ws)
+        assert all(bool(torch.isfinite(g).all()) for g in grads)
+        back = e(last, n * C, d=b)
+        mhc.mhc_ckpt_unpack(last, n, C, codes[m - last:], scales[m - last:], back)
+        return [t[m - last:].clone() for t in (codes, scales, dF, dH, dX)] + [back]
+
+    for whole, own in zip(calls(0, B), calls(B - last, B)):
+        assert torch.equal(whole, own)
+
+    del X
+    V = 2 ** 31 // C + 1000
+    table = e(V, C, d=b).normal_(generator=gen)
+    tokens = torch.randint(0, V, (B,), generator=gen, device="cuda")
+    tokens[-last:] = torch.randperm(last, generator=gen, device="cuda") + V - last
+    tokens[:-last] %= V - last
+    X_0 = e(B, n * C, d=b)
+    mhc.mhc_embed(B, n, C, V, tokens, table, 2.0, X_0)
+    assert torch.equal(X_0[-last:].view(last, n, C), (2 * table[tokens[-last:]])[:, None].expand(last, n, C))
+    ws = e(mhc.mhc_embed_bwd_workspace_size(B, n, C, V), d=torch.uint8)
+    dtable = e(V, C)
+    mhc.mhc_embed_bwd(B, n, C, V, tokens, G, 2.0, dtable, ws)
+    g = G[-last:].view(last, n, C).double()
+    want, total = 2 * g.sum(1), 2 * g.abs().sum(1)
+    assert bool(((dtable[tokens[-last:]].double() - want).abs() <= (n + 2) * U * total).all())
+
+
 # -- a training step --------------------------------------------------------------------------------
 
 class Model:
