@@ -40,20 +40,82 @@ struct Tiles {
   static constexpr int JW = NS == 8 ? 2 : NS;   // streams a wave forms dX and dphi of
   static constexpr int GROUPS = NS / JW;        // waves that share a tile of rows and channels
   static constexpr int CW = 32;                 // channels a wave
-  // What dx_dphi_kernel needs of a tile of 16 rows, written by coeffs_bwd_kernel
-  // (byte offsets in the tile's record; every part is a multiple of 16):
-  //   rows_b  [hi, mid][KS][lane][8] bf16  B operand of dlogit . phi^T: lane
-  //           16 q + i has coefficients 32 ks + 8 q .. + 7 of row i
-  //   cols_a  [MT][lane][8] bf16  A operand of dphi^T += dlogit^T X: lane
-  //           16 q + m has hi, then mid, of rows 4 q .. + 3 of coefficient 16 mt + m
-  //   cols_c  [MT][lane][4] bf16  the same with the low parts
-  //   mix     [KH][16 rows] fp32  H_pre and H_res
-  //   turn    [16 rows] fp32      the factor of X_t that r contributes
+  // What dx_dphi_kernel needs of a tile of 16 rows, a record written by
+  // coeffs_bwd_kernel: dlogit, then the factors of dX
+  //   mix   [KH][16 rows] fp32  H_pre and H_res
+  //   turn  [16 rows] fp32      the factor of X_t that r contributes
   static constexpr int KH = NS + NS * NS;
-  static constexpr int kColsA = 2 * KS * 1024, kColsC = kColsA + MT * 1024, kMix = kColsC + MT * 512;
-  static constexpr int kTurn = kMix + KH * 64, kBytes = kTurn + 64;
-  static constexpr int kChunks = (kBytes + 1023) / 1024, kStride = kChunks * 1024;
+  // dlogit as the matrix core's operands (byte offsets; every part is a
+  // multiple of 16), bf16 parts whose sum is dlogit to 2^-17 (hi + mid: for
+  // dX, which is rounded to bf16) or 2^-25 (hi + mid + low: for dphi, fp32) of
+  // it:
+  //   rows_b  [hi, mid][KS][lane][8]  B operand of dlogit . phi^T: lane
+  //           16 q + i has coefficients 32 ks + 8 q .. + 7 of row i
+  //   cols_a  [MT][lane][8]  A operand of dphi^T += dlogit^T X: lane 16 q + m
+  //           has hi, then mid, of rows 4 q .. + 3 of coefficient 16 mt + m
+  //   cols_c  [MT][lane][4]  the same with the low parts
+  static constexpr int kColsA = 2 * KS * 1024, kColsC = kColsA + MT * 1024, kOperands = kColsC + MT * 512;
+  // At n = 4 a tile's dlogit goes out as it is, [16][N] fp32, and
+  // dx_dphi_kernel forms the operands in LDS: they have 3.3 times the bytes,
+  // read by every workgroup along the channels (625 us against 638 at C=7168,
+  // B=16384 from the checkpoint; few rows take 0.3 us longer).  At n = 8, with
+  // 80 coefficients, forming them there costs more than the bytes (570 us
+  // against 552 at C=4096, B=8192), and at n = 1 and 2 the tiles are short
+  // (n=1, B=120: 23 us against 20).
+  static constexpr bool kLate = NS == 4;
+  static constexpr int kDlogit = kLate ? 16 * N * 4 : kOperands;
+  static constexpr int kTurn = kDlogit + KH * 64, kEnd = kTurn + 64, kMix = kEnd - kDlogit;
+  static constexpr int kStride = kLate ? kEnd : (kEnd + 1023) / 1024 * 1024;
 };
+
+__device__ __forceinline__ float bf16_round(float x) { return bf16_lo(pack_bf16x2(x, 0.f)); }
+
+// One wave's part `item` (below KS: a step of rows_b, then a tile of cols) of
+// a tile's operands, from its dlogit dl[row * STRIDE + coefficient].
+// Coefficients past N are zeros.
+template <int NS, int STRIDE>
+__device__ __forceinline__ void form_operands(const float *dl, int item, int lane, char *to) {
+  using T = Tiles<NS>;
+  constexpr int N = T::N, KS = T::KS;
+  const int lo16 = lane & 15, q = lane >> 4;
+  if (item < KS) {
+    const int k0 = 32 * item + 8 * q;
+    float v[8];
+    if constexpr (STRIDE % 4 == 0) {
+      f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+      if (k0 < N) {
+        const f32x4 *row = reinterpret_cast<const f32x4 *>(dl + lo16 * STRIDE + k0);
+        a = row[0], b = row[1];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = k0 + j < N ? dl[lo16 * STRIDE + k0 + j] : 0.f;
+    }
+    u32x4 hi, mid;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      mid[j] = pack_bf16x2(v[2 * j] - bf16_lo(hi[j]), v[2 * j + 1] - bf16_hi(hi[j]));
+    }
+    reinterpret_cast<u32x4 *>(to)[item * 64 + lane] = hi;
+    reinterpret_cast<u32x4 *>(to)[(KS + item) * 64 + lane] = mid;
+  } else {
+    const int mt = item - KS, k = 16 * mt + lo16;
+    float v[4], h[4], m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = k < N ? dl[(4 * q + j) * STRIDE + k] : 0.f;
+      h[j] = bf16_round(v[j]);
+      m[j] = bf16_round(v[j] - h[j]);
+      v[j] = v[j] - h[j] - m[j];
+    }
+    reinterpret_cast<u32x4 *>(to + T::kColsA)[mt * 64 + lane] =
+        u32x4{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(m[0], m[1]), pack_bf16x2(m[2], m[3])};
+    reinterpret_cast<u32x2 *>(to + T::kColsC)[mt * 64 + lane] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  }
+}
 
 // dH_pre [B, n]: a workgroup a row (103 us at n=4, C=7168, B=16384 from the
 // checkpoint: 0.72 GB at 7.0 TB/s).
@@ -161,14 +223,9 @@ __device__ __forceinline__ double recip(double x) {  // two steps: 2^-23, 2^-46,
 // with 49 degrees of freedom, fp32's errors stay under 4e-7 of the sums, and
 // 64 bits would not fit the registers of 1024 threads.
 //
-// dlogit leaves in the tiles' records, in the matrix core's operand order,
-// split into bf16 parts whose sum is dlogit to 2^-17 (hi + mid: for dX, which
-// is rounded to bf16) or 2^-25 (hi + mid + low: for dphi, fp32) of it.  Rows
-// past the last and coefficients past N are zeros.
+// dlogit leaves in tiles of 16 rows; rows past the last are zeros.
 template <int NS>
 constexpr int sum_threads() { return NS == 8 ? 1024 : 256; }  // a multiple of 16 rows a workgroup
-
-__device__ __forceinline__ float bf16_round(float x) { return bf16_lo(pack_bf16x2(x, 0.f)); }
 
 // With Dots (where X_t is), the row dot products are formed here too, by eight
 // waves, rather than in a launch of their own.
@@ -237,7 +294,8 @@ __global__ __launch_bounds__((coeff_threads<NS, kFused<D>>())) void coeffs_bwd_k
     D dots, const float *__restrict__ logits, const float *__restrict__ r_in, float alpha_pre, float alpha_post,
     float alpha_res, const float *__restrict__ b_pre, const float *__restrict__ b_post,
     const float *__restrict__ b_res, const float *__restrict__ dH, const float *__restrict__ dpre,
-    const float *__restrict__ H, char *__restrict__ records, double *__restrict__ sums, uint32_t B, double inv_k) {
+    const float *__restrict__ H, char *__restrict__ records, double *__restrict__ sums,
+    uint32_t B, double inv_k) {
   using T = Tiles<NS>;
   constexpr int TH = coeff_threads<NS, kFused<D>>();
   constexpr int NN = NS * NS, N = NN + 2 * NS, R = sum_threads<NS>() / NN;
@@ -320,42 +378,19 @@ __global__ __launch_bounds__((coeff_threads<NS, kFused<D>>())) void coeffs_bwd_k
       }
     }
     __syncthreads();
-    const auto at_row = [&](int i, int k) { return k < N ? sh.dl[i][k] : 0.f; };
-    constexpr int kItems = T::KS + T::MT;  // rows_b steps (both parts at once), then cols tiles
     const uint32_t tiles = (B + 15) / 16;
-    for (int w = threadIdx.x; w < R / 16 * kItems * 64; w += TH) {
-      const int lane = w & 63, item = (w >> 6) % kItems, tl = (w >> 6) / kItems;
-      const size_t tile = row0 / 16 + tl;
-      if (tile >= tiles) continue;
-      char *rec = records + tile * T::kStride;
-      const int lo16 = lane & 15, q = lane >> 4;
-      if (item < T::KS) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = at_row(tl * 16 + lo16, 32 * item + 8 * q + j);
-        u32x4 hi, mid;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          hi[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-          mid[j] = pack_bf16x2(v[2 * j] - bf16_lo(hi[j]), v[2 * j + 1] - bf16_hi(hi[j]));
-        }
-        u32x4 *rows_b = reinterpret_cast<u32x4 *>(rec);
-        rows_b[item * 64 + lane] = hi;
-        rows_b[(T::KS + item) * 64 + lane] = mid;
-      } else {
-        const int mt = item - T::KS;
-        float v[4], h[4], m[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = at_row(tl * 16 + 4 * q + j, 16 * mt + lo16);
-          h[j] = bf16_round(v[j]);
-          m[j] = bf16_round(v[j] - h[j]);
-          v[j] = v[j] - h[j] - m[j];
-        }
-        reinterpret_cast<u32x4 *>(rec + T::kColsA)[mt * 64 + lane] = u32x4{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]),
-                                                        pack_bf16x2(m[0], m[1]), pack_bf16x2(m[2], m[3])};
-        reinterpret_cast<u32x2 *>(rec + T::kColsC)[mt * 64 + lane] =
-            u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    if constexpr (T::kLate) {
+      for (int w = threadIdx.x; w < R * N; w += TH) {
+        const int i = w / N, k = w - i * N;
+        if (row0 + i < tiles * 16)
+          reinterpret_cast<float *>(records + (size_t)(row0 + i) / 16 * T::kStride)[(i & 15) * N + k] = sh.dl[i][k];
+      }
+    } else {
+      constexpr int kItems = T::KS + T::MT;
+      for (int w = threadIdx.x >> 6; w < R / 16 * kItems; w += TH / 64) {
+        const size_t tile = row0 / 16 + w / kItems;
+        if (tile < tiles)
+          form_operands<NS, NP>(sh.dl[w / kItems * 16], w % kItems, threadIdx.x & 63, records + tile * T::kStride);
       }
     }
     for (int w = threadIdx.x; w < R * (T::KH + 1); w += TH) {
@@ -372,7 +407,7 @@ __global__ __launch_bounds__((coeff_threads<NS, kFused<D>>())) void coeffs_bwd_k
       } else if (row < B) {
         x = H[row * N + (k < NS ? k : k + NS)];  // the post block is not needed
       }
-      reinterpret_cast<float *>(records + tile * T::kStride + T::kMix)[k * 16 + i] = x;
+      reinterpret_cast<float *>(records + tile * T::kStride + T::kDlogit)[k * 16 + i] = x;
     }
     __syncthreads();
   }
@@ -445,16 +480,19 @@ struct Sums {
 // at a time at n = 4, 128 at n = 8), one or two tiles ahead, without
 // registers; a row's 16-byte pieces are exchanged by an xor with the row, so
 // that the reads in the matrix layout meet no bank twice.  dX takes G's or
-// X_t's place in LDS and is stored from there, four or eight lanes a row.  A
-// tile's record is staged the same way.
+// X_t's place in LDS and is stored from there, four or eight lanes a row.
 //
-// Measured at n=4, C=7168, B=16384 from the checkpoint: 495 us for 2.6 GB of
-// tensors (5.3 TB/s; with the records, read once a slice, 5.6).  The same
-// loads and stores without the arithmetic took 490 (with a run of rows a
-// range): bound by HBM and the order in which it is reached.  At n=8, C=4096,
-// B=8192 from the stream 410 us for 1.7 GB (4.1 TB/s): the registers of a
-// compute unit hold phi and dphi of 64 channels, so rows are read 128 bytes at
-// a time.
+// A tile's record is staged the same way; where the operands are formed here,
+// dlogit one tile further ahead: the waves form a share each, a tile before
+// the use.
+//
+// Measured at n=4, C=7168, B=16384 from the checkpoint: 460 to 485 us on three
+// cards for 2.6 GB of tensors (5.4 to 5.7 TB/s).  Without the arithmetic the
+// call's 638 us were 619: bound by HBM and the order in which it is reached.
+// At n=8, C=4096, B=8192 from the stream 400 us for 1.7 GB (4.3 TB/s): the
+// registers of a compute unit hold phi and dphi of 64 channels, so rows are
+// read 128 bytes at a time (without the arithmetic the call took 510 us, not
+// 545; with 1 KB of the record instead of 19, 495).
 //
 // Waits: vmcnt counts in order, and between a tile's loads and their use the
 // wave issues the loads and dX stores of the tiles in between and no other
@@ -494,7 +532,7 @@ struct Stage {
   // shared that of X_t, or (from codes) a place of its own.
   static constexpr bool kOwnOut = kShared && CK;
   static constexpr int kOutBytes = kOwnOut ? kWaves * T::JW * 1024 : 16;
-  // Loads a wave issues for a tile at least (without its share of the record),
+  // Loads a wave issues for a tile at least (without its share of dlogit and mix),
   // and its stores of a tile: what may be younger than a tile's loads.
   static constexpr int kLoads = (kShared ? T::JW : NS + 1) + (CK ? T::JW / 2 + 1 : T::JW);
   static constexpr int kStores = T::JW;
@@ -511,8 +549,9 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
   using S = Stage<NS, CK>;
   constexpr int N = T::N, KS = T::KS, MT = T::MT, JW = T::JW, GROUPS = T::GROUPS;
   __shared__ __attribute__((aligned(1024))) char stage[S::kStages][S::kBytes];
-  __shared__ __attribute__((aligned(1024))) char record[S::kStages][T::kStride];
-  __shared__ __attribute__((aligned(1024))) char own_out[S::kOutBytes];
+  __shared__ __attribute__((aligned(16))) char record[S::kStages][T::kStride];
+  __shared__ __attribute__((aligned(16))) char formed[T::kLate ? 2 : 1][T::kLate ? T::kOperands : 16];
+  __shared__ __attribute__((aligned(16))) char own_out[S::kOutBytes];
   if (blockIdx.x == slices * split) {  // with one row range there is no join_kernel
     for (int k = threadIdx.x; k < N + 3; k += blockDim.x) {
       double a = 0.0;
@@ -543,7 +582,16 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
   const auto turn = [](int row, int l) { return l >= 4 ? row : (row >> (4 - l)) & ((1 << l) - 1); };
   const auto piece_of = [&](int row, int p, int l) { return ((row << l) + (p ^ turn(row, l))) * 16; };
 
-  const auto issue = [&](uint32_t tile, int st) {
+  const auto issue_part = [&](uint32_t tile, int from, auto bytes, int st) {
+    constexpr int count = decltype(bytes)::value;
+    const char *src = records + (size_t)tile * T::kStride + from;
+    for (int k = wave * 1024; k < count; k += waves * 1024)
+      if (count % 1024 == 0 || k + lane * 16 < count) dma<16>(src + k + lane * 16, lds_addr_of(record[st]) + from + k);
+  };
+  // A tile's tensors and mix, and its dlogit or (where the operands are formed
+  // here, a tile before their use) the next one's.
+  const auto issue = [&](uint32_t k, int st) {
+    const uint32_t tile = tile_at(k);
     const char *zero = reinterpret_cast<const char *>(g_train_zero);
     const uint32_t at = lds_addr_of(stage[st]), row0 = tile * 16;
     // bf16 tiles: KiB cw of a stream's.
@@ -587,12 +635,22 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
                  : zero,
              at + S::kG + S::kX + S::kF + (uint32_t)wave * 256);
     }
-    for (int k = wave; k < T::kChunks; k += waves)
-      dma<16>(records + (size_t)tile * T::kStride + k * 1024 + lane * 16, lds_addr_of(record[st]) + k * 1024);
+    if constexpr (T::kLate) {
+      issue_part(tile, T::kDlogit, std::integral_constant<int, T::kMix>{}, st);
+      if (k + 1 < count) issue_part(tile_at(k + 1), 0, std::integral_constant<int, T::kDlogit>{}, st + 1 == S::kStages ? 0 : st + 1);
+    } else {
+      issue_part(tile, 0, std::integral_constant<int, T::kStride>{}, st);
+    }
   };
+  const auto form = [&](const char *dl, char *to) {
+    if constexpr (T::kLate)
+      for (int item = wave; item < KS + MT; item += waves)
+        form_operands<NS, N>(reinterpret_cast<const float *>(dl), item, lane, to);
+  };
+  if constexpr (T::kLate) issue_part(tile_at(0), 0, std::integral_constant<int, T::kDlogit>{}, 0);
 #pragma unroll
   for (int k = 0; k < S::kDist; ++k)
-    if ((uint32_t)k < count) issue(tile_at(k), k);
+    if ((uint32_t)k < count) issue(k, k);
 
   // phi: operand (stream, t, ks), lane 16 q + m: coefficients 32 ks + 8 q .. + 7
   // of the wave's channel 8 (m / 4) + 4 t + m % 4.
@@ -636,6 +694,13 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
   // Where all of the wave's pieces have channels, every store is issued each
   // tile.
   const bool full = v_wave + 4 <= cvec;
+  if constexpr (T::kLate) {
+    // (The builtin, so that the compiler knows phi's loads to have ended and
+    // puts no wait of its own into the loop.)
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
+    form(record[0], formed[0]);
+  }
   int st = 0;  // the tile's stage
   for (uint32_t k = 0; k < count; ++k) {
     const uint32_t tile = tile_at(k);
@@ -646,10 +711,11 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
     // The other waves' share of the tile has landed, and everybody has read
     // the last of the stage that the next loads fill.
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (k + S::kDist < count) issue(tile_at(k + S::kDist), st == 0 ? S::kStages - 1 : st - 1);
+    if (k + S::kDist < count) issue(k + S::kDist, st == 0 ? S::kStages - 1 : st - 1);
     char *mine = stage[st];
-    const char *now = record[st];
+    const char *now = T::kLate ? formed[T::kLate ? k & 1 : 0] : record[st], *factors = record[st] + T::kDlogit;
     st = st + 1 == S::kStages ? 0 : st + 1;
+    if (T::kLate && k + 1 < count) form(record[st], formed[T::kLate ? (k + 1) & 1 : 0]);
     const char *const f_at = mine + S::kG + S::kX;
     const uint32_t *const s_at = reinterpret_cast<const uint32_t *>(f_at + S::kF + wave * 256);
     bf16x8 bh[KS], bm[KS];
@@ -658,8 +724,8 @@ __global__ __launch_bounds__(512, 2) void dx_dphi_kernel(
       bh[ks] = reinterpret_cast<const bf16x8 *>(now)[ks * 64 + lane];
       bm[ks] = reinterpret_cast<const bf16x8 *>(now)[(KS + ks) * 64 + lane];
     }
-    const float *mix = reinterpret_cast<const float *>(now + T::kMix) + lo16;
-    const float c = reinterpret_cast<const float *>(now + T::kTurn)[lo16];
+    const float *mix = reinterpret_cast<const float *>(factors) + lo16;
+    const float c = mix[T::KH * 16];
     const bf16x8 *cols_a = reinterpret_cast<const bf16x8 *>(now + T::kColsA) + lane;
     const u32x2 *cols_c = reinterpret_cast<const u32x2 *>(now + T::kColsC) + lane;
     const int at = piece_of(lo16, cw * 4 + q, lg);

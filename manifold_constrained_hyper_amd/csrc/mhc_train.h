@@ -29,8 +29,8 @@ hipError_t launch_post_res_bwd(int n, int64_t B, int64_t C, HeldX X, const void 
                                const void *dX_next, void *dF_out, float *dH, hipStream_t st);
 
 // Workspace of the coefficient and pre-mix gradient (bytes from its start):
-//   records                  a record for each tile of 16 rows: dlogit in bf16
-//                            parts and what else its dX needs of H and r
+//   records                  a record for each tile of 16 rows: dlogit and what
+//                            else its dX needs of H and r
 //                            (mhc_coeffs_pre_bwd.hip)
 //   dpre   fp32 [B, n]       gradient of H_pre
 //   sums   fp64 [sum_blocks, N + 3]  partial sums of the bias and alpha gradients
