@@ -349,18 +349,24 @@ __global__ __launch_bounds__((coeff_threads<NS, kFused<D>>())) void coeffs_bwd_k
           m0 = exp(z);
         else
           m0 = expf(z);
-        real y[2 * IT], inv[2 * IT];
+        real y[IT], inv[2 * IT];  // every second y: the others are a product away (registers)
         const real total = axis_sum<NS, 2>(m0);
         real m = y[0] = m0 / total;
 #pragma unroll
         for (int k = 1; k < 2 * IT; ++k) {
           inv[k] = recip(k % 2 ? axis_sum<NS, 1>(m) : axis_sum<NS, 2>(m));
-          y[k] = m = m * inv[k];
+          m *= inv[k];
+          if (k % 2 == 0) y[k / 2] = m;
         }
         real d = dH[(size_t)row * N + 2 * NS + e];
 #pragma unroll
         for (int k = 2 * IT - 1; k > 0; --k) {
-          const real dy = d * y[k];
+          real yk = y[k / 2];
+          if (k % 2) {
+            asm("" : "+v"(yk));  // (or the compiler keeps the products)
+            yk *= inv[k];
+          }
+          const real dy = d * yk;
           d = (d - (k % 2 ? axis_sum<NS, 1>(dy) : axis_sum<NS, 2>(dy))) * inv[k];
         }
         // dz = m0 (d - sum) / total, with m0 / total = y[0]
