@@ -30,6 +30,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
+// acc + a.lo b.lo + a.hi b.hi of packed bf16 pairs in one instruction (the
+// products are exact in fp32).  The builtin, not inline assembly: another
+// vector instruction may read the result only three wait states later, and
+// the compiler adds them only behind a dot product that it issues itself.
+__device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t b, float acc) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), acc, false);
+}
+
 // FP8 E4M3 (the OCP "fn" encoding: bias 7, max 448, no infinities), four
 // values per 32-bit word, byte k holding element k.  gfx950's conversions use
 // this encoding and round to nearest even; narrowing would give NaN from

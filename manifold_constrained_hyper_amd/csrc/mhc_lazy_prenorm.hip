@@ -34,7 +34,7 @@
 //    (v_permlane32_swap) and stores 16 bytes;
 //  * the row sums of squares run on the vector unit beside the matrix core:
 //    thread t adds the squares of half of row t >> 1 of every A chunk (four
-//    independent partial sums, one v_dot2_f32_bf16 per packed pair);
+//    independent partial sums, one dot2_bf16 per packed pair);
 //  * tiles are walked in groups of 4 tile rows, each XCD taking a contiguous
 //    run of the order.
 #include "mhc_device.h"
@@ -89,14 +89,6 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-}
-
-// lo^2 + hi^2 + acc of a packed bf16 pair in one instruction (bf16 squares
-// are exact in fp32).  Written as inline asm: through the builtin, hipcc
-// passed element 0 of a 4-word vector for every element.
-__device__ __forceinline__ float dot2_sq_bf16(uint32_t v, float acc) {
-  asm("v_dot2_f32_bf16 %0, %1, %1, %0" : "+v"(acc) : "v"(v));
-  return acc;
 }
 
 struct Operands {
@@ -222,7 +214,7 @@ __global__ __launch_bounds__(512, 1) void lazy_prenorm_gemm_kernel(
     for (int p = 0; p < kPieces / 2; ++p)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        ssp[w] = dot2_sq_bf16(sq[p][w], ssp[w]);
+        ssp[w] = dot2_bf16(sq[p][w], sq[p][w], ssp[w]);
       }
   };
 
@@ -488,8 +480,8 @@ __global__ __launch_bounds__(256, 1) void lazy_prenorm_gemm4_kernel(
     if (i >= 8 && i < 12) {
       const int b = (i - 8) >> 1, h = (i - 8) & 1;  // a[b], words 2 h, 2 h + 1
       const u32x4 v = __builtin_bit_cast(u32x4, o.a[b]);
-      ssq[b] = dot2_sq_bf16(v[2 * h], ssq[b]);
-      ssq[b] = dot2_sq_bf16(v[2 * h + 1], ssq[b]);
+      ssq[b] = dot2_bf16(v[2 * h], v[2 * h], ssq[b]);
+      ssq[b] = dot2_bf16(v[2 * h + 1], v[2 * h + 1], ssq[b]);
     }
   };
   // One 16-k step: its 16 MFMAs in a fixed order, `slot(i)` placing other

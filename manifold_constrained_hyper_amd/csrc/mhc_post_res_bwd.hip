@@ -8,8 +8,8 @@
 //
 // Every input is read once; the n + n*n sums over the channels stay in
 // registers (fp32) and are joined over a row's lanes and waves in a fixed
-// order.  Products of two bf16 values go two at a time through v_dot2_f32_bf16
-// (exact products, fp32 sums), straight from the packed words.  The gradient
+// order.  Products of two bf16 values go two at a time through dot2_bf16 (exact
+// products, fp32 sums), straight from the packed words.  The gradient
 // with respect to X_t is not formed here: it needs the gradient of the layer's
 // input, which comes later, and is then one pass over G with everything else
 // that flows into X_t (mhc_coeffs_pre_bwd.hip).
@@ -24,12 +24,6 @@
 namespace mhc {
 
 namespace {
-
-// acc + a.lo b.lo + a.hi b.hi of packed bf16 pairs.
-__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float acc) {
-  asm("v_dot2_f32_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(a), "v"(b));
-  return acc;
-}
 
 // Sums of K values (a multiple of 4) over a wave's lanes.  Two halvings trade
 // half of the values between half-waves, then between rows of 16 lanes, so
@@ -99,7 +93,7 @@ __global__ __launch_bounds__(64 * max_waves<NS>()) void post_res_bwd_kernel(
 #pragma unroll
         for (int e = 0; e < 8; ++e) out[e] = fmaf(hpost[i], gw[e], out[e]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) acc[i] = dot2(g[i][w], f[w], acc[i]);
+        for (int w = 0; w < 4; ++w) acc[i] = dot2_bf16(g[i][w], f[w], acc[i]);
       }
       const u32x4 o = {pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3]), pack_bf16x2(out[4], out[5]),
                        pack_bf16x2(out[6], out[7])};
@@ -110,7 +104,7 @@ __global__ __launch_bounds__(64 * max_waves<NS>()) void post_res_bwd_kernel(
 #pragma unroll
         for (int w = 0; w < 4; ++w)
 #pragma unroll
-          for (int i = 0; i < NS; ++i) acc[NS + i * NS + j] = dot2(g[i][w], xw[w], acc[NS + i * NS + j]);
+          for (int i = 0; i < NS; ++i) acc[NS + i * NS + j] = dot2_bf16(g[i][w], xw[w], acc[NS + i * NS + j]);
       }
     }
     wave_sums(acc);

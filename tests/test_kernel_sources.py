@@ -51,3 +51,10 @@ def test_wait_state_between_m0_and_direct_to_lds_loads():
                 assert b.startswith("s_nop"), (f, template)
         assert not re.match(r"s_\w+ m0\b", lines[-1]), (f, template)
     assert seen
+
+
+def test_no_dot_or_matrix_product_in_inline_assembly():
+    """Another vector instruction may read a dot product's result only three
+    wait states later, and a matrix product's later still."""
+    bad = [(f, t) for f, t, _ in _asm_statements() if re.search(r"\bv_(dot|s?mfma|smfmac|wmma)", t)]
+    assert not bad, bad
