@@ -507,16 +507,24 @@ struct Sums {
 // first and last tiles, waves past the channels) the wait is for all.
 __device__ __attribute__((aligned(256))) uint32_t g_train_zero[64];  // what loads past the edges read
 
+// (M0 is reserved, of which the compiler warns where it is on a clobber list;
+// the entry keeps it from relying on M0's old value.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int BYTES>
 __device__ __forceinline__ void dma(const void *src, uint32_t lds_addr) {  // lane l's data lands at lds_addr + BYTES l
   lds_addr = (uint32_t)uniform((int)lds_addr);
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_addr) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_addr)
+                 : "m0", "memory");
   else if constexpr (BYTES == 4)
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_addr) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds_addr)
+                 : "m0", "memory");
   else  // one byte, zero-extended to the lane's four
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off" ::"v"(src), "s"(lds_addr) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off" ::"v"(src), "s"(lds_addr)
+                 : "m0", "memory");
 }
+#pragma clang diagnostic pop
 typedef __attribute__((address_space(3))) char lds_char;
 __device__ __forceinline__ uint32_t lds_addr_of(const char *p) { return (uint32_t)(uintptr_t)(lds_char *)p; }
 

@@ -69,14 +69,19 @@ __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
 // Direct-to-LDS 16-byte loads: lane i's data lands at M0 + 16 i.  The load
 // may read M0 only a wait state after its write, and the compiler adds none
-// inside an asm block.
+// inside an asm block.  (M0 is reserved, of which the compiler warns where it
+// is on a clobber list; the entry keeps it from relying on M0's old value.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma_saddr(const void *sbase, uint32_t voff, uint32_t lds_addr) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "s"(lds_addr)
-               : "memory");
+               : "m0", "memory");
 }
 __device__ __forceinline__ void dma_vaddr(const void *vaddr, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(vaddr), "s"(lds_addr) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(vaddr), "s"(lds_addr)
+               : "m0", "memory");
 }
+#pragma clang diagnostic pop
 template <int N> __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));

@@ -58,3 +58,14 @@ def test_no_dot_or_matrix_product_in_inline_assembly():
     wait states later, and a matrix product's later still."""
     bad = [(f, t) for f, t, _ in _asm_statements() if re.search(r"\bv_(dot|s?mfma|smfmac|wmma)", t)]
     assert not bad, bad
+
+
+def test_asm_that_writes_m0_says_so():
+    """M0 is also what the compiler's own direct-to-LDS loads and lane moves
+    by M0 read: it has to know that its value is gone."""
+    seen = 0
+    for f, template, rest in _asm_statements():
+        if re.search(r"\bs_\w+ m0\b", template):
+            seen += 1
+            assert '"m0"' in rest, (f, template)
+    assert seen
