@@ -32,6 +32,7 @@ import manifold_constrained_hyper_amd as mhc
 import oracle
 import synth
 from oracle import backward
+from tests import eight_streams
 
 pytestmark = pytest.mark.gpu
 
@@ -761,3 +762,67 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for (_, _, _, want), g in zip(work, got):
             assert all(torch.equal(want[k], g[k]) for k in want)
+
+
+# -- eight streams ----------------------------------------------------------------------------------
+
+def _eight_streams_call(logits, r, b, dH, seed):
+    """The coefficient gradients of rows with these logits (alpha_res = 1)."""
+    B, n, C = len(r), 8, 8
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    inp = {"X": rand(B, n * C).to(torch.bfloat16), "phi": rand(n * C, n * n + 2 * n).to(torch.bfloat16),
+           "alphas": (0.3, 0.2, 1.0), "b_pre": rand(n), "b_post": rand(n), "b_res": dev(b), "logits": dev(logits),
+           "r": dev(r), "H": torch.rand(B, n * n + 2 * n, generator=gen, device="cuda"),
+           "G": rand(B, n * C).to(torch.bfloat16), "dF_pre": rand(B, C).to(torch.bfloat16)}
+    return inp, _coeffs_pre_bwd(inp, (inp["X"],), dev(dH), B, n, C)
+
+
+@pytest.mark.parametrize("diag,spread", eight_streams.SPREADS)
+def test_eight_streams_row_by_row(diag, spread):
+    """One row's db_res is its dz: within the bound of tests/eight_streams.py,
+    which a missing iteration exceeds."""
+    logits, r, b, dH, z = eight_streams.inputs(diag, spread, 12, seed=5)
+    want, bound = eight_streams.exact(z, dH[:, 16:]), eight_streams.row_bound(z, dH[:, 16:])
+    for k in range(len(r)):
+        _say(f"eight streams diag={diag} spread={spread} row {k}")
+        _, got = _eight_streams_call(logits[k:k + 1], r[k:k + 1], b, dH[k:k + 1], seed=k)
+        off = np.abs(f64(got["db_res"]).reshape(8, 8) - want[k]).max()
+        _say(f"  {off / (U * np.abs(dH[k, 16:]).max()):.2f} u max|dH_res|")
+        assert off <= bound[k]
+
+
+@pytest.mark.parametrize("diag,spread", eight_streams.SPREADS)
+def test_eight_streams_sums_over_rows(diag, spread):
+    """Rows' errors are independent and have no side, so what they add up to
+    is compared with six times the root of their squared bounds; the sums
+    themselves are 64-bit (db_res, dalpha), or as at the top of this file
+    (dphi)."""
+    B, n, C = 333, 8, 8
+    _say(f"eight streams sums diag={diag} spread={spread}")
+    logits, r, b, dH, z = eight_streams.inputs(diag, spread, B, seed=6)
+    inp, got = _eight_streams_call(logits, r, b, dH, seed=7)
+    want = eight_streams.exact(z, dH[:, 16:]).reshape(B, 64)
+    bound, lg, r64 = eight_streams.row_bound(z, dH[:, 16:]), logits[:, 16:].astype(np.float64), r.astype(np.float64)
+    db = want.sum(0)
+    _say(f"  off by {np.max(np.abs(f64(got['db_res']) - db) / np.abs(want).sum(0)):.1e} of the terms")
+    _near(got["db_res"], db, 6 * np.sqrt(np.sum(bound ** 2)) + U * np.abs(db), "db_res")
+    ratio = lg / r64[:, None]
+    da = np.sum(want * ratio)
+    _near(got["dalpha"][2:], np.array([da]),
+          np.array([6 * np.sqrt(np.sum((bound * np.abs(ratio).sum(1)) ** 2)) + U * abs(da)]), "dalpha")
+    x, dl = f64(inp["X"]), want / r64[:, None]
+    terms = np.abs(x).T @ np.abs(dl)
+    _near(got["dphi"][:, 16:].contiguous(), x.T @ dl,
+          6 * np.sqrt((x ** 2).T @ ((bound / r64)[:, None] ** 2)) + ((B + 8) * U + 2.0 ** -22) * terms, "dphi")
+
+
+@pytest.mark.parametrize("alpha,scale", [(0.01, 1.0), (6.0, 1.0), (0.5, 2.0 ** -40), (0.5, 2.0 ** 30)])
+def test_ranges_of_eight_streams(alpha, scale):
+    B, n, C = 70, 8, 104
+    inp = _inputs(B, n, C, seed=12, alpha=alpha, scale=scale)
+    for x in ("bf16", "e4m3"):
+        held, xv = _held(inp, x, n, C)
+        dH = _check_post_res(inp, held, xv, B, n, C)
+        _check_coeffs_pre(inp, held, xv, dH, B, n, C)
