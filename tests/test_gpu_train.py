@@ -32,7 +32,7 @@ import manifold_constrained_hyper_amd as mhc
 import oracle
 import synth
 from oracle import backward
-from tests import eight_streams
+from tests import eight_streams, train_replay
 
 pytestmark = pytest.mark.gpu
 
@@ -818,6 +818,22 @@ def test_eight_streams_sums_over_rows(diag, spread):
           6 * np.sqrt((x ** 2).T @ ((bound / r64)[:, None] ** 2)) + ((B + 8) * U + 2.0 ** -22) * terms, "dphi")
 
 
+# Many tiles a range of rows and several slices of channels, and a launch of
+# each other number of streams.
+@pytest.mark.parametrize("B,n,C", [(4096, 4, 2048), (3000, 1, 1032), (5000, 2, 520), (2100, 8, 264)])
+def test_same_bits_of_many_tiles(B, n, C):
+    _say(f"same bits B={B} n={n} C={C}")
+    inp = _inputs(B, n, C, seed=32)
+    for x in ("bf16", "e4m3"):
+        held = (inp["X"],) if x == "bf16" else _pack(inp["X"], n, C)
+        dH = _post_res_bwd(inp, held, B, n, C)[1]
+        want = _coeffs_pre_bwd(inp, held, dH, B, n, C)
+        for _ in range(4):
+            assert torch.equal(_post_res_bwd(inp, held, B, n, C)[1], dH)
+            got = _coeffs_pre_bwd(inp, held, dH, B, n, C)
+            assert all(torch.equal(got[k], want[k]) for k in want)
+
+
 @pytest.mark.parametrize("alpha,scale", [(0.01, 1.0), (6.0, 1.0), (0.5, 2.0 ** -40), (0.5, 2.0 ** 30)])
 def test_ranges_of_eight_streams(alpha, scale):
     B, n, C = 70, 8, 104
@@ -826,3 +842,51 @@ def test_ranges_of_eight_streams(alpha, scale):
         held, xv = _held(inp, x, n, C)
         dH = _check_post_res(inp, held, xv, B, n, C)
         _check_coeffs_pre(inp, held, xv, dH, B, n, C)
+
+
+# -- a training step, closely -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("ckpt", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("B,n,C,V", [(300, 4, 256, 50), (37, 2, 96, 20), (64, 8, 64, 30)])
+def test_training_step_against_its_replay(B, n, C, V, ckpt):
+    """Four layers whose streams differ, against the same step in 64 bits with
+    the same values rounded (tests/train_replay.py), so that what is left is
+    the calls' own arithmetic and the few stored values that it moves across
+    a rounding border.
+
+    Bounds, from replays whose values were moved by 2e-6 of themselves before
+    each rounding (32-bit sums and the forward's exponentials move them by some
+    2^-24 = 6e-8, a thirtieth, and the number of values that cross a border,
+    whose root is the distance, goes down with it): the table's gradient moved
+    by 1.1e-3 of its norm and dphi by 4.2e-3, 2^-9 and 2^-8 are allowed; the
+    small vectors, which are sums over rows that cancel, by 9.3e-4 of `noise`
+    (db_res: 1e-5, most of dH_res cancels), 2^-11 and 2^-17 are, and 2^-9 of
+    their norm.  A gradient of half its size fails in each of these but db_res
+    of the first and the last layer, which are next to 0 (see
+    test_training_step)."""
+    _say(f"training step and replay B={B} n={n} C={C} V={V} ckpt={ckpt}")
+    L = 4
+    m = Model(B, n, C, V, L, ckpt, seed=B + 1)
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    for p in m.layers:
+        p["b_pre"].mul_(10)
+        p["b_post"].mul_(10)
+        p["b_res"].add_(0.5 * torch.randn(n * n, generator=gen, device="cuda"))
+    m.step()
+    torch.cuda.synchronize()
+    want, noise = train_replay.step(
+        {"tokens": m.tokens.tolist(), "table": f64(m.table), "scale": m.scale, "out": f64(m.out),
+         "alphas": [float(np.float32(a)) for a in m.alphas],
+         "layers": [{k: f64(v) for k, v in p.items()} for p in m.layers]}, B, n, C, ckpt)
+    for k, v in m.results().items():
+        w = want[k]
+        norm, off = np.linalg.norm(w), np.linalg.norm(f64(v).reshape(w.shape) - w)
+        if k.startswith(("dtable", "dphi")):
+            bound = (2.0 ** -9 if k == "dtable" else 2.0 ** -8) * norm
+        else:
+            size = np.sqrt(w.size) * noise[int(k[-1])]
+            bound = 2.0 ** -9 * norm + (2.0 ** -17 if k.startswith("db_res") else 2.0 ** -11) * size
+            if not (k.startswith("db_res") and k[-1] in "03"):
+                assert norm / 2 > bound, k
+        _say(f"  {k}: off by {off / norm:.1e} of the norm, {off / bound:.2f} of the bound")
+        assert off <= bound, k
