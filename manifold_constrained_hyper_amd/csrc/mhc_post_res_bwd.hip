@@ -126,13 +126,15 @@ __global__ __launch_bounds__(64 * max_waves<NS>()) void post_res_bwd_kernel(
 }
 
 // Waves a row: two steps of 512 channels each, at most eight, where there are
-// rows enough (n=4, C=7168, B=16384, from the checkpoint: 325 us with 7 or 8
-// waves, 345 with 4, 375 with a wave a step; n=8, C=4096, B=8192: 211 us with
-// 4, 233 with 8, 223 with 2); a wave a step where few rows leave the chip
-// idle (n=4, C=7168, B=64: 12.5 us with 14, 15.7 with 4).
+// rows enough to fill the chip so; a wave a step where there are not.  In us
+// (n=4, C=7168 from the checkpoint, from the stream; n=8, C=4096):
+//     rows                 256           512            768           1024           4096
+//     a wave a step     8.0  8.8 11.5  12.6 13.8 16.0  19.2 19.3 24.0  25.0 26.7 29.6  91.7  96.5 110.5
+//     two steps a wave  8.3  9.0 14.4  11.1 14.3 18.8  15.8 19.8 23.8  20.9 25.8 28.3  79.4 103.4 104.1
+constexpr int64_t kManyRows = 768;
 int waves_of(int most, int64_t B, int64_t C) {
-  const int64_t steps = (C + 511) / 512, want = B >= 1024 ? (steps + 1) / 2 : steps;
-  const int64_t cap = B >= 1024 ? 8 : most;
+  const int64_t steps = (C + 511) / 512, want = B >= kManyRows ? (steps + 1) / 2 : steps;
+  const int64_t cap = B >= kManyRows ? 8 : most;
   return (int)(want < cap ? want : cap);
 }
 

@@ -818,6 +818,19 @@ def test_eight_streams_sums_over_rows(diag, spread):
           6 * np.sqrt((x ** 2).T @ ((bound / r64)[:, None] ** 2)) + ((B + 8) * U + 2.0 ** -22) * terms, "dphi")
 
 
+@pytest.mark.parametrize("x", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,n,C", [(767, 4, 2056), (768, 4, 2056), (768, 8, 2056), (3, 4, 7176), (2, 8, 8200), (5, 1, 9000)])
+def test_apply_gradients_by_waves_a_row(B, n, C, x):
+    """Both sides of the choice of waves a row, and rows of as many as there are."""
+    _say(f"apply gradients B={B} n={n} C={C} x={x}")
+    gen = torch.Generator(device="cuda").manual_seed(B + C)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    inp = {"X": rand(B, n * C).to(torch.bfloat16), "F_out": rand(B, C).to(torch.bfloat16),
+           "H": rand(B, n * n + 2 * n), "G": rand(B, n * C).to(torch.bfloat16)}
+    held, xv = _held(inp, x, n, C)
+    _check_post_res(inp, held, xv, B, n, C)
+
+
 # Many tiles a range of rows and several slices of channels, and a launch of
 # each other number of streams.
 @pytest.mark.parametrize("B,n,C", [(4096, 4, 2048), (3000, 1, 1032), (5000, 2, 520), (2100, 8, 264)])
