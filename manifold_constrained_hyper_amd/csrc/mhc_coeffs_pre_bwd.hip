@@ -117,8 +117,8 @@ __device__ __forceinline__ void form_operands(const float *dl, int item, int lan
   }
 }
 
-// dH_pre [B, n]: a workgroup a row (103 us at n=4, C=7168, B=16384 from the
-// checkpoint: 0.72 GB at 7.0 TB/s).
+// dH_pre [B, n]: a workgroup a row (106 us at n=4, C=7168, B=16384 from the
+// checkpoint, 0.72 GB at 6.8 TB/s; 174 from the stream, 1.17 GB at 6.7).
 template <int NS, bool CK, int W>
 __global__ __launch_bounds__(64 * W) void pre_dots_kernel(const void *__restrict__ X,
                                                           const uint8_t *__restrict__ scales,
@@ -220,8 +220,10 @@ __device__ __forceinline__ double recip(double x) {  // two steps: 2^-23, 2^-46,
 // n = 4 so are the normalisations: most of dH_res cancels in them (at n = 2
 // all but one degree of freedom), and fp32 left errors of 1e-6 of small
 // batches' sums.  That costs 5 us at n=4, B=16384 (19 against 14).  At n = 8,
-// with 49 degrees of freedom, fp32's errors stay under 4e-7 of the sums, and
-// 64 bits would not fit the registers of 1024 threads.
+// with 49 degrees of freedom, fp32 leaves dz within 1.1 * 2^-24 of a row's
+// largest dH_res, and sums over 333 rows within 6e-8 of the sums of their
+// terms' magnitudes, from balanced matrices to ones that 20 iterations do not
+// balance; 64 bits would not fit the registers of 1024 threads.
 //
 // dlogit leaves in tiles of 16 rows; rows past the last are zeros.
 template <int NS>
@@ -470,9 +472,9 @@ struct Sums {
 //    exactly, with lane 16 q + c holding rows 4 q .. 4 q + 3 of channel c --
 //    the B layout.  dlogit^T goes in three bf16 parts (coeffs_bwd_kernel), two
 //    of them in one 32-deep product against the same X twice, so dphi has
-//    fp32's accuracy (the third's product has zeros in its other half: a
-//    16x16x16 product before a 16x16x32 one on the same sums gave results
-//    that changed from run to run).  Sums over a workgroup's rows stay in
+//    fp32's accuracy (the third's product has zeros in its other half: with a
+//    16x16x16 product before a 16x16x32 one on the same sums results changed
+//    from run to run, for a cause that was not found).  Sums over a workgroup's rows stay in
 //    registers and are joined over the row ranges by join_kernel, in their
 //    order.
 //
@@ -492,13 +494,14 @@ struct Sums {
 // dlogit one tile further ahead: the waves form a share each, a tile before
 // the use.
 //
-// Measured at n=4, C=7168, B=16384 from the checkpoint: 460 to 485 us on three
-// cards for 2.6 GB of tensors (5.4 to 5.7 TB/s).  Without the arithmetic the
-// call's 638 us were 619: bound by HBM and the order in which it is reached.
-// At n=8, C=4096, B=8192 from the stream 400 us for 1.7 GB (4.3 TB/s): the
-// registers of a compute unit hold phi and dphi of 64 channels, so rows are
-// read 128 bytes at a time (without the arithmetic the call took 510 us, not
-// 545; with 1 KB of the record instead of 19, 495).
+// Measured at n=4, C=7168, B=16384 from the checkpoint: 487 us (460 on the
+// fastest card) for 2.77 GB (5.7 TB/s); from the stream 585 for 3.11 (5.3).
+// Without the arithmetic the call from the checkpoint takes 618 us, not 628:
+// bound by HBM and the order in which it is reached.  At n=8, C=4096, B=8192
+// from the stream 407 us for 1.81 GB (4.5 TB/s): the registers of a compute
+// unit hold phi and dphi of 64 channels, so rows are read 128 bytes at a time
+// (without the arithmetic the call takes 511 us, not 525; with 1 KB of the
+// record instead of 19, 493).
 //
 // Waits: vmcnt counts in order, and between a tile's loads and their use the
 // wave issues the loads and dX stores of the tiles in between and no other

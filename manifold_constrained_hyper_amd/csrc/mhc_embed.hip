@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const int64_t *__restri
 // joined 16 at a time: a key's place in the joined run is its place in its
 // own run plus, for each other run, the number of smaller keys there (a
 // binary search).  One launch for up to 1024 rows (5.5 us), two for up to
-// 16384 (20 us: the tiles' bitonic sort and the join are chains of lane moves
+// 16384 (19 us: the tiles' bitonic sort and the join are chains of lane moves
 // and LDS reads).
 typedef unsigned long long u64;
 constexpr uint32_t kNoToken = 0xffffffffu;
@@ -228,9 +228,10 @@ __device__ __forceinline__ void write_row(f32x4 *o, const float (&acc)[8], float
 // kZeroRows at most (with 8 rows each the table of n=4, C=7168, B=16384,
 // V=32768 took 405 us, not 396, and V=65536, C=64 with 300 rows 30, not 18).
 //
-// Bound by HBM where there are many rows: 326 us of the call's 398 at n=4,
-// C=7168, B=16384, V=32768, for 0.94 GB of dX_0 and 0.94 of the table (5.7
-// TB/s); by latency where there are few (7 us at n=2, C=1000, B=1001).
+// Bound by HBM where there are many rows: 336 us of the call's 398 at n=4,
+// C=7168, B=16384, V=32768, for 0.94 GB of dX_0 and 0.94 of the table (5.6
+// TB/s), 250 where it adds to the table (1.24 GB); by latency where there are
+// few (8 us at n=2, C=1000, B=1001).
 constexpr int kAhead = 16;  // 16-byte loads a lane has in flight
 constexpr uint32_t kZeroRows = 32, kZeroBytes = 1 << 14;
 
@@ -490,10 +491,13 @@ EmbedBwdPlan plan_embed_bwd(int64_t B, int64_t C) {
   EmbedBwdPlan p;
   const int64_t slices = (C + 511) / 512;
   // Long blocks where there are rows enough for one round of waves (4 on each
-  // SIMD of the 256 compute units), short ones for latency otherwise: at n=4,
-  // C=7168, B=16384 64 rows a block take 380 us, 32 397; with few waves n=4,
-  // C=256, B=3000 takes 21.5 us with 4, 24 with 8, n=2, C=1000, B=1001 17.5
-  // with 4, 18.5 with 8.
+  // SIMD of the 256 compute units), short ones for latency otherwise.  In us,
+  // one call at a time (V = 32768, the last one 5003; * what is taken):
+  //     rows a block                   4     8    16    32    64
+  //     n=4, C=7168, B=16384         440   405   391   381   367*
+  //     n=4, C=1024, B=16384        92.8  82.4* 79.0  83.4   110
+  //     n=4, C=256, B=3000          27.0* 29.2  36.4  51.5  80.0
+  //     n=2, C=1000, B=1001         19.5* 21.2  25.9  36.4  59.0
   p.rb = 4;
   while (p.rb < 64 && B * slices / p.rb > (p.rb == 4 ? 1024 : 4096)) p.rb *= 2;
   const size_t list = ((size_t)B * 8 + 15) / 16 * 16;

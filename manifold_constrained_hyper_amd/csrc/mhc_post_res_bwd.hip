@@ -14,9 +14,10 @@
 // input, which comes later, and is then one pass over G with everything else
 // that flows into X_t (mhc_coeffs_pre_bwd.hip).
 //
-// Bound by HBM, at 6.0 TB/s: 317 us at n=4, C=7168, B=16384 from the
-// checkpoint (1.90 GB), 203 at n=8, C=4096, B=8192 (1.21 GB).  64 rows of
-// n=4, C=7168 take 6.9, which is the launch.
+// Bound by HBM: 320 us at n=4, C=7168, B=16384 from the checkpoint (1.90 GB,
+// 5.9 TB/s), 428 from the stream (2.35 GB, 5.5 TB/s), 205 at n=8, C=4096,
+// B=8192 (1.21 GB, 5.9 TB/s).  64 rows of n=4, C=7168 take 7.1, which is the
+// launch (6.2 of the kernel).
 #include "mhc_finish.h"
 #include "mhc_held.h"
 #include "mhc_train.h"
