@@ -221,6 +221,11 @@ __global__ __launch_bounds__(512, 1) void lazy_prenorm_gemm_kernel(
       for (int w = 0; w < 4; ++w) {
         ssp[w] = dot2_bf16(sq[p][w], sq[p][w], ssp[w]);
       }
+    // Here, between the matrix products: left alone, the compiler moves the dot
+    // products behind the chunk's barrier (1438 against 1464 us at M=16384,
+    // N=K=7168).
+#pragma unroll
+    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(ssp[w]));
   };
 
   f32x16 acc[4][2];
