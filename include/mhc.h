@@ -670,6 +670,179 @@ int mhc_embed_bwd(int64_t B, int32_t n, int64_t C, int64_t V, const int64_t *tok
                   void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Around a layer of experts.
+ *
+ * Where the layer F between mhc_pre and mhc_post_res is a layer of experts,
+ * these calls are what surrounds the experts' own matrix products:
+ *
+ *   mhc_rmsnorm               F_pre normalised, to bf16 or to the 8-bit format
+ *                             of mhc_ckpt_pack (what scaled 8-bit products take);
+ *   (the router's product: the caller's, or mhc_lazy_prenorm_gemm)
+ *   mhc_route                 the k experts of each row, and their weights;
+ *   mhc_experts_order         places of the (row, expert) pairs in the order of
+ *                             the experts, so that each expert's rows are
+ *                             neighbours;
+ *   mhc_experts_gather(_ckpt) the rows, copied to those places;
+ *   (the experts' products)
+ *   mhc_experts_combine       their outputs, weighted and summed: F_out.
+ *
+ * And backwards, from dF_out (mhc_post_res_bwd) to dF_pre (mhc_coeffs_pre_bwd):
+ * mhc_experts_combine_bwd, (the experts), mhc_experts_combine without weights
+ * (the gradient of the gather), mhc_route_bwd, (the router), mhc_rmsnorm_bwd.
+ * A rounding to 8 bits is passed by the gradient as if it were not there.
+ *
+ * Rows are B >= 0 and channels C % 8 == 0 as above; k <= 32 experts are chosen
+ * of E <= 1024, and B * k < 2^31.  Sums run in fp32 or wider and in a fixed
+ * order (no atomics): equal inputs give equal bits.  Conventions, checks and
+ * errors are those at the top of this file.  bf16, codes and the gain's
+ * tensors are 16-byte aligned; indexes and other fp32 tensors 4-byte; scales
+ * are bytes.
+ * ------------------------------------------------------------------------ */
+
+/* Root-mean-square norm of each row, with the shortcut's addition:
+ *
+ *   s    = bf16(x + shortcut), or x where there is no shortcut
+ *   rstd = 1 / sqrt(mean(s^2) + eps)
+ *   y    = s * rstd * weight
+ *
+ *   x         in  bf16 [B, C]
+ *   shortcut  in  bf16 [B, C], or NULL
+ *   weight    in  fp32 [C], or NULL (1)
+ *   eps       host fp32 >= 0 (else MHC_ERR_INVALID_ARG)
+ *   sum       out bf16 [B, C]: s, or NULL if not wanted; needs shortcut
+ *   y         out bf16 [B, C], or NULL
+ *   codes     out E4M3 [B, C]; scales out uint8 [B, ceil(C / 32)]: y in the
+ *             format of mhc_ckpt_pack, rounded once from fp32 (a block's scale
+ *             is chosen by the fp32 values), both or neither; y or codes is
+ *             needed, and both may be asked for
+ *   rstd      out fp32 [B], or NULL
+ *
+ * C <= 65536 (else MHC_ERR_UNSUPPORTED).  With eps = 0 a row of zeros is NaN.
+ * Sums of squares are fp32: rows whose squares pass its range give rstd = 0. */
+int mhc_rmsnorm(int64_t B, int64_t C, const void *x, const void *shortcut, const float *weight,
+                float eps, void *sum, void *y, void *codes, uint8_t *scales, float *rstd,
+                void *stream);
+
+/* Its gradients.  With n = s * rstd and g = dy * weight,
+ *
+ *   dx      = rstd * (g - n * mean(g * n)) + dsum
+ *   dweight = sum over the rows of dy * n
+ *
+ *   sum      in  bf16 [B, C]: the rows that were normalised (x without shortcut)
+ *   weight   in  fp32 [C], or NULL (1);  rstd in fp32 [B], as the forward wrote it
+ *   dy       in  bf16 [B, C];  dsum in bf16 [B, C] or NULL: the gradient that
+ *                arrives at the sum on its other path
+ *   dx       out bf16 [B, C]: the gradient of x, and of the shortcut
+ *   dweight  out fp32 [C], overwritten (zeros at B == 0), or NULL if not wanted;
+ *                then no workspace is needed
+ *   workspace  scratch, >= mhc_rmsnorm_bwd_workspace_size(B, C) bytes, 16-byte
+ *              aligned; contents on entry ignored. */
+size_t mhc_rmsnorm_bwd_workspace_size(int64_t B, int64_t C);
+
+int mhc_rmsnorm_bwd(int64_t B, int64_t C, const void *sum, const float *weight, const float *rstd,
+                    const void *dy, const void *dsum, void *dx, float *dweight,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* The k experts of each row.
+ *
+ *   score_e  = sigmoid(logit_e), or the softmax over the row (MHC_ROUTE_SOFTMAX)
+ *   choice_e = score_e + bias_e     (the bias moves the choice, not the weights)
+ *
+ * An expert whose logit or choice is minus infinity or NaN cannot be chosen;
+ * plus infinity counts as the largest finite fp32 number.  The experts are
+ * `groups` groups of E / groups neighbours.  A group ranks by its largest
+ * choice, or, with a bias, by the sum of its two largest; the best top_groups
+ * groups stay.  Of their experts the k largest choices are taken, in descending
+ * order.  Among equal ones, groups too, the lowest index comes first.  Scores
+ * and choices are computed so that the order is that of 64-bit arithmetic.
+ *
+ *   weight_j = scale * score_j, or with MHC_ROUTE_RENORM
+ *              scale * score_j / (sum of the chosen scores), which holds for
+ *              logits of any size (no score underflows in it)
+ *
+ *   flags    MHC_ROUTE_SOFTMAX, MHC_ROUTE_RENORM, MHC_ROUTE_BF16 (bf16 logits)
+ *   logits   in  fp32 [B, E], or bf16
+ *   bias     in  fp32 [E], or NULL
+ *   ids      out int32 [B, k]: -1 where no expert is left
+ *   weights  out fp32 [B, k]: 0 there
+ *
+ * groups divides E, top_groups <= groups, k <= top_groups * (E / groups) (else
+ * MHC_ERR_INVALID_ARG); groups <= 64 (else MHC_ERR_UNSUPPORTED). */
+enum mhc_route_flags {
+  MHC_ROUTE_SOFTMAX = 1,
+  MHC_ROUTE_RENORM = 2,
+  MHC_ROUTE_BF16 = 4
+};
+
+int mhc_route(int64_t B, int32_t E, int32_t k, int32_t groups, int32_t top_groups, int32_t flags,
+              float scale, const void *logits, const float *bias, int32_t *ids, float *weights,
+              void *stream);
+
+/* The logits' gradient from the weights': the choice itself has none.
+ *
+ *   logits, flags, scale  as in the forward;  ids in int32 [B, k], as it wrote
+ *                         them (ids outside [0, E) have no weight; an id may
+ *                         occur twice)
+ *   dweights  in  fp32 [B, k]
+ *   dlogits   out fp32 [B, E], or bf16 as the logits: every value is written,
+ *                 zeros where no gradient arrives */
+int mhc_route_bwd(int64_t B, int32_t E, int32_t k, int32_t flags, float scale, const void *logits,
+                  const int32_t *ids, const float *dweights, void *dlogits, void *stream);
+
+/* Places of the pairs (b, j) in the order of their experts ids[b, j], pairs of
+ * one expert in the order of (b, j).
+ *
+ *   ids      in  int32 [B, k]
+ *   slots    out int32 [B, k]: the pair's place; -1 where its id is outside [0, E)
+ *   offsets  out int32 [E + 1]: expert e has the places offsets[e] to
+ *                offsets[e + 1] - 1; offsets[E] places are taken in all (zeros
+ *                at B == 0)
+ *   workspace  scratch, >= mhc_experts_order_workspace_size(B, k, E) bytes,
+ *              16-byte aligned; contents on entry ignored. */
+size_t mhc_experts_order_workspace_size(int64_t B, int32_t k, int32_t E);
+
+int mhc_experts_order(int64_t B, int32_t k, int32_t E, const int32_t *ids, int32_t *slots,
+                      int32_t *offsets, void *workspace, size_t workspace_bytes, void *stream);
+
+/* rows[slots[b, j]] = X[b].  Slots outside [0, B * k) are passed over, and rows
+ * that no slot names are left as they were; slots that are not negative must
+ * be different from each other.
+ *
+ *   X in bf16 [B, C];  slots in int32 [B, k];  rows out bf16 [B * k, C]
+ *
+ * mhc_experts_gather_ckpt: the same for rows held as codes [., C] and scales
+ * [., ceil(C / 32)] (mhc_rmsnorm, or mhc_ckpt_pack at n = 1). */
+int mhc_experts_gather(int64_t B, int32_t k, int64_t C, const void *X, const int32_t *slots,
+                       void *rows, void *stream);
+
+int mhc_experts_gather_ckpt(int64_t B, int32_t k, int64_t C, const void *codes,
+                            const uint8_t *scales, const int32_t *slots, void *row_codes,
+                            uint8_t *row_scales, void *stream);
+
+/* F_out[b] = shared[b] + sum over j of weights[b, j] * Y[slots[b, j]], in fp32
+ * in the order of j, rounded once to bf16.  Slots outside [0, B * k) add
+ * nothing, whatever their weight.
+ *
+ *   Y       in  bf16 [B * k, C]: the experts' outputs (rows that no slot names
+ *               are not read)
+ *   slots   in  int32 [B, k];  weights in fp32 [B, k], or NULL (1: with dY of
+ *               the experts in Y this is the gradient of mhc_experts_gather)
+ *   shared  in  bf16 [B, C], or NULL (0)
+ *   F_out   out bf16 [B, C] */
+int mhc_experts_combine(int64_t B, int32_t k, int64_t C, const void *Y, const int32_t *slots,
+                        const float *weights, const void *shared, void *F_out, void *stream);
+
+/* Its gradients: dY[slots[b, j]] = weights[b, j] * dF_out[b] (rows that no slot
+ * names are left as they were), dweights[b, j] = sum over c of dF_out[b, c] *
+ * Y[slots[b, j], c], 0 where the slot is outside [0, B * k).  That of `shared`
+ * is dF_out.  Slots that are not negative must be different from each other.
+ *
+ *   dF_out in bf16 [B, C];  dY out bf16 [B * k, C];  dweights out fp32 [B, k] */
+int mhc_experts_combine_bwd(int64_t B, int32_t k, int64_t C, const void *Y, const int32_t *slots,
+                            const float *weights, const void *dF_out, void *dY, float *dweights,
+                            void *stream);
+
+/* ------------------------------------------------------------------------
  * Testing and tuning.
  *
  * Every call above picks its kernels and launch shapes by the sizes of the

@@ -18,5 +18,7 @@ from .binding import (  # noqa: F401
     mhc_coeffs_pre_fp8_workspace_size, mhc_coeffs_pre_fp8, mhc_coeffs_pre_fp8_one_pass,
     mhc_ckpt_scales_per_row, mhc_ckpt_pack, mhc_ckpt_unpack, mhc_post_res_bwd, mhc_post_res_bwd_ckpt,
     mhc_coeffs_pre_bwd_workspace_size, mhc_coeffs_pre_bwd, mhc_coeffs_pre_bwd_ckpt, mhc_embed,
-    mhc_embed_bwd_workspace_size, mhc_embed_bwd,
+    mhc_embed_bwd_workspace_size, mhc_embed_bwd, MHC_ROUTE_SOFTMAX, MHC_ROUTE_RENORM, MHC_ROUTE_BF16, mhc_rmsnorm,
+    mhc_rmsnorm_bwd_workspace_size, mhc_rmsnorm_bwd, mhc_route, mhc_route_bwd, mhc_experts_order_workspace_size,
+    mhc_experts_order, mhc_experts_gather, mhc_experts_gather_ckpt, mhc_experts_combine, mhc_experts_combine_bwd,
 )

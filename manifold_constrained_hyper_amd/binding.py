@@ -21,6 +21,9 @@ MHC_ERR_WORKSPACE = 3
 MHC_ERR_HIP = 4
 MHC_ERR_INCOMPLETE = 5
 MHC_SINKHORN_ITERS = 20
+MHC_ROUTE_SOFTMAX = 1
+MHC_ROUTE_RENORM = 2
+MHC_ROUTE_BF16 = 4
 
 EXPORTED = ("mhc_status_string", "mhc_coeffs_workspace_size", "mhc_coeffs_split_k",
             "mhc_coeffs", "mhc_pre", "mhc_post_res", "mhc_post_res_coeffs_workspace_size",
@@ -38,7 +41,9 @@ EXPORTED = ("mhc_status_string", "mhc_coeffs_workspace_size", "mhc_coeffs_split_
             "mhc_coeffs_pre_fp8_one_pass", "mhc_ckpt_scales_per_row", "mhc_ckpt_pack", "mhc_ckpt_unpack",
             "mhc_post_res_bwd", "mhc_post_res_bwd_ckpt", "mhc_coeffs_pre_bwd_workspace_size",
             "mhc_coeffs_pre_bwd", "mhc_coeffs_pre_bwd_ckpt", "mhc_embed", "mhc_embed_bwd_workspace_size",
-            "mhc_embed_bwd")
+            "mhc_embed_bwd", "mhc_rmsnorm", "mhc_rmsnorm_bwd_workspace_size", "mhc_rmsnorm_bwd", "mhc_route",
+            "mhc_route_bwd", "mhc_experts_order_workspace_size", "mhc_experts_order", "mhc_experts_gather",
+            "mhc_experts_gather_ckpt", "mhc_experts_combine", "mhc_experts_combine_bwd")
 
 MHC_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -141,6 +146,21 @@ def load():
                        ("mhc_coeffs_pre_bwd_ckpt", [vp] * 2 + bwd), ("mhc_embed", [i64, vp, vp, f32, vp, vp]),
                        ("mhc_embed_bwd", [i64, vp, vp, f32, i32, vp, vp, sz, vp])):
         getattr(lib, name).argtypes = shape + args
+        getattr(lib, name).restype = ctypes.c_int
+    lib.mhc_rmsnorm_bwd_workspace_size.argtypes = [i64, i64]
+    lib.mhc_rmsnorm_bwd_workspace_size.restype = sz
+    lib.mhc_experts_order_workspace_size.argtypes = [i64, i32, i32]
+    lib.mhc_experts_order_workspace_size.restype = sz
+    for name, args in (("mhc_rmsnorm", [i64, i64] + [vp] * 3 + [f32] + [vp] * 6),
+                       ("mhc_rmsnorm_bwd", [i64, i64] + [vp] * 8 + [sz, vp]),
+                       ("mhc_route", [i64] + [i32] * 5 + [f32] + [vp] * 5),
+                       ("mhc_route_bwd", [i64] + [i32] * 3 + [f32] + [vp] * 5),
+                       ("mhc_experts_order", [i64, i32, i32] + [vp] * 4 + [sz, vp]),
+                       ("mhc_experts_gather", [i64, i32, i64] + [vp] * 4),
+                       ("mhc_experts_gather_ckpt", [i64, i32, i64] + [vp] * 6),
+                       ("mhc_experts_combine", [i64, i32, i64] + [vp] * 6),
+                       ("mhc_experts_combine_bwd", [i64, i32, i64] + [vp] * 7)):
+        getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
     lib.mhc_tuning_reset.argtypes = []
     lib.mhc_tuning_reset.restype = None
@@ -690,6 +710,177 @@ def mhc_embed_bwd(B, n, C, V, tokens, dX_0, scale, dtable, workspace, accumulate
                               _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_embed_bwd")
+    return st
+
+
+# Around a layer of experts: norm, choice of experts, rows into the experts'
+# order and back.  On the current device, as the training calls.
+
+@functools.lru_cache(maxsize=256)
+def _rmsnorm_sizes(B, C):
+    B = max(B, 0)
+    some = 4 * C if B > 0 else 0  # at B == 0 nothing is touched
+    return ((B * C * 2, 2, "x"), (B * C * 2, 2, "shortcut"), (some, 4, "weight"), (B * C * 2, 2, "sum"),
+            (B * C * 2, 2, "y"), (B * C, 1, "codes"), (B * -(-C // 32), 1, "scales"), (B * 4, 4, "rstd"))
+
+
+def mhc_rmsnorm(B, C, x, weight, y=None, codes=None, scales=None, shortcut=None, sum=None, rstd=None, eps=1e-5,
+                stream=None, check=True):
+    """Root-mean-square norm of x (plus the shortcut, kept in sum), times weight
+    (fp32 [C] or None): y in bf16, or codes and scales in 8 bits, or all three
+    (see include/mhc.h)."""
+    B, C, dev = int(B), int(C), _device()
+    x, shortcut, weight, *out = _dev_ptrs(dev, (x, shortcut, weight, sum, y, codes, scales, rstd), _rmsnorm_sizes(B, C))
+    st = load().mhc_rmsnorm(B, C, x, shortcut, weight, float(eps), *out, _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_rmsnorm")
+    return st
+
+
+def mhc_rmsnorm_bwd_workspace_size(B, C):
+    return int(load().mhc_rmsnorm_bwd_workspace_size(int(B), int(C)))
+
+
+@functools.lru_cache(maxsize=256)
+def _rmsnorm_bwd_sizes(B, C):
+    B = max(B, 0)
+    some = 4 * C if B > 0 else 0
+    return ((B * C * 2, 2, "sum"), (some, 4, "weight"), (B * 4, 4, "rstd"), (B * C * 2, 2, "dy"),
+            (B * C * 2, 2, "dsum"), (B * C * 2, 2, "dx"), (4 * C, 4, "dweight"))
+
+
+def mhc_rmsnorm_bwd(B, C, sum, weight, rstd, dy, dx, dweight=None, workspace=None, dsum=None, workspace_bytes=None,
+                    stream=None, check=True):
+    """Gradients of mhc_rmsnorm: dx (with dsum, what arrives at the sum on its
+    other path) and, with a workspace, dweight (see include/mhc.h)."""
+    B, C, dev = int(B), int(C), _device()
+    p = _dev_ptrs(dev, (sum, weight, rstd, dy, dsum, dx, dweight), _rmsnorm_bwd_sizes(B, C))
+    wb = _ws_bytes(workspace, workspace_bytes)
+    p += _dev_ptrs(dev, (workspace,), ((wb, None, "workspace"),))
+    st = load().mhc_rmsnorm_bwd(B, C, *p, wb, _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_rmsnorm_bwd")
+    return st
+
+
+def _logits_size(logits, softmax, renorm, bf16):
+    """Element size and flags: the logits' type is the tensor's (bf16 says it for raw addresses)."""
+    if bf16 is None:
+        bf16 = isinstance(logits, torch.Tensor) and logits.dtype == torch.bfloat16
+    if isinstance(logits, torch.Tensor) and logits.dtype not in (torch.bfloat16, torch.float32, torch.uint8):
+        raise ValueError(f"logits: {logits.dtype}, the call takes float32 or bfloat16")
+    return (2 if bf16 else 4,
+            (MHC_ROUTE_SOFTMAX if softmax else 0) | (MHC_ROUTE_RENORM if renorm else 0) | (MHC_ROUTE_BF16 if bf16 else 0))
+
+
+def mhc_route(B, E, k, logits, ids, weights, bias=None, groups=1, top_groups=1, softmax=False, renorm=True, scale=1.0,
+              bf16=None, stream=None, check=True):
+    """The k experts of each row of logits (fp32 or bf16 [B, E]): ids (int32)
+    and weights (fp32), both [B, k] (see include/mhc.h)."""
+    B, E, k, dev = int(B), int(E), int(k), _device()
+    one, flags = _logits_size(logits, softmax, renorm, bf16)
+    rows = max(B, 0)
+    logits, bias, ids, weights = _dev_ptrs(dev, (logits, bias, ids, weights), (
+        (rows * E * one, one, "logits"), (4 * E if rows else 0, 4, "bias"), (rows * k * 4, 4, "ids"),
+        (rows * k * 4, 4, "weights")))
+    st = load().mhc_route(B, E, k, int(groups), int(top_groups), flags, float(scale), logits, bias, ids, weights,
+                          _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_route")
+    return st
+
+
+def mhc_route_bwd(B, E, k, logits, ids, dweights, dlogits, softmax=False, renorm=True, scale=1.0, bf16=None,
+                  stream=None, check=True):
+    """Gradient of mhc_route's weights with respect to the logits, in their
+    type (see include/mhc.h)."""
+    B, E, k, dev = int(B), int(E), int(k), _device()
+    one, flags = _logits_size(logits, softmax, renorm, bf16)
+    rows = max(B, 0)
+    logits, ids, dweights, dlogits = _dev_ptrs(dev, (logits, ids, dweights, dlogits), (
+        (rows * E * one, one, "logits"), (rows * k * 4, 4, "ids"), (rows * k * 4, 4, "dweights"),
+        (rows * E * one, one, "dlogits")))
+    st = load().mhc_route_bwd(B, E, k, flags, float(scale), logits, ids, dweights, dlogits, _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_route_bwd")
+    return st
+
+
+def mhc_experts_order_workspace_size(B, k, E):
+    return int(load().mhc_experts_order_workspace_size(int(B), int(k), int(E)))
+
+
+def mhc_experts_order(B, k, E, ids, slots, offsets, workspace, workspace_bytes=None, stream=None, check=True):
+    """Places (int32 [B, k]) of the pairs (row, ids[row, j]) in the order of
+    their experts, and the experts' first places (int32 [E + 1]; see
+    include/mhc.h)."""
+    B, k, E, dev = int(B), int(k), int(E), _device()
+    rows, wb = max(B, 0), _ws_bytes(workspace, workspace_bytes)
+    ids, slots, offsets, workspace = _dev_ptrs(dev, (ids, slots, offsets, workspace), (
+        (rows * k * 4, 4, "ids"), (rows * k * 4, 4, "slots"), ((max(E, 0) + 1) * 4, 4, "offsets"),
+        (wb, None, "workspace")))
+    st = load().mhc_experts_order(B, k, E, ids, slots, offsets, workspace, wb, _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_experts_order")
+    return st
+
+
+# Tensors of B rows and of their B * k pairs.
+@functools.lru_cache(maxsize=256)
+def _pair_sizes(B, k, C):
+    B = max(B, 0)
+    return {"row": B * C * 2, "rows": B * k * C * 2, "pairs": B * k * 4, "codes": B * C, "scales": B * -(-C // 32)}
+
+
+def mhc_experts_gather(B, k, C, X, slots, rows, stream=None, check=True):
+    """rows[slots[b, j]] = X[b] (bf16; see include/mhc.h)."""
+    B, k, C, dev = int(B), int(k), int(C), _device()
+    z = _pair_sizes(B, k, C)
+    X, slots, rows = _dev_ptrs(dev, (X, slots, rows), (
+        (z["row"], 2, "X"), (z["pairs"], 4, "slots"), (z["rows"], 2, "rows")))
+    st = load().mhc_experts_gather(B, k, C, X, slots, rows, _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_experts_gather")
+    return st
+
+
+def mhc_experts_gather_ckpt(B, k, C, codes, scales, slots, row_codes, row_scales, stream=None, check=True):
+    """mhc_experts_gather of rows held in 8 bits, codes and scales (see include/mhc.h)."""
+    B, k, C, dev = int(B), int(k), int(C), _device()
+    z = _pair_sizes(B, k, C)
+    p = _dev_ptrs(dev, (codes, scales, slots, row_codes, row_scales), (
+        (z["codes"], 1, "codes"), (z["scales"], 1, "scales"), (z["pairs"], 4, "slots"),
+        (z["codes"] * k, 1, "row_codes"), (z["scales"] * k, 1, "row_scales")))
+    st = load().mhc_experts_gather_ckpt(B, k, C, *p, _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_experts_gather_ckpt")
+    return st
+
+
+def mhc_experts_combine(B, k, C, Y, slots, weights, F_out, shared=None, stream=None, check=True):
+    """F_out[b] = shared[b] + sum_j weights[b, j] Y[slots[b, j]]; weights None:
+    1, the gradient of mhc_experts_gather (see include/mhc.h)."""
+    B, k, C, dev = int(B), int(k), int(C), _device()
+    z = _pair_sizes(B, k, C)
+    p = _dev_ptrs(dev, (Y, slots, weights, shared, F_out), (
+        (z["rows"], 2, "Y"), (z["pairs"], 4, "slots"), (z["pairs"], 4, "weights"), (z["row"], 2, "shared"),
+        (z["row"], 2, "F_out")))
+    st = load().mhc_experts_combine(B, k, C, *p, _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_experts_combine")
+    return st
+
+
+def mhc_experts_combine_bwd(B, k, C, Y, slots, weights, dF_out, dY, dweights, stream=None, check=True):
+    """Gradients of mhc_experts_combine with respect to Y and the weights (see include/mhc.h)."""
+    B, k, C, dev = int(B), int(k), int(C), _device()
+    z = _pair_sizes(B, k, C)
+    p = _dev_ptrs(dev, (Y, slots, weights, dF_out, dY, dweights), (
+        (z["rows"], 2, "Y"), (z["pairs"], 4, "slots"), (z["pairs"], 4, "weights"), (z["row"], 2, "dF_out"),
+        (z["rows"], 2, "dY"), (z["pairs"], 4, "dweights")))
+    st = load().mhc_experts_combine_bwd(B, k, C, *p, _dev_stream(stream, dev))
+    if check:
+        _check(st, "mhc_experts_combine_bwd")
     return st
 
 

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 namespace mhc {
 
 // Largest problem accepted: B*n*C elements below 2^40 and K = n*C below 2^30
@@ -42,6 +44,33 @@ inline int check_shape(int64_t B, int32_t n, int64_t C) {
 }
 
 inline int64_t ncoef(int32_t n) { return (int64_t)n * n + 2 * (int64_t)n; }
+
+// Every buffer of a call: where it is, how far it reaches, its alignment, and
+// whether the caller may leave it out (NULL).
+struct Buf {
+  const void *p;
+  size_t bytes;
+  uintptr_t align;
+  bool optional = false;
+  Span span() const { return mhc::span(p, p ? bytes : 0); }
+};
+
+// NULL, then misalignment, then an output over an input or another output.
+inline int check_buffers(std::initializer_list<Buf> in, std::initializer_list<Buf> out) {
+  for (const auto *l : {&in, &out})
+    for (const Buf &b : *l)
+      if (!b.p && !b.optional) return MHC_ERR_INVALID_ARG;
+  for (const auto *l : {&in, &out})
+    for (const Buf &b : *l)
+      if (!aligned(b.p, b.align)) return MHC_ERR_UNSUPPORTED;
+  for (const Buf *o = out.begin(); o != out.end(); ++o) {
+    for (const Buf &i : in)
+      if (overlaps(o->span(), i.span())) return MHC_ERR_INVALID_ARG;
+    for (const Buf *q = out.begin(); q != o; ++q)
+      if (overlaps(o->span(), q->span())) return MHC_ERR_INVALID_ARG;
+  }
+  return MHC_OK;
+}
 
 inline int from_hip(hipError_t e) { return e == hipSuccess ? MHC_OK : MHC_ERR_HIP; }
 

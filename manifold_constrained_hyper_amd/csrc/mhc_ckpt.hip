@@ -17,13 +17,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
-  uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, false);  // lane ^ 1
-  x = x > y ? x : y;
-  y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, false);  // lane ^ 2
-  return x > y ? x : y;
-}
-
 // slots: four lanes for every block of every stream of every row; cvec
 // vectors a stream (the last block's lanes past it carry zeros).
 __global__ __launch_bounds__(kThreads) void pack_kernel(const u32x4 *__restrict__ X, u32x2 *__restrict__ codes,
@@ -42,26 +35,9 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const u32x4 *__restrict_
       amax = amax > m ? amax : m;
     }
     const int s = ckpt_scale(quad_max(amax));
-    const float f = ckpt_inverse(s);
     float y[8];
     widen8(x, y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= f;
-    if (s == kCkptMaxScale) {
-      // 255 * 2^120 would round to 256 * 2^120 = 2^128, Inf in bf16 and fp32.
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (fabsf(y[e]) < 256.0f) y[e] = fminf(fmaxf(y[e], -240.0f), 240.0f);
-    }
-    u32x2 q;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      // |x| * 2^(127-s) <= 448 by the choice of s: no saturation is needed,
-      // and Inf and NaN convert to the NaN code.
-      int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * w], y[4 * w + 1], 0, false);
-      c = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * w + 2], y[4 * w + 3], c, true);
-      q[w] = (uint32_t)c;
-    }
+    const u32x2 q = held_codes(y, s);
     if (v < cvec) codes[at] = q;
     if ((v & 3u) == 0) scales[g >> 2] = (uint8_t)s;
   }

@@ -32,8 +32,43 @@ __device__ __forceinline__ int ckpt_scale(uint32_t amax) {
   const int s = (int)(amax >> 7) - 8 + ((amax & 0x7fu) > 0x60u ? 1 : 0);
   return s < 1 ? 1 : s;
 }
+// The same from the largest finite fp32 magnitude's bits.
+__device__ __forceinline__ int ckpt_scale32(uint32_t amax) {
+  const int s = (int)(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return s < 1 ? 1 : s;
+}
+// The largest of the four lanes that share a block.
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+  uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, false);  // lane ^ 1
+  x = x > y ? x : y;
+  y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, false);  // lane ^ 2
+  return x > y ? x : y;
+}
 __device__ __forceinline__ float ckpt_value(int s) { return __uint_as_float((uint32_t)s << 23); }          // 2^(s-127)
 __device__ __forceinline__ float ckpt_inverse(int s) { return __uint_as_float((uint32_t)(254 - s) << 23); }  // 2^(127-s)
+
+// Codes of eight channels under the scale byte s of their block (y is scaled in place).
+__device__ __forceinline__ u32x2 held_codes(float (&y)[8], int s) {
+  const float f = ckpt_inverse(s);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] *= f;
+  if (s == kCkptMaxScale) {
+    // 255 * 2^120 would round to 256 * 2^120 = 2^128, Inf in bf16 and fp32.
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (fabsf(y[e]) < 256.0f) y[e] = fminf(fmaxf(y[e], -240.0f), 240.0f);
+  }
+  u32x2 q;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    // |x| * 2^(127-s) <= 448 by the choice of s: no saturation is needed,
+    // and Inf and NaN convert to the NaN code.
+    int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * w], y[4 * w + 1], 0, false);
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * w + 2], y[4 * w + 3], c, true);
+    q[w] = (uint32_t)c;
+  }
+  return q;
+}
 
 // Eight channels of X_t as fp32.  CK: from codes (8 bytes) and a scale byte.
 template <bool CK>

@@ -4,36 +4,9 @@
 #include "mhc_check.h"
 #include "mhc_train.h"
 
-#include <initializer_list>
-
 using namespace mhc;
 
 namespace {
-
-// Every buffer of a call: where it is, how far it reaches, its alignment.
-struct Buf {
-  const void *p;
-  size_t bytes;
-  uintptr_t align;
-  Span span() const { return mhc::span(p, bytes); }
-};
-
-// NULL, then misalignment, then an output over an input or another output.
-int check_buffers(std::initializer_list<Buf> in, std::initializer_list<Buf> out) {
-  for (const auto *l : {&in, &out})
-    for (const Buf &b : *l)
-      if (!b.p) return MHC_ERR_INVALID_ARG;
-  for (const auto *l : {&in, &out})
-    for (const Buf &b : *l)
-      if (!aligned(b.p, b.align)) return MHC_ERR_UNSUPPORTED;
-  for (const Buf *o = out.begin(); o != out.end(); ++o) {
-    for (const Buf &i : in)
-      if (overlaps(o->span(), i.span())) return MHC_ERR_INVALID_ARG;
-    for (const Buf *q = out.begin(); q != o; ++q)
-      if (overlaps(o->span(), q->span())) return MHC_ERR_INVALID_ARG;
-  }
-  return MHC_OK;
-}
 
 // Bytes of a call's tensors.
 struct Sizes {
