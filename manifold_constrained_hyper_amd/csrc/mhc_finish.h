@@ -55,6 +55,35 @@ __device__ __forceinline__ float tree16_sum_serial(const float (&x)[16]) {
   return (z[0] + z[1]) + (z[2] + z[3]);
 }
 
+// Sums of K values (a multiple of 4) over a wave's lanes.  Two halvings trade
+// half of the values between half-waves, then between rows of 16 lanes, so
+// that each lane goes on with a quarter of them; the rest are lane moves
+// inside a row.  Afterwards v[k], k < K / 4, of any lane holds the sum of
+// value k + K/4 (row & 1) + K/2 (row / 2), row = lane / 16.
+template <int K>
+__device__ __forceinline__ void wave_sums(float (&v)[K]) {
+  static_assert(K % 4 == 0, "quarters");
+#pragma unroll
+  for (int k = 0; k < K / 2; ++k) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + K / 2]), false, false);
+    v[k] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+#pragma unroll
+  for (int k = 0; k < K / 4; ++k) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]), __float_as_uint(v[k + K / 4]), false, false);
+    v[k] = tree16_sum(__uint_as_float(s[0]) + __uint_as_float(s[1]));
+  }
+}
+
+// Sum over a wave's lanes; every lane has it.
+__device__ __forceinline__ float wave_sum(float x) {
+  x = tree16_sum(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 template <int NS>
 __device__ __forceinline__ float group_sum(float x) {
   if constexpr (NS >= 2) x = dpp_add_xor1(x);

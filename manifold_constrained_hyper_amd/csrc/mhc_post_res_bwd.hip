@@ -26,26 +26,6 @@ namespace mhc {
 
 namespace {
 
-// Sums of K values (a multiple of 4) over a wave's lanes.  Two halvings trade
-// half of the values between half-waves, then between rows of 16 lanes, so
-// that each lane goes on with a quarter of them; the rest are lane moves
-// inside a row.  Afterwards v[k], k < K / 4, of any lane holds the sum of
-// value k + K/4 (row & 1) + K/2 (row / 2), row = lane / 16.
-template <int K>
-__device__ __forceinline__ void wave_sums(float (&v)[K]) {
-  static_assert(K % 4 == 0, "quarters");
-#pragma unroll
-  for (int k = 0; k < K / 2; ++k) {
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + K / 2]), false, false);
-    v[k] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  }
-#pragma unroll
-  for (int k = 0; k < K / 4; ++k) {
-    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[k]), __float_as_uint(v[k + K / 4]), false, false);
-    v[k] = tree16_sum(__uint_as_float(s[0]) + __uint_as_float(s[1]));
-  }
-}
-
 template <int NS, bool CK>
 __device__ __forceinline__ u32x4 x_words(const Held8<CK> &x) {
   if constexpr (CK)

@@ -18,15 +18,6 @@ namespace {
 
 constexpr int kMostWaves = 16;
 
-// Sum over a wave's lanes; every lane has it.
-__device__ __forceinline__ float wave_sum(float x) {
-  x = tree16_sum(x);
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 // Sum over the workgroup, in the order of its waves.  `part` is used again
 // only behind the caller's next barrier.
 __device__ __forceinline__ float group_total(float x, float *part) {
