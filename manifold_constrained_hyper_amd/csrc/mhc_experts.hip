@@ -75,101 +75,78 @@ __device__ __forceinline__ uint32_t group_scan(uint32_t x, uint32_t *sums, uint3
   return before + y - x;
 }
 
-constexpr int kOneWaves = 16, kOnePairs = kOneWaves * 64 * kRounds;
-__global__ __launch_bounds__(64 * kOneWaves) void order_kernel(const int32_t *__restrict__ ids, uint32_t pairs, int E,
-                                                               int32_t *__restrict__ slots,
-                                                               int32_t *__restrict__ offsets) {
-  extern __shared__ uint16_t seen[];  // [waves][E]
-  __shared__ uint32_t first[kMaxExperts], sums[kOneWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint16_t *mine = seen + wave * E;
-  // Each wave takes whole rounds, so that the pairs stay in their order.
-  const uint32_t rounds = (pairs + 63) / 64, per = (rounds + kOneWaves - 1) / kOneWaves;
-  const uint32_t p0 = wave * per * 64 + lane;
-  int32_t id[kRounds], rank[kRounds];
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r) id[r] = (uint32_t)r < per && p0 + 64 * r < pairs ? ids[p0 + 64 * r] : -1;
-  for (int e = lane; e < E; e += 64) mine[e] = 0;
-  wave_ranks(id, E, mine, rank);
-  __syncthreads();
-  uint32_t count = 0;  // of the expert that is this thread's index
-  if ((int)threadIdx.x < E) {
-    for (int w = 0; w < kOneWaves; ++w) {
-      const uint32_t c = seen[w * E + threadIdx.x];
-      seen[w * E + threadIdx.x] = (uint16_t)count;
-      count += c;
-    }
-  }
-  uint32_t all;
-  const uint32_t at = group_scan<kOneWaves>(count, sums, &all);
-  if ((int)threadIdx.x < E) {
-    first[threadIdx.x] = at;
-    offsets[threadIdx.x] = (int32_t)at;
-  }
-  if (threadIdx.x == 0) offsets[E] = (int32_t)all;
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r)
-    if ((uint32_t)r < per && p0 + 64 * r < pairs)
-      slots[p0 + 64 * r] = rank[r] < 0 ? -1 : (int32_t)(first[id[r]] + mine[id[r]]) + rank[r];
-}
-
-constexpr int kRankWaves = 4, kChunk = kRankWaves * 64 * kRounds;
+// A workgroup ranks the pairs of a tile, a chunk at a time.  ONE: there is no
+// other, and the slots are final (3.7 us for 8 pairs, 7.2 for 4096).
+constexpr int kRankWaves = 16, kChunk = kRankWaves * 64 * kRounds;
+template <bool ONE>
 __global__ __launch_bounds__(64 * kRankWaves) void rank_kernel(const int32_t *__restrict__ ids, uint32_t pairs,
                                                                uint32_t tile, int E, int32_t *__restrict__ slots,
-                                                               uint32_t *__restrict__ counts) {
+                                                               uint32_t *__restrict__ counts,
+                                                               int32_t *__restrict__ offsets) {
   extern __shared__ uint16_t seen[];  // [waves][E]
-  __shared__ uint32_t so_far[kMaxExperts];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ uint32_t so_far[kMaxExperts], sums[kRankWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, own = threadIdx.x;  // own: a thread's expert
   uint16_t *mine = seen + wave * E;
   const uint64_t first = (uint64_t)blockIdx.x * tile, last = first + tile < pairs ? first + tile : pairs;
-  for (int e = threadIdx.x; e < E; e += 64 * kRankWaves) so_far[e] = 0;
+  uint32_t total = 0;  // of the own expert
   for (uint64_t c = first; c < last; c += kChunk) {
-    const uint64_t p0 = c + wave * 64 * kRounds + lane;
+    // Each wave takes whole rounds, so that the pairs stay in their order.
+    const uint32_t size = last - c < kChunk ? (uint32_t)(last - c) : kChunk;
+    const uint32_t per = (size + 64 * kRankWaves - 1) / (64 * kRankWaves), at = wave * per * 64 + lane;
     int32_t id[kRounds], rank[kRounds];
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) id[r] = p0 + 64 * r < last ? ids[p0 + 64 * r] : -1;
+    for (int r = 0; r < kRounds; ++r) id[r] = (uint32_t)r < per && at + 64 * r < size ? ids[c + at + 64 * r] : -1;
     for (int e = lane; e < E; e += 64) mine[e] = 0;
     wave_ranks(id, E, mine, rank);
     __syncthreads();
-    uint32_t base[kRounds];
+    if (own < E) {  // the earlier waves' counts
+      uint32_t n = 0;
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      base[r] = 0;
-      if (rank[r] >= 0) {
-        base[r] = so_far[id[r]];
-        for (int w = 0; w < wave; ++w) base[r] += seen[w * E + id[r]];
+      for (int w = 0; w < kRankWaves; ++w) {
+        const uint32_t m = seen[w * E + own];
+        seen[w * E + own] = (uint16_t)n;
+        n += m;
       }
-      if (p0 + 64 * r < last) slots[p0 + 64 * r] = rank[r] < 0 ? -1 : (int32_t)base[r] + rank[r];
+      so_far[own] = total;
+      total += n;
+    }
+    if constexpr (ONE) {  // the smaller experts' (its barrier is before the store)
+      uint32_t all;
+      const uint32_t start = group_scan<kRankWaves>(total, sums, &all);
+      if (own < E) {
+        so_far[own] = start;
+        offsets[own] = (int32_t)start;
+      }
+      if (own == 0) offsets[E] = (int32_t)all;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 64 * kRankWaves) {
-      uint32_t t = so_far[e];
 #pragma unroll
-      for (int w = 0; w < kRankWaves; ++w) t += seen[w * E + e];
-      so_far[e] = t;
-    }
-    __syncthreads();
+    for (int r = 0; r < kRounds; ++r)
+      if ((uint32_t)r < per && at + 64 * r < size)
+        slots[c + at + 64 * r] = rank[r] < 0 ? -1 : (int32_t)(so_far[id[r]] + mine[id[r]]) + rank[r];
+    if (last - c > kChunk) __syncthreads();
   }
-  for (int e = threadIdx.x; e < E; e += 64 * kRankWaves) counts[(size_t)blockIdx.x * E + e] = so_far[e];
+  if (!ONE && own < E) counts[(size_t)blockIdx.x * E + own] = total;
 }
 
-// A workgroup takes a tile.  `stride`: E rounded up to a power of two; the
-// threads are kPlaceThreads / stride teams that share the tiles.
+// A workgroup takes `share` pairs of a tile.  `stride`: E rounded up to a power
+// of two; the threads are kPlaceThreads / stride teams that share the tiles.
 constexpr int kPlaceThreads = 1024;
 __global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t *__restrict__ ids, uint32_t pairs,
-                                                              uint32_t tile, uint32_t tiles, int E, uint32_t stride,
-                                                              const uint32_t *__restrict__ counts,
+                                                              uint32_t share, uint32_t tile, uint32_t tiles, int E,
+                                                              uint32_t stride, const uint32_t *__restrict__ counts,
                                                               int32_t *__restrict__ slots,
                                                               int32_t *__restrict__ offsets) {
   __shared__ uint32_t before[kPlaceThreads], total[kPlaceThreads], sums[kPlaceThreads / 64];
   const uint32_t tid = threadIdx.x, e = tid & (stride - 1), teams = kPlaceThreads / stride;
+  const uint64_t first = (uint64_t)blockIdx.x * share, last = first + share < pairs ? first + share : pairs;
+  const uint32_t mine = (uint32_t)(first / tile);
   uint32_t b = 0, all = 0;
   if (e < (uint32_t)E) {
 #pragma unroll 8
     for (uint32_t t = tid / stride; t < tiles; t += teams) {
       const uint32_t c = counts[(size_t)t * E + e];
-      b += t < blockIdx.x ? c : 0;
+      b += t < mine ? c : 0;
       all += c;
     }
   }
@@ -190,7 +167,6 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t *__r
   }
   if (blockIdx.x == 0 && tid == 0) offsets[E] = (int32_t)every;
   __syncthreads();
-  const uint64_t first = (uint64_t)blockIdx.x * tile, last = first + tile < pairs ? first + tile : pairs;
   for (uint64_t p = first + tid; p < last; p += kPlaceThreads) {
     const int32_t id = ids[p];
     if (id >= 0 && id < E) slots[p] += (int32_t)before[id];
@@ -200,69 +176,84 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t *__r
 // -- rows -------------------------------------------------------------------
 //
 // A row of up to 32 vectors shares a wave with others: `lanes` (a power of
-// two) of them a row.  Of a longer one a wave takes 64 vectors at a time; all
-// of its lanes have the same row then, and slots and weights come by scalar
-// loads.
+// two) of them a row.  The lanes of a wave that works on a longer one have the
+// same row, and slots and weights come by scalar loads.
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-
-struct Rows {
-  uint64_t units;    // of work, one a wave: 64 vectors of a row, or 64 / lanes rows
-  uint32_t segs;     // units a row (LONG)
-  uint32_t lanes;    // lanes a row (not LONG)
-  uint32_t vecs;     // vectors a row
-};
-
-// The row and the vector of a lane in unit u; false where there is none.
-template <bool LONG>
-__device__ __forceinline__ bool place_of(const Rows &r, uint64_t u, uint64_t B, uint32_t per, uint64_t *row,
-                                         uint32_t *v) {
-  const uint32_t lane = threadIdx.x & 63;
-  if constexpr (LONG) {
-    // (units are below 2^32 but for rows beyond a few TB)
-    *row = u >> 32 ? u / per : (uint32_t)u / per;
-    *v = (uint32_t)(u - *row * per) * 64 + lane;
-    return true;
-  } else {
-    *row = u * (64 / r.lanes) + lane / r.lanes;
-    *v = lane & (r.lanes - 1);
-    return *row < B;
-  }
-}
 
 __device__ __forceinline__ uint64_t wave_index() {
   return (uint64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
+// (u is below 2^32 but for tensors beyond a few TB)
+__device__ __forceinline__ uint64_t quotient(uint64_t u, uint32_t d) { return u >> 32 ? u / d : (uint32_t)u / d; }
+
+// Units of work of short rows, one a wave; a lane's row and vector.
+struct Short {
+  uint64_t units;
+  uint32_t lanes, vecs;
+};
+__device__ __forceinline__ bool place_of(const Short &r, uint64_t u, uint64_t B, uint64_t *row, uint32_t *v) {
+  const uint32_t lane = threadIdx.x & 63;
+  *row = u * (64 / r.lanes) + lane / r.lanes;
+  *v = lane & (r.lanes - 1);
+  return *row < B;
+}
 
 // -- gather -----------------------------------------------------------------
 //
-// A lane moves a vector (T: 16 or 8 bytes) of a row to the row's places.  A
-// row's scale bytes are a further unit of it (LONG), or a lane each.
-template <class T, bool LONG>
-__global__ __launch_bounds__(kThreads) void gather_kernel(const T *__restrict__ x, const uint8_t *__restrict__ scales,
+// A wave copies a row (T: vectors of 16 or 8 bytes), or one of `parts` of it,
+// to one place, in one piece: 182 us for the 940 MB of B=16384, k=8, C=7168 in
+// 8 bits (5.8 TB/s with what is read), where waves that write 1 KB each to all
+// of the row's places take 210.  The row's k waves find it in the cache.
+template <class T, class S>
+__global__ __launch_bounds__(kThreads) void gather_kernel(const T *__restrict__ x, const S *__restrict__ scales,
                                                           const int32_t *__restrict__ slots, T *__restrict__ rows,
-                                                          uint8_t *__restrict__ row_scales, Rows r, uint64_t B,
-                                                          uint32_t blocks, int k, uint32_t pairs) {
-  const uint32_t per = r.segs + (scales ? 1 : 0);
+                                                          S *__restrict__ row_scales, uint64_t units, uint32_t parts,
+                                                          uint32_t part, uint32_t vecs, uint32_t blocks, uint32_t k,
+                                                          uint32_t pairs) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t step = (uint64_t)gridDim.x * kWaves;
+  for (uint64_t u = wave_index(); u < units; u += step) {
+    const uint64_t p = quotient(u, parts);
+    const uint32_t first = (uint32_t)(u - p * parts) * part, slot = (uint32_t)slots[p];
+    if (slot >= pairs) continue;
+    const uint64_t row = (uint32_t)p / k;
+    const T *from = x + row * vecs;
+    T *to = rows + (size_t)slot * vecs;
+    const uint32_t last = first + part < vecs ? first + part : vecs;
+    // The scales are asked for first and stored last: a further wait at the
+    // end of each wave took the call from 213 us to 272.
+    const bool more = scales && first == 0;
+    S s = 0;
+    if (more && lane < blocks) s = scales[row * blocks + lane];
+#pragma unroll 4
+    for (uint32_t v = first + lane; v < last; v += 64) __builtin_nontemporal_store(from[v], to + v);
+    if (more) {
+      if (lane < blocks) row_scales[(size_t)slot * blocks + lane] = s;
+      for (uint32_t i = lane + 64; i < blocks; i += 64) row_scales[(size_t)slot * blocks + i] = scales[row * blocks + i];
+    }
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void gather_short_kernel(const T *__restrict__ x,
+                                                                const uint8_t *__restrict__ scales,
+                                                                const int32_t *__restrict__ slots,
+                                                                T *__restrict__ rows, uint8_t *__restrict__ row_scales,
+                                                                Short r, uint64_t B, uint32_t blocks, int k,
+                                                                uint32_t pairs) {
   const uint64_t step = (uint64_t)gridDim.x * kWaves;
   for (uint64_t u = wave_index(); u < r.units; u += step) {
     uint64_t row;
     uint32_t v;
-    if (!place_of<LONG>(r, u, B, per, &row, &v)) continue;
-    const int32_t *to = slots + row * k;
-    if (LONG ? v >= r.segs * 64 : scales && v < blocks) {
-      for (uint32_t i = LONG ? v - r.segs * 64 : v; i < blocks; i += 64) {
-        const uint8_t d = scales[row * blocks + i];
-        for (int j = 0; j < k; ++j) {
-          const uint32_t slot = (uint32_t)to[j];
-          if (slot < pairs) row_scales[(size_t)slot * blocks + i] = d;
-        }
-      }
-    }
-    if (v >= r.vecs) continue;
+    if (!place_of(r, u, B, &row, &v) || v >= r.vecs) continue;
     const T d = __builtin_nontemporal_load(x + row * r.vecs + v);
+    const bool scale = scales && v < blocks;  // (there are no more of them than vectors)
+    const uint8_t sc = scale ? scales[row * blocks + v] : 0;
     for (int j = 0; j < k; ++j) {
-      const uint32_t slot = (uint32_t)to[j];
-      if (slot < pairs) __builtin_nontemporal_store(d, rows + (size_t)slot * r.vecs + v);
+      const uint32_t slot = (uint32_t)slots[row * k + j];
+      if (slot >= pairs) continue;
+      __builtin_nontemporal_store(d, rows + (size_t)slot * r.vecs + v);
+      if (scale) row_scales[(size_t)slot * blocks + v] = sc;
     }
   }
 }
@@ -271,17 +262,25 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const T *__restrict__ 
 
 constexpr int kBatch = 8;  // slots whose rows are in flight at a time
 
+// A lane takes a vector of a row: of a long one (LONG) 64 of a wave's are
+// neighbours, and neighbouring waves have neighbouring pieces.
 template <bool LONG>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const u32x4 *__restrict__ Y,
                                                            const int32_t *__restrict__ slots,
                                                            const float *__restrict__ weights,
                                                            const u32x4 *__restrict__ shared, u32x4 *__restrict__ out,
-                                                           Rows r, uint64_t B, int k, uint32_t pairs) {
+                                                           Short r, uint32_t segs, uint64_t B, int k, uint32_t pairs) {
   const uint64_t step = (uint64_t)gridDim.x * kWaves;
   for (uint64_t u = wave_index(); u < r.units; u += step) {
     uint64_t row;
     uint32_t v;
-    if (!place_of<LONG>(r, u, B, r.segs, &row, &v) || v >= r.vecs) continue;
+    if constexpr (LONG) {
+      row = quotient(u, segs);
+      v = (uint32_t)(u - row * segs) * 64 + (threadIdx.x & 63);
+    } else if (!place_of(r, u, B, &row, &v)) {
+      continue;
+    }
+    if (v >= r.vecs) continue;
     const size_t at = row * r.vecs + v;
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (shared) widen8(__builtin_nontemporal_load(shared + at), o);
@@ -327,20 +326,57 @@ __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float acc) {
   return acc;
 }
 
+// k <= 2 of many rows: a wave takes a pair, reads its row of Y and writes that of dY in one
+// piece, and dout comes from the cache for all but the first of a row's waves.
+constexpr int kAhead = 4;  // vectors in flight a lane
+__global__ __launch_bounds__(kThreads) void combine_bwd_pair_kernel(
+    const u32x4 *__restrict__ Y, const int32_t *__restrict__ slots, const float *__restrict__ weights,
+    const u32x4 *__restrict__ dout, u32x4 *__restrict__ dY, float *__restrict__ dweights, uint32_t cvec, uint32_t k,
+    uint32_t pairs) {
+  const uint32_t lane = threadIdx.x & 63, step = gridDim.x * kWaves;
+  for (uint64_t u = wave_index(); u < pairs; u += step) {
+    const uint32_t p = (uint32_t)u, slot = (uint32_t)slots[p];
+    float dot = 0.f;
+    if (slot < pairs) {
+      const float w = weights[p];
+      const u32x4 *d = dout + (size_t)(p / k) * cvec, *y = Y + (size_t)slot * cvec;
+      u32x4 *to = dY + (size_t)slot * cvec;
+      for (uint32_t v0 = 0; v0 < cvec; v0 += 64 * kAhead) {
+        u32x4 a[kAhead], g[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const uint32_t v = v0 + 64 * i + lane;
+          if (v >= cvec) continue;
+          a[i] = __builtin_nontemporal_load(y + v);
+          g[i] = d[v];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const uint32_t v = v0 + 64 * i + lane;
+          if (v >= cvec) continue;
+          dot = dot8(g[i], a[i], dot);
+          store16_nt(to + v, weighted(g[i], w));
+        }
+      }
+    }
+    dot = wave_sum(dot);
+    if (lane == 0) dweights[p] = dot;
+  }
+}
+
 // A workgroup takes a row.
 constexpr int kRowWaves = 16;
 __global__ __launch_bounds__(64 * kRowWaves) void combine_bwd_kernel(
     const u32x4 *__restrict__ Y, const int32_t *__restrict__ slots, const float *__restrict__ weights,
     const u32x4 *__restrict__ dout, u32x4 *__restrict__ dY, float *__restrict__ dweights, uint32_t B, uint32_t cvec,
     int k, uint32_t pairs) {
-  __shared__ float part[2][kMaxChosen][kRowWaves];
+  __shared__ float part[kMaxChosen][kRowWaves];
   const uint32_t T = blockDim.x, waves = T >> 6;
   const int wave = threadIdx.x >> 6, row16 = (threadIdx.x & 63) >> 4;
-  int turn = 0;
-  for (uint32_t row = blockIdx.x; row < B; row += gridDim.x, turn ^= 1) {
-    const u32x4 *d = dout + (size_t)row * cvec;
-    const int32_t *from = slots + (size_t)row * k;
-    const float *weight = weights + (size_t)row * k;
+  for (uint64_t row = blockIdx.x; row < B; row += gridDim.x) {
+    const u32x4 *d = dout + row * cvec;
+    const int32_t *from = slots + row * k;
+    const float *weight = weights + row * k;
     for (int j0 = 0; j0 < k; j0 += kBatch) {
       float dot[kBatch];
 #pragma unroll
@@ -363,37 +399,37 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_bwd_kernel(
           store16_nt(dY + (size_t)slot * cvec + v, weighted(g, weight[j0 + j]));
         }
       }
-      wave_sums(dot);  // v[i] of lane row q: the sum of slot i + 2 (q & 1) + 4 (q / 2)
+      wave_sums(dot);  // dot[i] of lane row q: the sum of slot i + 2 (q & 1) + 4 (q / 2)
       if ((threadIdx.x & 15) == 0) {
 #pragma unroll
         for (int i = 0; i < kBatch / 4; ++i) {
           const int j = j0 + i + kBatch / 4 * (row16 & 1) + kBatch / 2 * (row16 >> 1);
-          if (j < k) part[turn][j][wave] = dot[i];
+          if (j < k) part[j][wave] = dot[i];
         }
       }
     }
     __syncthreads();
     if (threadIdx.x < (uint32_t)k) {
       float t = 0.f;
-      for (uint32_t w = 0; w < waves; ++w) t += part[turn][threadIdx.x][w];
-      dweights[(size_t)row * k + threadIdx.x] = t;
+      for (uint32_t w = 0; w < waves; ++w) t += part[threadIdx.x][w];
+      dweights[row * k + threadIdx.x] = t;
     }
+    __syncthreads();
   }
 }
 
-// Rows of up to 32 vectors, several a wave.
+// Short rows, several a wave.
 __global__ __launch_bounds__(kThreads) void combine_bwd_short_kernel(
     const u32x4 *__restrict__ Y, const int32_t *__restrict__ slots, const float *__restrict__ weights,
-    const u32x4 *__restrict__ dout, u32x4 *__restrict__ dY, float *__restrict__ dweights, Rows r, uint64_t B, int k,
+    const u32x4 *__restrict__ dout, u32x4 *__restrict__ dY, float *__restrict__ dweights, Short r, uint64_t B, int k,
     uint32_t pairs) {
   const uint64_t step = (uint64_t)gridDim.x * kWaves;
   for (uint64_t u = wave_index(); u < r.units; u += step) {
     uint64_t row;
     uint32_t v;
-    const bool real = place_of<false>(r, u, B, 1, &row, &v);
+    const bool real = place_of(r, u, B, &row, &v);
     const bool mine = real && v < r.vecs;
     const u32x4 g = mine ? dout[row * r.vecs + v] : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll 4
     for (int j = 0; j < k; ++j) {
       const uint32_t slot = real ? (uint32_t)slots[row * k + j] : ~0u;
       float dot = 0.f;
@@ -415,36 +451,72 @@ uint32_t grid_of(uint64_t total, int per) {
 
 bool is_long(int64_t vecs) { return vecs > 32; }
 
-// more: units a row beside its vectors' (LONG).
-Rows rows_of(int64_t B, int64_t vecs, int more) {
-  Rows r{};
-  r.vecs = (uint32_t)vecs;
-  r.segs = (uint32_t)((vecs + 63) / 64);
-  r.lanes = 1;
-  if (is_long(vecs)) {
-    r.units = (uint64_t)B * (r.segs + more);
-  } else {
-    while (r.lanes < vecs) r.lanes *= 2;
-    r.units = ((uint64_t)B * r.lanes + 63) / 64;
-  }
+Short short_of(int64_t B, int64_t vecs) {
+  Short r{0, 1, (uint32_t)vecs};
+  while (r.lanes < vecs) r.lanes *= 2;
+  r.units = ((uint64_t)B * r.lanes + 63) / 64;
   return r;
+}
+
+// Waves that the chip holds about once: with fewer pairs a row is shared by
+// several waves (512 rows, k=8, C=7168 in 8 bits: 14.4 us so, 18.0 with four
+// times the waves; from 2048 rows on they are the same).
+constexpr int64_t kManyWaves = 4096;
+
+// Scales beyond what the L2 caches hold together leave them as parts of lines
+// when they are written between the rows: a launch of their own is faster
+// there (k=8, C=7168, us with the order: 187 apart, 178 between at 14336 rows,
+// 25.7 MB of scales; 210, 258 at 16384, 29.4 MB).
+constexpr int64_t kScalesApart = 26 << 20;
+
+template <class T, class S>
+hipError_t gather_long(int64_t B, int k, int64_t vecs, const void *x, const void *scales, int64_t blocks,
+                       const int32_t *slots, void *rows, void *row_scales, hipStream_t st) {
+  const int64_t pairs = B * k, segs = (vecs + 63) / 64;
+  int64_t parts = (kManyWaves + pairs - 1) / pairs;
+  parts = parts < segs ? parts : segs;
+  const int64_t part = (segs + parts - 1) / parts * 64;
+  parts = (vecs + part - 1) / part;
+  const uint64_t units = (uint64_t)(pairs * parts);
+  gather_kernel<T, S><<<grid_of(units, kWaves), kThreads, 0, st>>>(
+      static_cast<const T *>(x), static_cast<const S *>(scales), slots, static_cast<T *>(rows),
+      static_cast<S *>(row_scales), units, (uint32_t)parts, (uint32_t)part, (uint32_t)vecs, (uint32_t)blocks,
+      (uint32_t)k, (uint32_t)pairs);
+  return hipGetLastError();
 }
 
 template <class T>
 hipError_t gather_t(int64_t B, int k, int64_t vecs, const void *x, const uint8_t *scales, int64_t blocks,
                     const int32_t *slots, void *rows, uint8_t *row_scales, hipStream_t st) {
-  const Rows r = rows_of(B, vecs, scales ? 1 : 0);
-  const auto kernel = is_long(vecs) ? gather_kernel<T, true> : gather_kernel<T, false>;
-  kernel<<<grid_of(r.units, kWaves), kThreads, 0, st>>>(static_cast<const T *>(x), scales, slots,
-                                                        static_cast<T *>(rows), row_scales, r, (uint64_t)B,
-                                                        (uint32_t)blocks, k, (uint32_t)(B * k));
+  if (is_long(vecs)) {
+    const int64_t pairs = B * k;
+    // Scale bytes four at a time where rows and tensors allow it.
+    const uintptr_t where = reinterpret_cast<uintptr_t>(scales) | reinterpret_cast<uintptr_t>(row_scales);
+    if (blocks % 4 == 0 && where % 4 == 0 && blocks <= 256 && pairs * blocks > kScalesApart) {
+      const hipError_t e = gather_long<T, uint8_t>(B, k, vecs, x, nullptr, 0, slots, rows, nullptr, st);
+      if (e != hipSuccess) return e;
+      const Short r = short_of(B, blocks / 4);
+      gather_short_kernel<uint32_t><<<grid_of(r.units, kWaves), kThreads, 0, st>>>(
+          reinterpret_cast<const uint32_t *>(scales), nullptr, slots, reinterpret_cast<uint32_t *>(row_scales), nullptr,
+          r, (uint64_t)B, 0, k, (uint32_t)pairs);
+      return hipGetLastError();
+    }
+    if (blocks % 4 == 0 && where % 4 == 0)
+      return gather_long<T, uint32_t>(B, k, vecs, x, scales, blocks / 4, slots, rows, row_scales, st);
+    return gather_long<T, uint8_t>(B, k, vecs, x, scales, blocks, slots, rows, row_scales, st);
+  }
+  const Short r = short_of(B, vecs);
+  gather_short_kernel<T><<<grid_of(r.units, kWaves), kThreads, 0, st>>>(
+      static_cast<const T *>(x), scales, slots, static_cast<T *>(rows), row_scales, r, (uint64_t)B, (uint32_t)blocks,
+      k, (uint32_t)(B * k));
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Tiles of at least 1024 pairs, at most 256 of them: their counts are added up
-// by every workgroup of the second kernel.
+// Tiles of at least 4096 pairs, at most 256 of them: their counts are added up
+// by every workgroup of the second kernel, which is most of its time (all of
+// them read 4 tiles E bytes).
 OrderPlan plan_experts_order(int64_t pairs, int E) {
   OrderPlan p;
   constexpr int64_t kMost = 256;
@@ -457,19 +529,23 @@ OrderPlan plan_experts_order(int64_t pairs, int E) {
 
 hipError_t launch_experts_order(const OrderPlan &p, int64_t pairs, int E, const int32_t *ids, int32_t *slots,
                                 int32_t *offsets, void *ws, hipStream_t st) {
-  if (pairs <= kOnePairs) {
-    order_kernel<<<1, 64 * kOneWaves, (size_t)kOneWaves * E * 2, st>>>(ids, (uint32_t)pairs, E, slots, offsets);
+  uint32_t *counts = static_cast<uint32_t *>(ws), stride = 64;
+  const uint32_t tiles = (uint32_t)p.tiles, tile = (uint32_t)p.tile;
+  const size_t lds = (size_t)kRankWaves * E * 2;
+  if (tiles == 1) {
+    rank_kernel<true><<<1, 64 * kRankWaves, lds, st>>>(ids, (uint32_t)pairs, tile, E, slots, counts, offsets);
     return hipGetLastError();
   }
-  uint32_t *counts = static_cast<uint32_t *>(ws), stride = 64;
-  while (stride < (uint32_t)E) stride *= 2;
-  const uint32_t tiles = (uint32_t)p.tiles;
-  rank_kernel<<<tiles, 64 * kRankWaves, (size_t)kRankWaves * E * 2, st>>>(ids, (uint32_t)pairs, (uint32_t)p.tile, E,
-                                                                          slots, counts);
+  rank_kernel<false><<<tiles, 64 * kRankWaves, lds, st>>>(ids, (uint32_t)pairs, tile, E, slots, counts, offsets);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  place_kernel<<<tiles, kPlaceThreads, 0, st>>>(ids, (uint32_t)pairs, (uint32_t)p.tile, tiles, E, stride, counts,
-                                                slots, offsets);
+  while (stride < (uint32_t)E) stride *= 2;
+  // Shares divide a tile; about 256 workgroups where there are pairs enough.
+  uint32_t share = tile;
+  while (share > kPlaceThreads && pairs / share < 128) share /= 2;
+  place_kernel<<<(uint32_t)((pairs + share - 1) / share), kPlaceThreads, 0, st>>>(ids, (uint32_t)pairs, share, tile,
+                                                                                  tiles, E, stride, counts, slots,
+                                                                                  offsets);
   return hipGetLastError();
 }
 
@@ -483,11 +559,18 @@ hipError_t launch_experts_gather(int64_t B, int k, int64_t C, const void *x, con
 
 hipError_t launch_experts_combine(int64_t B, int k, int64_t C, const void *Y, const int32_t *slots,
                                   const float *weights, const void *shared, void *out, hipStream_t st) {
-  const Rows r = rows_of(B, C / 8, 0);
-  const auto kernel = is_long(C / 8) ? combine_kernel<true> : combine_kernel<false>;
-  kernel<<<grid_of(r.units, kWaves), kThreads, 0, st>>>(static_cast<const u32x4 *>(Y), slots, weights,
-                                                        static_cast<const u32x4 *>(shared), static_cast<u32x4 *>(out),
-                                                        r, (uint64_t)B, k, (uint32_t)(B * k));
+  const auto *y = static_cast<const u32x4 *>(Y), *add = static_cast<const u32x4 *>(shared);
+  u32x4 *o = static_cast<u32x4 *>(out);
+  const uint32_t pairs = (uint32_t)(B * k), segs = (uint32_t)((C / 8 + 63) / 64);
+  if (is_long(C / 8)) {
+    const Short r{(uint64_t)B * segs, 64, (uint32_t)(C / 8)};
+    combine_kernel<true><<<grid_of(r.units, kWaves), kThreads, 0, st>>>(y, slots, weights, add, o, r, segs,
+                                                                        (uint64_t)B, k, pairs);
+  } else {
+    const Short r = short_of(B, C / 8);
+    combine_kernel<false><<<grid_of(r.units, kWaves), kThreads, 0, st>>>(y, slots, weights, add, o, r, segs,
+                                                                         (uint64_t)B, k, pairs);
+  }
   return hipGetLastError();
 }
 
@@ -498,13 +581,20 @@ hipError_t launch_experts_combine_bwd(int64_t B, int k, int64_t C, const void *Y
   u32x4 *dy = static_cast<u32x4 *>(dY);
   const uint32_t pairs = (uint32_t)(B * k), cvec = (uint32_t)(C / 8);
   if (!is_long(cvec)) {
-    const Rows r = rows_of(B, cvec, 0);
+    const Short r = short_of(B, cvec);
     combine_bwd_short_kernel<<<grid_of(r.units, kWaves), kThreads, 0, st>>>(y, slots, weights, g, dy, dweights, r,
                                                                             (uint64_t)B, k, pairs);
+  } else if (k <= 2 && pairs >= 2048) {
+    // A workgroup a row has few loads in flight at k = 1 and 2 (C=7168, us: 30
+    // against 40 for 4096 rows at k=1, 51 against 59 at k=2); from k = 3 on it
+    // is faster (183 against 188 at k=8), and with few rows (4.5 against 7.4
+    // for 64 at k=2).
+    combine_bwd_pair_kernel<<<grid_of(pairs, kWaves), kThreads, 0, st>>>(y, slots, weights, g, dy, dweights, cvec,
+                                                                         (uint32_t)k, pairs);
   } else {
     const uint32_t waves = (cvec + 63) / 64 < kRowWaves ? (cvec + 63) / 64 : kRowWaves;
-    const uint32_t grid = (uint32_t)(B < (1 << 21) ? B : (1 << 21));
-    combine_bwd_kernel<<<grid, 64 * waves, 0, st>>>(y, slots, weights, g, dy, dweights, (uint32_t)B, cvec, k, pairs);
+    combine_bwd_kernel<<<(uint32_t)(B < (1 << 21) ? B : (1 << 21)), 64 * waves, 0, st>>>(y, slots, weights, g, dy, dweights, (uint32_t)B, cvec, k,
+                                                           pairs);
   }
   return hipGetLastError();
 }
