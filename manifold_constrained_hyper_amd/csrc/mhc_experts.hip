@@ -201,9 +201,11 @@ __device__ __forceinline__ bool place_of(const Short &r, uint64_t u, uint64_t B,
 // -- gather -----------------------------------------------------------------
 //
 // A wave copies a row (T: vectors of 16 or 8 bytes), or one of `parts` of it,
-// to one place, in one piece: 182 us for the 940 MB of B=16384, k=8, C=7168 in
-// 8 bits (5.8 TB/s with what is read), where waves that write 1 KB each to all
-// of the row's places take 210.  The row's k waves find it in the cache.
+// to one place, in one piece; the row's k waves share it in the cache.  Bound
+// by the writes: 198 us for the codes of B=16384, k=8, C=7168 (1.06 GB, 5.3
+// TB/s; 183 without any read).  Waves that write 1 KB each to all of a row's
+// places take 20 us more.
+constexpr int kGatherAhead = 8;  // vectors in flight a lane (222 us with the order; with four 242)
 template <class T, class S>
 __global__ __launch_bounds__(kThreads) void gather_kernel(const T *__restrict__ x, const S *__restrict__ scales,
                                                           const int32_t *__restrict__ slots, T *__restrict__ rows,
@@ -225,8 +227,15 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const T *__restrict__ 
     const bool more = scales && first == 0;
     S s = 0;
     if (more && lane < blocks) s = scales[row * blocks + lane];
-#pragma unroll 4
-    for (uint32_t v = first + lane; v < last; v += 64) __builtin_nontemporal_store(from[v], to + v);
+    for (uint32_t v0 = first + lane; v0 < last; v0 += 64 * kGatherAhead) {
+      T d[kGatherAhead];
+#pragma unroll
+      for (int i = 0; i < kGatherAhead; ++i)
+        if (v0 + 64 * i < last) d[i] = from[v0 + 64 * i];
+#pragma unroll
+      for (int i = 0; i < kGatherAhead; ++i)
+        if (v0 + 64 * i < last) __builtin_nontemporal_store(d[i], to + v0 + 64 * i);
+    }
     if (more) {
       if (lane < blocks) row_scales[(size_t)slot * blocks + lane] = s;
       for (uint32_t i = lane + 64; i < blocks; i += 64) row_scales[(size_t)slot * blocks + i] = scales[row * blocks + i];
@@ -328,7 +337,7 @@ __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float acc) {
 
 // k <= 2 of many rows: a wave takes a pair, reads its row of Y and writes that of dY in one
 // piece, and dout comes from the cache for all but the first of a row's waves.
-constexpr int kAhead = 4;  // vectors in flight a lane
+constexpr int kAhead = 4;  // vectors in flight a lane (with eight 33 us, not 30, for 4096 rows at k=1, C=7168)
 __global__ __launch_bounds__(kThreads) void combine_bwd_pair_kernel(
     const u32x4 *__restrict__ Y, const int32_t *__restrict__ slots, const float *__restrict__ weights,
     const u32x4 *__restrict__ dout, u32x4 *__restrict__ dY, float *__restrict__ dweights, uint32_t cvec, uint32_t k,
