@@ -77,15 +77,15 @@ def weights_of(x, ids, softmax, renorm, scale):
 
 
 def route(logits, k, bias=None, groups=1, top_groups=1, softmax=False, renorm=True, scale=1.0):
-    """(ids int [B, k], weights [B, k])."""
+    """(ids int [B, k], weights [B, k]).  Without a bias the order is that of the logits."""
     logits = clean(logits)
     B, E = logits.shape
     ids, weights = np.full((B, k), -1, np.int64), np.zeros((B, k))
     for b in range(B):
         x = logits[b]
-        choice = _softmax(x) if softmax else sigmoid(x)
+        choice = x
         if bias is not None:
-            choice = choice + np.asarray(bias, np.float64)
+            choice = (_softmax(x) if softmax else sigmoid(x)) + np.asarray(bias, np.float64)
         choice = np.where((x > -np.inf) & ~np.isnan(choice), choice, -np.inf)
         if top_groups < groups:
             each = choice.reshape(groups, -1)
