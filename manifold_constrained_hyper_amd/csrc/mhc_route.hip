@@ -8,6 +8,10 @@
 // these cannot tell the order of two and it matters, the chosen ones and the
 // two behind them (or the groups' sums) are formed once more and compared whole.
 //
+// Bound by vector instructions: 1514 a wave of four rows of 256 experts in
+// eight groups, of which the scores in 64 bits are a third, the sort and the k
+// maxima half; 18 us at B=16384 (17.8 MB).  One row takes 5.5.
+//
 // Renormalised weights are formed from exp(min(x, 0) - most) / (1 + exp(-|x|)),
 // the scores times a common factor under which the largest does not underflow.
 #include "mhc_experts.h"
@@ -23,29 +27,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // A logit as it counts: NaN is minus infinity (no expert), plus infinity the
 // largest number.
-__device__ __forceinline__ float clean(float x) { return x != x ? -__builtin_inff() : fminf(x, kLargest); }
+__device__ __forceinline__ float clean(float x) {
+  return fminf(fmaxf(x, -__builtin_inff()), kLargest);  // (the maximum of a NaN and a number is the number)
+}
 __device__ __forceinline__ float logit_at(const void *p, size_t i, bool bf16) {
   return clean(bf16 ? bf16_lo(static_cast<const uint16_t *>(p)[i]) : static_cast<const float *>(p)[i]);
 }
-template <bool BF16>
-__device__ __forceinline__ float logit_at(const void *p, size_t i) {
-  return logit_at(p, i, BF16);
-}
-
-template <class T>
-__device__ __forceinline__ T wave_total(T x) {
-  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
-  return x;
-}
-template <class T>
-__device__ __forceinline__ T wave_max(T x) {
-  for (int d = 32; d > 0; d >>= 1) {
-    const T y = __shfl_xor(x, d);
-    x = y > x ? y : x;
-  }
-  return x;
-}
-
 // What a wave's lanes wrote to LDS is there for its other lanes (its LDS
 // accesses keep their order; the compiler has to keep it too).
 __device__ __forceinline__ void wave_lds_fence() {
@@ -128,54 +115,91 @@ __device__ __forceinline__ float row_sum(float x) {
 // A key is the choice as a double whose ten lowest bits hold the index, so that
 // one maximum compares the choices and, of equal ones, takes the lowest index.
 constexpr int kIndexMask = kMaxExperts - 1;
-constexpr double kNoKey = -1e300;  // below every choice
+constexpr double kNoKey = -1e300;  // below every choice; with an index in it, it is one still
+__device__ __forceinline__ bool is_key(double key) { return key > -1e299; }
 
 __device__ __forceinline__ double key_of(double choice, int index) {
-  const u32x2 w = __builtin_bit_cast(u32x2, choice);
-  const uint32_t low = (int)w[1] < 0 ? index : kIndexMask - index;
+  const u32x2 w = __builtin_bit_cast(u32x2, __builtin_fmax(choice, kNoKey));
+  const uint32_t low = (int)w[1] < 0 ? index : index ^ kIndexMask;
   return __builtin_bit_cast(double, u32x2{(w[0] & ~(uint32_t)kIndexMask) | low, w[1]});
 }
 __device__ __forceinline__ int index_of(double key) {
   const u32x2 w = __builtin_bit_cast(u32x2, key);
   const int low = w[0] & kIndexMask;
-  return key == kNoKey ? -1 : (int)w[1] < 0 ? low : kIndexMask - low;
+  return !is_key(key) ? -1 : (int)w[1] < 0 ? low : low ^ kIndexMask;
 }
 __device__ __forceinline__ double choice_of(double key) {
   const u32x2 w = __builtin_bit_cast(u32x2, key);
   return __builtin_bit_cast(double, u32x2{w[0] & ~(uint32_t)kIndexMask, w[1]});
 }
 
-// exp(x) to 2^-50 of its value, from 2^n exp(r), |r| <= ln 2 / 2, by the power
-// series up to r^12 (the next term is below 2^-52); |x| beyond 700 counts as 700.
-__device__ __forceinline__ double exp_64(double x) {
-  x = __builtin_fmin(__builtin_fmax(x, -700.0), 700.0);
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  // ln 2 in two parts, the upper one with few enough bits for n times it to be exact
-  const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x));
-  double p = 1.0 / 479001600.0;
-  constexpr double kInverse[] = {1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320, 1.0 / 5040, 1.0 / 720,
-                                 1.0 / 120,      1.0 / 24,      1.0 / 6,      0.5,         1.0,        1.0};
+// exp of each x, |x| <= 700, from 2^n exp(r), |r| <= ln 2 / 2, by the power
+// series up to r^TERMS: to 2^-50 of its value with 12 terms (the next one is
+// below 2^-52), to 2^-36 with 9.  N of them go step by step, as each is a chain
+// of dependent products.
+template <int TERMS, int N>
+__device__ __forceinline__ void exp_64(double (&x)[N]) {
+  constexpr double kInverse[] = {1.0,         1.0,          0.5,           1.0 / 6,        1.0 / 24,
+                                 1.0 / 120,   1.0 / 720,    1.0 / 5040,    1.0 / 40320,    1.0 / 362880,
+                                 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
+  constexpr double kShift = 0x1.8p52;  // a number added to it is rounded to an integer in the low bits
+  double n[N], p[N];
 #pragma unroll
-  for (double c : kInverse) p = fma(p, r, c);
-  return __builtin_amdgcn_ldexp(p, (int)n);
+  for (int i = 0; i < N; ++i) n[i] = fma(x[i], 1.4426950408889634, kShift);
+  int e[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    e[i] = (int)__builtin_bit_cast(u32x2, n[i])[0];
+    n[i] -= kShift;
+  }
+  // ln 2 in two parts, the upper one with few enough bits for n times it to be exact
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = fma(n[i], -0.6931471803691238, x[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = fma(n[i], -1.9082149292705877e-10, x[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = kInverse[TERMS];
+#pragma unroll
+  for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma(p[i], x[i], kInverse[t]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __builtin_amdgcn_ldexp(p[i], e[i]);
 }
-// 1 / x for x >= 1: the hardware's estimate and two Newton steps.
-__device__ __forceinline__ double reciprocal_64(double x) {
-  double y = __builtin_amdgcn_rcp(x);
-  y = fma(y, fma(-x, y, 1.0), y);
-  return fma(y, fma(-x, y, 1.0), y);
+// 1 / x for x >= 1: the hardware's estimate, to 2^-24, and Newton steps that
+// square its error.
+template <int STEPS, int N>
+__device__ __forceinline__ void reciprocal_64(double (&x)[N]) {
+  double y[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = __builtin_amdgcn_rcp(x[i]);
+#pragma unroll
+  for (int step = 0; step < STEPS; ++step)
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = fma(y[i], fma(-x[i], y[i], 1.0), y[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = y[i];
 }
-
-// The choice of a score and its bias, within what keys hold; kNoKey for a bias
-// that takes the expert out.
-__device__ __forceinline__ double choice_of_score(double score, float b) {
-  const double c = __builtin_fmin(score + (double)b, 1e299) + 0.0;  // (a zero without a sign)
-  return c > -1e299 && b == b ? c : kNoKey;
+// WHOLE: to all 64 bits; else to 2^-35.
+template <bool WHOLE, int N>
+__device__ __forceinline__ void sigmoid_64(const float (&x)[N], double (&s)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = -(double)__builtin_amdgcn_fmed3f(x[i], -700.0f, 700.0f);
+  exp_64<WHOLE ? 12 : 9>(s);
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] += 1.0;
+  reciprocal_64<WHOLE ? 2 : 1>(s);
 }
-__device__ __forceinline__ double key_of_choice(double score, float b, int index) {
-  const double c = choice_of_score(score, b);
-  return c == kNoKey ? kNoKey : key_of(c, index);
+// exp(x - top) for x <= top, 0 for minus infinity.
+template <bool WHOLE, int N>
+__device__ __forceinline__ void exp_from(const float (&x)[N], float top, double (&e)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) e[i] = __builtin_fmax((double)x[i] - (double)top, -700.0);
+  exp_64<WHOLE ? 12 : 9>(e);
+#pragma unroll
+  for (int i = 0; i < N; ++i) e[i] = x[i] > -__builtin_inff() ? e[i] : 0.0;
 }
+constexpr int kAtOnce = 2;
 
 // Batcher's odd-even merge sort, descending.
 template <int N>
@@ -196,9 +220,10 @@ __device__ __forceinline__ void sort_keys(double (&x)[N]) {
 }
 
 // How near two choices may be before their keys cannot tell their order,
-// relative to 1 + |choice|: a key's upper bits are off by 2^-42 of the choice,
-// the scores by less than 2^-47; twice that for two, and twice for safety.
-constexpr double kNear = 0x1p-40;
+// relative to 1 + |choice|: the scores are off by less than 2^-35 (of the
+// softmax's share of its sum too), a key's upper bits by 2^-42 of the choice;
+// twice that for two, and twice for safety.
+constexpr double kNear = 0x1p-33;
 
 // The weight (without the scale) of a chosen logit, one a lane of a row's L;
 // minus infinity where there is none.  top, all: the row's softmax.
@@ -215,8 +240,6 @@ __device__ __forceinline__ float weight_of(const RouteArgs &a, float x, float to
   return !is ? 0.f : a.softmax ? expf(x - top) / all : 1.0f / (1.0f + expf(-x));
 }
 
-constexpr int kAtOnce = 4;  // exponentials a lane works on at a time (all 16 take 216 registers)
-
 struct RouteShape {
   int groups, size;  // groups that are chosen among (1: all experts), experts of one
   int lanes_log;     // lanes of a group: 1 << lanes_log
@@ -227,86 +250,138 @@ struct RouteShape {
 // lanes' first keys is taken k times, and twice more to see what is left out:
 // KL >= min(V, k + 2) of a lane's keys can be among them.
 template <int V, int KL, int L>
-__global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, RouteShape g,
-                                                            const void *__restrict__ logits,
-                                                            const float *__restrict__ bias, int32_t *__restrict__ ids,
-                                                            float *__restrict__ weights, uint32_t B) {
-  extern __shared__ float shared[];  // each wave's rows of logits, then the bias
+__global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
+    RouteArgs a, RouteShape g, const void *__restrict__ logits, const float *__restrict__ bias,
+    int32_t *__restrict__ ids, float *__restrict__ weights, uint32_t B) {
+  // Each wave's rows of logits, the bias, and room behind both for what lanes
+  // read past their experts (and pass over).
+  extern __shared__ float shared[];
   constexpr int kRows = 64 / L;
-  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), l = lane & (L - 1), r = lane / L;
-  float *x_lds = shared + wave * kRows * a.E, *bias_lds = shared + kWaves * kRows * a.E;
+  const int wave = uniform((int)threadIdx.x >> 6);
+  float *x_lds = shared + wave * kRows * a.E, *bias_lds = shared + kWaves * kRows * a.E + L * V;
   if (bias) {
-    for (int i = threadIdx.x; i < a.E; i += 64 * kWaves) bias_lds[i] = bias[i];
+    for (int i = threadIdx.x; i < a.E; i += 64 * kWaves) bias_lds[i] = clean(bias[i]);
     __syncthreads();
   }
   const float none = -__builtin_inff();
-  const int group = l >> g.lanes_log;
-  // Lanes start at different ones of their experts, so that their reads fall
-  // on different LDS banks.
-  const int turn = (L == 64 ? lane / (64 / V) : r + 4 * (l / (64 / V))) & (V - 1);
   const bool sums = a.softmax && (bias || !a.renorm);
   for (uint64_t first = ((uint64_t)blockIdx.x * kWaves + wave) * kRows; first < B;
        first += (uint64_t)gridDim.x * kWaves * kRows) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // or the compiler keeps 64 registers of indexes and addresses over the rows
+    const int l = lane & (L - 1), r = lane / L, group = l >> g.lanes_log;
+    const int start = (l & ((1 << g.lanes_log) - 1)) * V;  // of the lane's experts in the group
+    // Lanes start at different ones of their experts, so that their reads fall
+    // on different LDS banks.
+    const int turn = (L == 64 ? lane / (64 / V) : r + 4 * (l / (64 / V))) & (V - 1);
     const uint64_t row = first + r;
     const bool real = row < B;
     const int total = (int)(B - first < kRows ? B - first : kRows) * a.E;
     const float *x_row = x_lds + r * a.E;
     float x[V];
-    if (a.bf16) {
-      const uint16_t *from = static_cast<const uint16_t *>(logits) + first * a.E;
-#pragma unroll
-      for (int t = 0; t < V; ++t) x[t] = lane + 64 * t < total ? bf16_lo(from[lane + 64 * t]) : 0.f;
-    } else {
+    if (total == 64 * V && !a.bf16) {
       const float *from = static_cast<const float *>(logits) + first * a.E;
 #pragma unroll
-      for (int t = 0; t < V; ++t) x[t] = lane + 64 * t < total ? from[lane + 64 * t] : 0.f;
-    }
+      for (int t = 0; t < V; ++t) x[t] = from[lane + 64 * t];
 #pragma unroll
-    for (int t = 0; t < V; ++t)
-      if (lane + 64 * t < total) x_lds[lane + 64 * t] = clean(x[t]);
+      for (int t = 0; t < V; ++t) x_lds[lane + 64 * t] = clean(x[t]);
+    } else {
+      if (a.bf16) {
+        const uint16_t *from = static_cast<const uint16_t *>(logits) + first * a.E;
+#pragma unroll
+        for (int t = 0; t < V; ++t) x[t] = lane + 64 * t < total ? bf16_lo(from[lane + 64 * t]) : 0.f;
+      } else {
+        const float *from = static_cast<const float *>(logits) + first * a.E;
+#pragma unroll
+        for (int t = 0; t < V; ++t) x[t] = lane + 64 * t < total ? from[lane + 64 * t] : 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < V; ++t)
+        if (lane + 64 * t < total) x_lds[lane + 64 * t] = clean(x[t]);
+    }
     wave_lds_fence();
-    int part = l & ((1 << g.lanes_log) - 1);
-    asm volatile("" : "+v"(part));  // or the compiler keeps 64 registers of indexes and addresses over the rows
-    const auto index_at = [&](int t) { return group * g.size + part * V + ((t + turn) & (V - 1)); };
+    const int mine = real && group < g.groups ? g.size - start : 0;  // experts of the lane, V or more: all
+    const int base = (group < g.groups ? group : 0) * g.size + start;
+    const auto index_at = [&](int t) { return base + (t ^ turn); };
 #pragma unroll
     for (int t = 0; t < V; ++t) {
-      const bool there = real && group < g.groups && part * V + ((t + turn) & (V - 1)) < g.size;
-      x[t] = there ? x_row[index_at(t)] : none;
+      const float z = x_row[index_at(t)];
+      x[t] = (t ^ turn) < mine ? z : none;
     }
     float top = none;
     double all = 0.0, key[V];
+    constexpr int kN = V < kAtOnce ? V : kAtOnce;
+    // f(x, key) for kN experts at a time.
+    const auto by_parts = [&](auto f) {
+#pragma unroll
+      for (int t = 0; t < V; t += kN) {
+        float z[kN];
+        double k[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) z[i] = x[t + i];
+        f(z, k);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) key[t + i] = k[i];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
     if (sums) {
 #pragma unroll
       for (int t = 0; t < V; ++t) top = fmaxf(top, x[t]);
       top = row_max<L>(top);
+      by_parts([&](const float(&z)[kN], double(&k)[kN]) {
+        exp_from<false>(z, top, k);
 #pragma unroll
-      for (int t = 0; t < V; ++t) {
-        key[t] = x[t] > none ? exp_64((double)x[t] - (double)top) : 0.0;
-        all += key[t];
-        if (t % kAtOnce == kAtOnce - 1) __builtin_amdgcn_sched_barrier(0);
-      }
+        for (int i = 0; i < kN; ++i) all += k[i];
+      });
       all = row_join<L>(all, [](double p, double q) { return p + q; });
     }
-    const double share = all > 0.0 ? reciprocal_64(all) : 0.0;
     if (bias) {
+      if (a.softmax) {
+        double share[1] = {__builtin_fmax(all, 1.0)};  // (the largest term of the sum is 1)
+        reciprocal_64<1>(share);
+#pragma unroll
+        for (int t = 0; t < V; ++t) key[t] *= share[0];
+      } else {
+        by_parts([&](const float(&z)[kN], double(&k)[kN]) { sigmoid_64<false>(z, k); });
+      }
 #pragma unroll
       for (int t = 0; t < V; ++t) {
-        const double score = a.softmax ? key[t] * share : reciprocal_64(1.0 + exp_64(-(double)x[t]));
-        key[t] = kNoKey;
-        if (x[t] > none) key[t] = key_of_choice(score, bias_lds[index_at(t)], index_at(t));
-        if (t % kAtOnce == kAtOnce - 1) __builtin_amdgcn_sched_barrier(0);
+        const float b = bias_lds[index_at(t)];
+        key[t] = key_of(key[t] + (double)(x[t] > none ? b : none), index_at(t));
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < V; ++t)
-        key[t] = x[t] > none ? key_of((double)(x[t] + 0.0f), index_at(t)) : kNoKey;  // (a zero without a sign)
+      for (int t = 0; t < V; ++t) key[t] = key_of((double)(x[t] + 0.0f), index_at(t));  // (a zero without a sign)
     }
-    // A candidate's choice once more, with all of its bits.
-    const auto whole = [&](double k) {
+    // A candidate's choice once more, with all of its bits, and the reciprocal
+    // of the softmax's sum that it needs (a loop: few rows come here).
+    const auto share_64 = [&]() {
+      if (!a.softmax) return 1.0;
+      double sum = 0.0;
+#pragma unroll 1
+      for (int t = 0; t < V; ++t) {
+        const float z[1] = {(t ^ turn) < mine ? x_row[index_at(t)] : none};
+        double c[1];
+        exp_from<true>(z, top, c);
+        sum += c[0];
+      }
+      double share[1] = {__builtin_fmax(row_join<L>(sum, [](double p, double q) { return p + q; }), 1.0)};
+      reciprocal_64<2>(share);
+      return share[0];
+    };
+    const auto whole = [&](double k, double share) {
       const int e = index_of(k);
       if (e < 0) return kNoKey;
-      const double z = x_row[e];
-      return choice_of_score(a.softmax ? exp_64(z - (double)top) * share : reciprocal_64(1.0 + exp_64(-z)), bias_lds[e]);
+      const float z[1] = {x_row[e]};
+      double c[1];
+      if (!a.softmax) {
+        sigmoid_64<true>(z, c);
+      } else {
+        exp_from<true>(z, top, c);
+        c[0] *= share;
+      }
+      return c[0] + (double)bias_lds[e];
     };
     sort_keys<V>(key);
     if (g.groups > 1) {
@@ -329,10 +404,10 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, RouteSh
       }
       if (group >= g.groups) a0 = a1 = kNoKey;
       double rank = a0, size = 0.0;  // size: of the choices that a rank is the sum of
-      if (bias && a0 != kNoKey) {
-        const double c0 = choice_of(a0), c1 = a1 != kNoKey ? choice_of(a1) : 0.0;
+      if (bias && is_key(a0)) {
+        const double c0 = choice_of(a0), c1 = is_key(a1) ? choice_of(a1) : 0.0;
         size = __builtin_fmax(__builtin_fabs(c0), __builtin_fabs(c1));
-        rank = key_of(c0 + c1 + 0.0, group);
+        rank = key_of(c0 + c1, group);
       }
       const double own = rank;
       bool kept = false;
@@ -346,8 +421,9 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, RouteSh
       }
       if (bias) {
         const double next = row_max<L>(rank);
-        if (__ballot(next != kNoKey && !(last - next > 4 * kNear * (1.0 + row_max<L>(size))))) {
-          const double sum = own == kNoKey ? kNoKey : whole(a0) + (a1 != kNoKey ? whole(a1) : 0.0);
+        if (__ballot(is_key(next) && !(last - next > 4 * kNear * (1.0 + row_max<L>(size))))) {
+          const double share = share_64();
+          const double sum = !is_key(own) ? kNoKey : whole(a0, share) + (is_key(a1) ? whole(a1, share) : 0.0);
           int better = 0;  // groups before the own one
           for (int q = 0; q < g.groups; ++q) {
             const double other = __shfl(sum, (lane & ~(L - 1)) + (q << g.lanes_log));
@@ -379,7 +455,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, RouteSh
       const double edge = best;
       const auto close = [](double p, double q) {
         const double c = choice_of(p);
-        return q != kNoKey && !(c - choice_of(q) > kNear * (1.0 + __builtin_fabs(c)));
+        return is_key(q) && !(c - choice_of(q) > kNear * (1.0 + __builtin_fabs(c)));
       };
       take(a.k);
       if (__ballot(close(edge, best))) take(a.k + 1);
@@ -388,7 +464,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, RouteSh
       const double next = __shfl_down(chosen, 1);
       const bool same = z == __shfl_down(z, 1) && b == __shfl_down(b, 1);
       if (__ballot(l <= a.k && id >= 0 && close(chosen, next) && !same)) {
-        const double c = whole(chosen);
+        const double c = whole(chosen, share_64());
         int better = 0;
         for (int q = 0; q < a.k + 2; ++q) {
           const double other = __shfl(c, (lane & ~(L - 1)) + q);
@@ -408,62 +484,103 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, RouteSh
   }
 }
 
-template <bool BF16>
+// -- gradient ---------------------------------------------------------------
+//
+//   softmax          dx_i = p_i (dw_i - sum p dw)           over all experts
+//   renormalised     dz_j = w_j (dw_j - sum w dw)           over the chosen ones
+//   sigmoid          dx_j = dz_j (1 - sigmoid(x_j)), dz_j = sigmoid(x_j) dw_j if
+//                    not renormalised
+//
+// L lanes take a row and form its gradient in LDS (the chosen ones' parts are
+// added to zeros or to the softmax's), which leaves in memory order, V values a
+// lane.  B=16383, E=100, k=6, softmax in bf16: 6.1 us (6.9 MB, and a launch is
+// 3.4).
+template <int V, int L>
 __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteArgs a, const void *__restrict__ logits,
                                                                 const int32_t *__restrict__ ids,
                                                                 const float *__restrict__ dweights,
-                                                                void *__restrict__ dlogits, uint32_t B) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+                                                                void *__restrict__ dlogits, uint32_t B, bool pairs) {
+  extern __shared__ float shared[];
+  constexpr int kRows = 64 / L;
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), l = lane & (L - 1), r = lane / L;
+  float *out = shared + wave * kRows * a.E, *out_row = out + r * a.E;
   const float none = -__builtin_inff();
-  for (uint64_t row = (uint64_t)blockIdx.x * kWaves + wave; row < B; row += (uint64_t)gridDim.x * kWaves) {
-    int id = lane < a.k ? ids[row * a.k + lane] : -1;
+  const bool every = a.softmax && !a.renorm;
+  for (uint64_t first = ((uint64_t)blockIdx.x * kWaves + wave) * kRows; first < B;
+       first += (uint64_t)gridDim.x * kWaves * kRows) {
+    const uint64_t row = first + r;
+    const bool real = row < B, slot = real && l < a.k;
+    const int total = (int)(B - first < kRows ? B - first : kRows) * a.E;
+    int id = slot ? ids[row * a.k + l] : -1;
     if (id >= a.E) id = -1;
-    const float x = id >= 0 ? logit_at<BF16>(logits, row * a.E + id) : none;
-    const float dw = id >= 0 ? a.scale * dweights[row * a.k + lane] : 0.f;
-    float top = none, inv_total = 0.f, along = 0.f;
-    float d = 0.f;  // the chosen logit's gradient (without -p along of the plain softmax)
-    const bool every = a.softmax && !a.renorm;
+    const float given = slot ? dweights[row * a.k + l] : 0.f;
+    const float x = id >= 0 ? logit_at(logits, row * a.E + id, a.bf16) : none;
+    const float dw = id >= 0 ? a.scale * given : 0.f;
+    float d;  // the chosen logit's part
     if (every) {
-      for (int i = lane; i < a.E; i += 64) top = fmaxf(top, logit_at<BF16>(logits, row * a.E + i));
-      top = wave_max(top);
-      float total = 0.f;
-      for (int i = lane; i < a.E; i += 64) {
-        const float y = logit_at<BF16>(logits, row * a.E + i);
-        total += y > none ? expf(y - top) : 0.f;
+      float y[V];
+#pragma unroll
+      for (int t = 0; t < V; ++t)
+        y[t] = lane + 64 * t < total ? logit_at(logits, first * a.E + lane + 64 * t, a.bf16) : none;
+#pragma unroll
+      for (int t = 0; t < V; ++t)
+        if (lane + 64 * t < total) out[lane + 64 * t] = y[t];
+      wave_lds_fence();
+      float top = none, all = 0.f;
+#pragma unroll
+      for (int t = 0; t < V; ++t) {
+        y[t] = real && l + L * t < a.E ? out_row[l + L * t] : none;
+        top = fmaxf(top, y[t]);
       }
-      total = wave_total(total);
-      inv_total = total > 0.f ? 1.0f / total : 0.f;
-      const float p = x > none ? expf(x - top) * inv_total : 0.f;
-      d = p * dw;
-      along = wave_total(d);
-    } else if (a.renorm) {
-      const float z = !(x > none) ? none : a.softmax ? x : fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
-      const float most = wave_max(z);
-      const float e = z > none ? expf(z - most) : 0.f;
-      const float total = wave_total(e);
-      const float w = total > 0.f ? e / total : 0.f;
-      d = w * (dw - wave_total(w * dw));
+      top = row_max<L>(top);
+#pragma unroll
+      for (int t = 0; t < V; ++t) {
+        y[t] = y[t] > none ? __builtin_amdgcn_exp2f((y[t] - top) * kLog2e) : 0.f;
+        all += y[t];
+      }
+      all = row_sum<L>(all);
+      const float share = all > 0.f ? 1.0f / all : 0.f;
+      d = x > none ? __builtin_amdgcn_exp2f((x - top) * kLog2e) * share * dw : 0.f;
+      const float along = row_sum<L>(d) * share;
+      wave_lds_fence();
+#pragma unroll
+      for (int t = 0; t < V; ++t)
+        if (real && l + L * t < a.E) out_row[l + L * t] = -y[t] * along;
     } else {
-      d = dw / (1.0f + expf(-x));
+#pragma unroll
+      for (int t = 0; t < V; ++t)
+        if (lane + 64 * t < total) out[lane + 64 * t] = 0.f;
+      d = dw;
+      const float w = weight_of<L>(a, x, 0.f, 1.f);  // the score itself where it is not renormalised
+      d = a.renorm ? w * (dw - row_sum<L>(w * dw)) : w * dw;
+      if (!a.softmax) d = d / (1.0f + expf(x));
+      if (!(x > none)) d = 0.f;
     }
-    if (!a.softmax) d = x > none ? d / (1.0f + expf(x)) : 0.f;
-    for (int i = lane; i - lane < a.E; i += 64) {
-      float o = 0.f;
-      if (every && i < a.E) {
-        const float y = logit_at<BF16>(logits, row * a.E + i);
-        o = y > none ? -expf(y - top) * inv_total * along : 0.f;
-      }
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __shfl(id, j);
-        const float g = __shfl(d, j);
-        if (e == i) o += g;
-      }
-      if (i >= a.E) continue;
-      if constexpr (BF16)
-        static_cast<uint16_t *>(dlogits)[row * a.E + i] = (uint16_t)pack_bf16x2(o, 0.f);
-      else
-        static_cast<float *>(dlogits)[row * a.E + i] = o;
+    // An expert that was given twice: the first of its lanes adds all parts.
+    bool lead = id >= 0;
+    float part = 0.f;
+    for (int q = 0; q < a.k; ++q) {
+      const int e = __shfl(id, (lane & ~(L - 1)) + q);
+      const float other = __shfl(d, (lane & ~(L - 1)) + q);
+      if (e == id) part += other;
+      if (e == id && q < l) lead = false;
     }
+    wave_lds_fence();
+    if (lead) out_row[id] += part;
+    wave_lds_fence();
+    if (!a.bf16) {
+      float *to = static_cast<float *>(dlogits) + first * a.E;
+#pragma unroll
+      for (int t = 0; t < V; ++t)
+        if (lane + 64 * t < total) to[lane + 64 * t] = out[lane + 64 * t];
+    } else {
+      uint16_t *to = static_cast<uint16_t *>(dlogits) + first * a.E;
+      const int even = pairs ? total & ~1 : 0;
+      for (int i = 2 * lane; i < even; i += 128)
+        *reinterpret_cast<uint32_t *>(to + i) = pack_bf16x2(out[i], out[i + 1]);
+      for (int i = even + lane; i < total; i += 64) to[i] = (uint16_t)pack_bf16x2(out[i], 0.f);
+    }
+    wave_lds_fence();  // the next rows go where these were
   }
 }
 
@@ -485,13 +602,16 @@ int experts_a_lane(int L, const RouteArgs &a, RouteShape *g) {
   return v;
 }
 
-constexpr int64_t kManyRows = 2048;
+// Rows from which sixteen lanes take one, where it fits them: with fewer rows
+// the shorter chains of a wave a row count (E=256 in eight groups, k=8, us:
+// 8.3 against 7.6 at 2048 rows, 8.7 against 10.9 at 4096, 18.2 against 31 at 16384).
+constexpr int64_t kManyRows = 2560;
 
 template <int V, int KL, int L>
 hipError_t launch_route_t(int64_t B, const RouteArgs &a, const RouteShape &g, const void *logits, const float *bias,
                           int32_t *ids, float *weights, hipStream_t st) {
   constexpr int kRows = 64 / L;
-  const size_t lds = (size_t)(kWaves * kRows + (bias ? 1 : 0)) * a.E * sizeof(float);
+  const size_t lds = ((size_t)(kWaves * kRows + (bias ? 1 : 0)) * a.E + (bias ? 2 : 1) * L * V) * sizeof(float);
   route_kernel<V, KL, L><<<grid_of(kWaves * kRows, B), 64 * kWaves, lds, st>>>(a, g, logits, bias, ids, weights,
                                                                               (uint32_t)B);
   return hipGetLastError();
@@ -524,14 +644,29 @@ hipError_t launch_route(int64_t B, const RouteArgs &a, const void *logits, const
   }
 }
 
+// (The gradient, E=256 in fp32, us: 4.9 against 4.3 at 2048 rows, 5.2 against
+// 5.0 at 4096, 6.1 against 7.0 at 8192, 9.1 against 11.3 at 16384.)
+constexpr int64_t kManyRowsBwd = 4096;
+
+template <int V, int L>
+hipError_t launch_route_bwd_t(int64_t B, const RouteArgs &a, const void *logits, const int32_t *ids,
+                              const float *dweights, void *dlogits, hipStream_t st) {
+  constexpr int kRows = 64 / L;
+  // Pairs of bf16 are stored together where every wave's rows begin at four bytes.
+  const bool pairs = kRows * a.E % 2 == 0 && reinterpret_cast<uintptr_t>(dlogits) % 4 == 0;
+  route_bwd_kernel<V, L><<<grid_of(kWaves * kRows, B), 64 * kWaves, (size_t)kWaves * kRows * a.E * sizeof(float), st>>>(
+      a, logits, ids, dweights, dlogits, (uint32_t)B, pairs);
+  return hipGetLastError();
+}
+
 hipError_t launch_route_bwd(int64_t B, const RouteArgs &a, const void *logits, const int32_t *ids,
                             const float *dweights, void *dlogits, hipStream_t st) {
-  const uint32_t grid = grid_of(kWaves, B);
-  if (a.bf16)
-    route_bwd_kernel<true><<<grid, 64 * kWaves, 0, st>>>(a, logits, ids, dweights, dlogits, (uint32_t)B);
-  else
-    route_bwd_kernel<false><<<grid, 64 * kWaves, 0, st>>>(a, logits, ids, dweights, dlogits, (uint32_t)B);
-  return hipGetLastError();
+  const auto go = [&](auto kernel) { return kernel(B, a, logits, ids, dweights, dlogits, st); };
+  if (a.k <= 16 && a.E <= 256 && B >= kManyRowsBwd) {
+    return a.E <= 64 ? go(launch_route_bwd_t<4, 16>) : a.E <= 128 ? go(launch_route_bwd_t<8, 16>)
+                                                                  : go(launch_route_bwd_t<16, 16>);
+  }
+  return a.E <= 256 ? go(launch_route_bwd_t<4, 64>) : go(launch_route_bwd_t<16, 64>);
 }
 
 }  // namespace mhc
