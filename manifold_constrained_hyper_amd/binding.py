@@ -538,7 +538,7 @@ def mhc_lazy_prenorm_gemm(M, N, K, A, W, C, rstd=None, eps=1e-5, stream=None, ch
 
 def _device():
     """The current device's index, -1 where no device is in use yet."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
 
 
 def _dev_ptrs(dev, tensors, sizes):
@@ -547,6 +547,9 @@ def _dev_ptrs(dev, tensors, sizes):
     (the kernels would run on another device than the tensor's)."""
     out = []
     for t, (nbytes, esize, name) in zip(tensors, sizes):
+        if t is None:
+            out.append(None)
+            continue
         # What nearly every tensor is, decided in a few attribute reads.
         if (type(t) is torch.Tensor and t.get_device() == dev and dev >= 0 and t.is_contiguous()
                 and (t.itemsize == esize or esize is None) and t.nbytes >= nbytes):
@@ -826,19 +829,32 @@ def mhc_experts_order(B, k, E, ids, slots, offsets, workspace, workspace_bytes=N
 
 
 # Tensors of B rows and of their B * k pairs.
+
 @functools.lru_cache(maxsize=256)
-def _pair_sizes(B, k, C):
+def _gather_sizes(B, k, C, ckpt):
     B = max(B, 0)
-    return {"row": B * C * 2, "rows": B * k * C * 2, "pairs": B * k * 4, "codes": B * C, "scales": B * -(-C // 32)}
+    if not ckpt:
+        return ((B * C * 2, 2, "X"), (B * k * 4, 4, "slots"), (B * k * C * 2, 2, "rows"))
+    blocks = -(-C // 32)
+    return ((B * C, 1, "codes"), (B * blocks, 1, "scales"), (B * k * 4, 4, "slots"), (B * k * C, 1, "row_codes"),
+            (B * k * blocks, 1, "row_scales"))
+
+
+@functools.lru_cache(maxsize=256)
+def _combine_sizes(B, k, C, bwd):
+    B = max(B, 0)
+    rows, pairs, row = B * k * C * 2, B * k * 4, B * C * 2
+    sizes = ((rows, 2, "Y"), (pairs, 4, "slots"), (pairs, 4, "weights"))
+    if bwd:
+        return sizes + ((row, 2, "dF_out"), (rows, 2, "dY"), (pairs, 4, "dweights"))
+    return sizes + ((row, 2, "shared"), (row, 2, "F_out"))
 
 
 def mhc_experts_gather(B, k, C, X, slots, rows, stream=None, check=True):
     """rows[slots[b, j]] = X[b] (bf16; see include/mhc.h)."""
     B, k, C, dev = int(B), int(k), int(C), _device()
-    z = _pair_sizes(B, k, C)
-    X, slots, rows = _dev_ptrs(dev, (X, slots, rows), (
-        (z["row"], 2, "X"), (z["pairs"], 4, "slots"), (z["rows"], 2, "rows")))
-    st = load().mhc_experts_gather(B, k, C, X, slots, rows, _dev_stream(stream, dev))
+    st = load().mhc_experts_gather(B, k, C, *_dev_ptrs(dev, (X, slots, rows), _gather_sizes(B, k, C, False)),
+                                   _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_experts_gather")
     return st
@@ -847,10 +863,7 @@ def mhc_experts_gather(B, k, C, X, slots, rows, stream=None, check=True):
 def mhc_experts_gather_ckpt(B, k, C, codes, scales, slots, row_codes, row_scales, stream=None, check=True):
     """mhc_experts_gather of rows held in 8 bits, codes and scales (see include/mhc.h)."""
     B, k, C, dev = int(B), int(k), int(C), _device()
-    z = _pair_sizes(B, k, C)
-    p = _dev_ptrs(dev, (codes, scales, slots, row_codes, row_scales), (
-        (z["codes"], 1, "codes"), (z["scales"], 1, "scales"), (z["pairs"], 4, "slots"),
-        (z["codes"] * k, 1, "row_codes"), (z["scales"] * k, 1, "row_scales")))
+    p = _dev_ptrs(dev, (codes, scales, slots, row_codes, row_scales), _gather_sizes(B, k, C, True))
     st = load().mhc_experts_gather_ckpt(B, k, C, *p, _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_experts_gather_ckpt")
@@ -861,10 +874,7 @@ def mhc_experts_combine(B, k, C, Y, slots, weights, F_out, shared=None, stream=N
     """F_out[b] = shared[b] + sum_j weights[b, j] Y[slots[b, j]]; weights None:
     1, the gradient of mhc_experts_gather (see include/mhc.h)."""
     B, k, C, dev = int(B), int(k), int(C), _device()
-    z = _pair_sizes(B, k, C)
-    p = _dev_ptrs(dev, (Y, slots, weights, shared, F_out), (
-        (z["rows"], 2, "Y"), (z["pairs"], 4, "slots"), (z["pairs"], 4, "weights"), (z["row"], 2, "shared"),
-        (z["row"], 2, "F_out")))
+    p = _dev_ptrs(dev, (Y, slots, weights, shared, F_out), _combine_sizes(B, k, C, False))
     st = load().mhc_experts_combine(B, k, C, *p, _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_experts_combine")
@@ -874,10 +884,7 @@ def mhc_experts_combine(B, k, C, Y, slots, weights, F_out, shared=None, stream=N
 def mhc_experts_combine_bwd(B, k, C, Y, slots, weights, dF_out, dY, dweights, stream=None, check=True):
     """Gradients of mhc_experts_combine with respect to Y and the weights (see include/mhc.h)."""
     B, k, C, dev = int(B), int(k), int(C), _device()
-    z = _pair_sizes(B, k, C)
-    p = _dev_ptrs(dev, (Y, slots, weights, dF_out, dY, dweights), (
-        (z["rows"], 2, "Y"), (z["pairs"], 4, "slots"), (z["pairs"], 4, "weights"), (z["row"], 2, "dF_out"),
-        (z["rows"], 2, "dY"), (z["pairs"], 4, "dweights")))
+    p = _dev_ptrs(dev, (Y, slots, weights, dF_out, dY, dweights), _combine_sizes(B, k, C, True))
     st = load().mhc_experts_combine_bwd(B, k, C, *p, _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_experts_combine_bwd")

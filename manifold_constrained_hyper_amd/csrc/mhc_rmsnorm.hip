@@ -7,6 +7,10 @@
 // A workgroup takes a row, which stays in registers between the sum and its
 // use, so every tensor is read or written once.  Squares and sums are fp32
 // (products of two bf16 values are exact there).
+//
+// Bound by HBM: 144 us for B=16384, C=7168 with the shortcut in 8 bits (826 MB,
+// 5.7 TB/s), 163 for its gradients with the shortcut's (940 MB, 5.8 TB/s, of
+// which 5 us join dweight).  One row takes 3.6, a launch.
 #include "mhc_experts.h"
 #include "mhc_finish.h"
 #include "mhc_held.h"
@@ -49,7 +53,7 @@ __device__ __forceinline__ u32x4 pack8(const float (&y)[8]) {
   return u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
 }
 
-// V vectors of eight channels a thread.
+// V vectors of eight channels a thread, all of a row.
 template <int V>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a, uint32_t B, uint32_t cvec, uint32_t blocks,
                                                        float inv_c) {
@@ -58,24 +62,27 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a, uint32_t B, u
   int turn = 0;
   for (uint32_t row = blockIdx.x; row < B; row += gridDim.x, turn ^= 1) {
     const size_t first = (size_t)row * cvec;
-    u32x4 s[V];
+    u32x4 s[V], c[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t v = threadIdx.x + i * T;
+      s[i] = c[i] = u32x4{0u, 0u, 0u, 0u};
+      if (v >= cvec) continue;
+      s[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.x) + first + v);
+      if (a.shortcut) c[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.shortcut) + first + v);
+    }
     float sq = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint32_t v = threadIdx.x + i * T;
-      s[i] = u32x4{0u, 0u, 0u, 0u};
-      if (v < cvec) {
-        s[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.x) + first + v);
-        if (a.shortcut) {
-          const u32x4 c = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.shortcut) + first + v);
+      if (a.shortcut) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            s[i][w] = pack_bf16x2(bf16_lo(s[i][w]) + bf16_lo(c[w]), bf16_hi(s[i][w]) + bf16_hi(c[w]));
-          if (a.sum) store16_nt(static_cast<u32x4 *>(a.sum) + first + v, s[i]);
-        }
+        for (int q = 0; q < 4; ++q)
+          s[i][q] = pack_bf16x2(bf16_lo(s[i][q]) + bf16_lo(c[i][q]), bf16_hi(s[i][q]) + bf16_hi(c[i][q]));
+        if (a.sum && v < cvec) store16_nt(static_cast<u32x4 *>(a.sum) + first + v, s[i]);
       }
 #pragma unroll
-      for (int w = 0; w < 4; ++w) sq = dot2_bf16(s[i][w], s[i][w], sq);
+      for (int q = 0; q < 4; ++q) sq = dot2_bf16(s[i][q], s[i][q], sq);
     }
     const float rstd = 1.0f / sqrtf(group_total(sq, part[turn]) * inv_c + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
@@ -84,7 +91,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a, uint32_t B, u
       const uint32_t v = threadIdx.x + i * T;
       float y[8], w[8];
       widen8(s[i], y);
-      if (v < cvec) load_weight(a.weight, v, w);
+      load_weight(v < cvec ? a.weight : nullptr, v, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = v < cvec ? y[e] * rstd * w[e] : 0.f;
       if (a.y && v < cvec) store16_nt(static_cast<u32x4 *>(a.y) + first + v, pack8(y));
@@ -106,39 +113,82 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a, uint32_t B, u
   }
 }
 
+// The partial sums of dweight stay in registers; with one vector a thread the
+// weight does too, and the next row is loaded while this one is worked on.
+// From four on a row does not fit beside them and is read twice (from the cache).
+template <int V>
+struct BwdRow {
+  u32x4 s[V], d[V], p[V];
+  float rstd;
+};
+template <int V>
+__device__ __forceinline__ void load_row(const NormBwdArgs &a, uint32_t row, uint32_t cvec, BwdRow<V> &x) {
+  const size_t first = (size_t)row * cvec;
+  x.rstd = a.rstd[row];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t v = threadIdx.x + i * blockDim.x;
+    x.s[i] = x.d[i] = x.p[i] = u32x4{0u, 0u, 0u, 0u};
+    if (v >= cvec) continue;
+    x.s[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.sum) + first + v);
+    x.d[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.dy) + first + v);
+    if (a.dsum) x.p[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.dsum) + first + v);
+  }
+}
+
 template <int V>
 __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, float *partial, uint32_t B, uint32_t cvec,
                                                            float inv_c) {
   __shared__ float part[2][kMostWaves];
   const uint32_t T = blockDim.x;
-  float dw[V][8];
+  constexpr bool kStay = V == 1, kKeep = V <= 2;
+  constexpr int kHeld = kStay ? V : 1;
+  float dw[V][8], held[kHeld][8];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+  BwdRow<kHeld> next;
+  if constexpr (kStay) {
+    load_weight(threadIdx.x < cvec ? a.weight : nullptr, threadIdx.x, held[0]);
+    load_row<kHeld>(a, blockIdx.x, cvec, next);
+  }
+  const auto weight_at = [&](uint32_t v, float(&w)[8]) {
+    if constexpr (kStay) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = held[0][e];
+    } else {
+      load_weight(v < cvec ? a.weight : nullptr, v, w);
+    }
+  };
   int turn = 0;
   for (uint32_t row = blockIdx.x; row < B; row += gridDim.x, turn ^= 1) {
     const size_t first = (size_t)row * cvec;
-    const float rstd = a.rstd[row];
-    u32x4 s[V], d[V];
+    const u32x4 *s = static_cast<const u32x4 *>(a.sum) + first, *d = static_cast<const u32x4 *>(a.dy) + first;
+    constexpr int kRow = kKeep ? V : 1;
+    BwdRow<kRow> x;
+    if constexpr (kStay) {
+      x = next;
+      if (row + gridDim.x < B) load_row<kHeld>(a, row + gridDim.x, cvec, next);
+    } else if constexpr (kKeep) {
+      load_row<kRow>(a, row, cvec, x);
+    } else {
+      x.rstd = a.rstd[row];
+    }
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint32_t v = threadIdx.x + i * T;
-      s[i] = d[i] = u32x4{0u, 0u, 0u, 0u};
-      if (v < cvec) {
-        s[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.sum) + first + v);
-        d[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.dy) + first + v);
-        float x[8], g[8], w[8];
-        widen8(s[i], x);
-        widen8(d[i], g);
-        load_weight(a.weight, v, w);
+      if (!kKeep && v >= cvec) continue;
+      float n[8], g[8], w[8];
+      widen8(kKeep ? x.s[kKeep ? i : 0] : s[v], n);
+      widen8(kKeep ? x.d[kKeep ? i : 0] : d[v], g);
+      weight_at(v, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = x[e] * rstd;
-          dw[i][e] = fmaf(g[e], n, dw[i][e]);
-          dot = fmaf(g[e] * w[e], n, dot);
-        }
+      for (int e = 0; e < 8; ++e) {
+        n[e] *= x.rstd;
+        dw[i][e] = fmaf(g[e], n[e], dw[i][e]);
+        dot = fmaf(g[e] * w[e], n[e], dot);
       }
     }
     const float mean = group_total(dot, part[turn]) * inv_c;
@@ -146,18 +196,17 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, float 
     for (int i = 0; i < V; ++i) {
       const uint32_t v = threadIdx.x + i * T;
       if (v >= cvec) continue;
-      float x[8], g[8], w[8], o[8];
-      widen8(s[i], x);
-      widen8(d[i], g);
-      load_weight(a.weight, v, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = rstd * (g[e] * w[e] - x[e] * rstd * mean);
-      if (a.dsum) {
-        float p[8];
-        widen8(__builtin_nontemporal_load(static_cast<const u32x4 *>(a.dsum) + first + v), p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += p[e];
+      float n[8], g[8], o[8], w[8];
+      widen8(kKeep ? x.s[kKeep ? i : 0] : s[v], n);
+      widen8(kKeep ? x.d[kKeep ? i : 0] : d[v], g);
+      weight_at(v, w);
+      if constexpr (kKeep) {
+        widen8(x.p[i], o);
+      } else {
+        widen8(a.dsum ? static_cast<const u32x4 *>(a.dsum)[first + v] : u32x4{0u, 0u, 0u, 0u}, o);
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += x.rstd * (g[e] * w[e] - n[e] * x.rstd * mean);
       store16_nt(static_cast<u32x4 *>(a.dx) + first + v, pack8(o));
     }
   }
@@ -172,62 +221,84 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, float 
   }
 }
 
-// dweight: the partial sums, a sixteenth of them a wave, then the waves'.
-constexpr int kJoinWaves = 16;
-__global__ __launch_bounds__(64 * kJoinWaves) void join_dweight_kernel(const f32x4 *partial, uint32_t parts,
-                                                                       uint32_t quads, f32x4 *dweight) {
-  __shared__ f32x4 sum[kJoinWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t q = blockIdx.x * 64 + lane;
+// dweight: 16 lanes take 64 columns, 64 teams of them a share of the partial
+// sums each, whose sums are then joined in the teams' order.
+constexpr int kJoinLanes = 16, kTeams = 64;
+__global__ __launch_bounds__(kJoinLanes *kTeams) void join_dweight_kernel(const f32x4 *__restrict__ partial,
+                                                                          uint32_t parts, uint32_t quads,
+                                                                          f32x4 *__restrict__ dweight) {
+  __shared__ f32x4 sum[kTeams][kJoinLanes];
+  const int lane = threadIdx.x % kJoinLanes, team = threadIdx.x / kJoinLanes;
+  const uint32_t q = blockIdx.x * kJoinLanes + lane;
   f32x4 t = {0.f, 0.f, 0.f, 0.f};
-  if (q < quads)
-    for (uint32_t p = wave; p < parts; p += kJoinWaves) t += partial[(size_t)p * quads + q];
-  sum[wave][lane] = t;
-  __syncthreads();
-  if (wave == 0 && q < quads) {
-#pragma unroll
-    for (int w = 1; w < kJoinWaves; ++w) t += sum[w][lane];
-    dweight[q] = t;
+  if (q < quads) {
+#pragma unroll 8
+    for (uint32_t p = team; p < parts; p += kTeams) t += partial[(size_t)p * quads + q];
   }
+  sum[team][lane] = t;
+#pragma unroll
+  for (int half = kTeams / 2; half > 0; half /= 2) {
+    __syncthreads();
+    if (team < half) {
+      t += sum[team + half][lane];
+      sum[team][lane] = t;
+    }
+  }
+  if (team == 0 && q < quads) dweight[q] = t;
 }
 
 struct Shape {
   uint32_t threads;
   int v;
 };
-Shape shape_of(int64_t C) {
-  const uint32_t cvec = (uint32_t)(C / 8);
-  const uint32_t threads = cvec > 2048 ? 1024 : cvec > 64 ? 256 : 64;
-  const uint32_t v = (cvec + threads - 1) / threads;
-  return Shape{threads, v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : 8};
+// Threads for rows of cvec vectors, `wide` of them at most: full waves, with 1,
+// 2, 4 or 8 vectors each.
+Shape shape_of(int64_t C, uint32_t wide) {
+  const uint32_t cvec = (uint32_t)(C / 8), v = (cvec + wide - 1) / wide;
+  Shape s{0, v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : 8};
+  s.threads = ((cvec + s.v - 1) / s.v + 63) / 64 * 64;
+  return s;
 }
 
 }  // namespace
 
 hipError_t launch_rmsnorm(int64_t B, int64_t C, const NormArgs &a, hipStream_t st) {
-  const Shape s = shape_of(C);
-  const uint32_t grid = (uint32_t)(B < (1 << 21) ? B : (1 << 21)), cvec = (uint32_t)(C / 8);
-  const uint32_t blocks = (uint32_t)ckpt_blocks(C);
+  // Many rows of up to 8192 channels: at most 256 threads a row (C=7168 in
+  // 8 bits, us: 147 against 163 with a thread a vector at 16384 rows, 24.8
+  // against 24.5 at 2048, 6.3 against 4.6 at 64).
+  const Shape s = shape_of(C, B >= 4096 && C <= 8192 ? 256 : 1024);
+  const uint32_t cvec = (uint32_t)(C / 8), blocks = (uint32_t)ckpt_blocks(C), rows = (uint32_t)B;
   const float inv_c = 1.0f / (float)C;
+  const uint32_t grid = (uint32_t)(B < (1 << 21) ? B : (1 << 21));
   switch (s.v) {
-    case 1: rmsnorm_kernel<1><<<grid, s.threads, 0, st>>>(a, (uint32_t)B, cvec, blocks, inv_c); break;
-    case 2: rmsnorm_kernel<2><<<grid, s.threads, 0, st>>>(a, (uint32_t)B, cvec, blocks, inv_c); break;
-    case 4: rmsnorm_kernel<4><<<grid, s.threads, 0, st>>>(a, (uint32_t)B, cvec, blocks, inv_c); break;
-    default: rmsnorm_kernel<8><<<grid, s.threads, 0, st>>>(a, (uint32_t)B, cvec, blocks, inv_c); break;
+    case 1: rmsnorm_kernel<1><<<grid, s.threads, 0, st>>>(a, rows, cvec, blocks, inv_c); break;
+    case 2: rmsnorm_kernel<2><<<grid, s.threads, 0, st>>>(a, rows, cvec, blocks, inv_c); break;
+    case 4: rmsnorm_kernel<4><<<grid, s.threads, 0, st>>>(a, rows, cvec, blocks, inv_c); break;
+    default: rmsnorm_kernel<8><<<grid, s.threads, 0, st>>>(a, rows, cvec, blocks, inv_c); break;
   }
   return hipGetLastError();
 }
 
 NormBwdPlan plan_rmsnorm_bwd(int64_t B, int64_t C) {
   NormBwdPlan p;
-  p.parts = B < 1024 ? B : 1024;
+  // Workgroups, each with its own partial sums of dweight: 512, or two waves a
+  // SIMD where rows are short, but not fewer than eight rows each (C=1000, us:
+  // 9.1 with 256 for 1001 rows, 12.9 with 1024; 34.5 with 1024 for 16384 rows,
+  // 37 with 512; C=7168: 164 with 512 for 16384 rows, 169 with 1024).
+  constexpr int64_t kPer = 8, kLeast = 256;
+  const int64_t waves = shape_of(C, 1024).threads / 64;
+  int64_t parts = 2048 / waves;
+  parts = parts < 512 ? 512 : parts;
+  parts = parts > B / kPer ? B / kPer : parts;
+  parts = parts < kLeast ? kLeast : parts;
+  p.parts = B < parts ? B : parts;
   p.total_bytes = (size_t)p.parts * C * 4;
   return p;
 }
 
 hipError_t launch_rmsnorm_bwd(const NormBwdPlan &p, int64_t B, int64_t C, const NormBwdArgs &a, void *ws,
                               hipStream_t st) {
-  const Shape s = shape_of(C);
+  const Shape s = shape_of(C, 1024);
   const uint32_t grid = (uint32_t)p.parts, cvec = (uint32_t)(C / 8);
   const float inv_c = 1.0f / (float)C;
   float *partial = a.dweight ? static_cast<float *>(ws) : nullptr;
@@ -240,8 +311,8 @@ hipError_t launch_rmsnorm_bwd(const NormBwdPlan &p, int64_t B, int64_t C, const 
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !partial) return e;
   const uint32_t quads = (uint32_t)(C / 4);
-  join_dweight_kernel<<<(quads + 63) / 64, 64 * kJoinWaves, 0, st>>>(reinterpret_cast<const f32x4 *>(partial), grid,
-                                                                     quads, reinterpret_cast<f32x4 *>(a.dweight));
+  join_dweight_kernel<<<(quads + kJoinLanes - 1) / kJoinLanes, kJoinLanes * kTeams, 0, st>>>(
+      reinterpret_cast<const f32x4 *>(partial), grid, quads, reinterpret_cast<f32x4 *>(a.dweight));
   return hipGetLastError();
 }
 
