@@ -95,7 +95,8 @@ def _near(got, want, tol, what):
 # -- norm -------------------------------------------------------------------------------------------
 
 NORM_SHAPES = [(1, 8), (1, 7168), (3, 24), (5, 40), (64, 512), (33, 520), (130, 1000), (7, 2048), (9, 2056), (2, 4104),
-               (17, 8192), (3, 8200), (2, 16384), (2, 32776), (1, 65536), (700, 72), (2100, 264)]
+               (17, 8192), (3, 8200), (2, 16384), (2, 32776), (1, 65536), (700, 72), (2100, 264),
+               (4100, 200), (4096, 1040), (4097, 2056)]
 
 
 def _rmsnorm(x, weight, shortcut, eps=1e-5, y=True, codes=True):
@@ -329,6 +330,48 @@ def test_route_near_ties(softmax):
     _check_route((close * -15).cuda(), k, softmax=softmax)
 
 
+def _some_rows(B):
+    """Rows to check of many: the first and the last ones, and some between."""
+    return np.unique(np.concatenate([np.arange(6), np.arange(B - 9, B), np.linspace(0, B - 1, 60).astype(int)]))
+
+
+@pytest.mark.parametrize("B,E,k,groups,top_groups", [
+    (2600, 16, 4, 1, 1), (2561, 30, 5, 3, 2), (2560, 64, 6, 8, 3), (2603, 128, 8, 1, 1), (2562, 100, 14, 4, 2),
+    (2600, 256, 8, 8, 4), (2563, 256, 12, 16, 5), (2565, 200, 10, 1, 1), (2560, 11, 3, 11, 7), (2600, 255, 9, 15, 14),
+    (2570, 300, 6, 1, 1), (2570, 64, 15, 1, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_route_many_rows(B, E, k, groups, top_groups, dtype):
+    """Rows enough for several to share a wave, masked ones among them, and rows whose choices are nearly equal."""
+    _say(f"route many B={B} E={E} k={k} groups={groups} top={top_groups} {dtype}")
+    gen = torch.Generator().manual_seed(B + E)
+    x = torch.randn(B, E, generator=gen) * 2
+    x[torch.rand(B, E, generator=gen) < 0.05] = -float("inf")
+    x[1], x[5, 1:], x[B - 2] = -float("inf"), -float("inf"), 0.25
+    x[3, ::3], x[4, ::2] = float("nan"), float("inf")
+    x[7] = torch.finfo(dtype).min
+    x[B - 9:B - 4] = x[B - 9] + torch.randint(-1, 2, (5, E), generator=gen) * 2.0 ** -22
+    x = x.to(dtype)
+    bias = _normal(gen, E, scale=0.1, dtype=torch.float32)
+    near = (0.5 - torch.sigmoid(x[B - 9].double())).float().nan_to_num(0.0).cuda()
+    rows = _some_rows(B)
+    x = x.cuda()
+    for softmax in (False, True):
+        for b in (None, bias, near):
+            how = dict(groups=groups, top_groups=top_groups, softmax=softmax, renorm=b is not near)
+            ids, weights = _route(x, k, b, **how)
+            want, want_w = experts.route(f64(x)[rows], k, None if b is None else f64(b), **how)
+            assert np.array_equal(ids.cpu().numpy()[rows], want)
+            z = experts.clean(f64(x)[rows])
+            with np.errstate(invalid="ignore"):
+                far = np.abs(np.take_along_axis(z, np.maximum(want, 0), 1) - np.max(z, axis=1, keepdims=True))
+            far = np.where((want >= 0) & np.isfinite(far), np.minimum(far, 1e6), 0.0)
+            _near(f64(weights)[rows], want_w, (32 + far) * U * np.abs(want_w), "weights")
+            # Every row as when it is on its own.
+            for r in (0, B // 2, B - 1):
+                one = _route(x[r:r + 1], k, b, **how)
+                assert torch.equal(one[0][0], ids[r])
+
+
 @pytest.mark.parametrize("B,E,k", [(1, 1, 1), (3, 2, 2), (130, 256, 8), (65, 100, 6), (7, 1024, 32), (5, 1000, 31),
                                    (300, 8, 2), (17, 65, 4), (9, 63, 1)])
 @pytest.mark.parametrize("dtype", [torch.float32, BF])
@@ -376,6 +419,31 @@ def _check_route_bwd(logits, ids, dw, softmax, renorm, scale=1.5):
     e = (48 + far) * U * size
     _near(out.t, want, half * (np.abs(want) + e) + e, "dlogits")
     return out.t
+
+
+@pytest.mark.parametrize("B,E,k", [(4096, 5, 2), (4099, 64, 6), (4097, 100, 6), (4100, 255, 16), (4096, 256, 8),
+                                   (4098, 33, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_route_bwd_many_rows(B, E, k, dtype):
+    _say(f"route_bwd many B={B} E={E} k={k} {dtype}")
+    gen = torch.Generator().manual_seed(E + k)
+    logits = _normal(gen, B, E, scale=2.0, dtype=dtype)
+    logits[B - 2, :E // 2] = -float("inf")
+    ids = torch.argsort(torch.rand(B, E, generator=gen), 1)[:, :k].to(torch.int32)
+    if k > 1:
+        ids[3, 1] = ids[3, 0]
+        ids[B - 1, k // 2:] = -1
+    rows = _some_rows(B)
+    ids, dw = ids.cuda(), _normal(gen, B, k, dtype=torch.float32)
+    for softmax in (False, True):
+        for renorm in (False, True):
+            out = Guarded(B, E, dtype=dtype)
+            mhc.mhc_route_bwd(B, E, k, logits, ids, dw, out.t, softmax=softmax, renorm=renorm, scale=1.5)
+            _checked(out)
+            few = _check_route_bwd(logits[rows], ids[rows], dw[rows], softmax, renorm)
+            # The same rows in a short call: within the roundings of two routes.
+            off = (out.t[rows].double() - few.double()).abs()
+            assert torch.all(off <= (2 * HALF_BF16 if dtype == BF else 96 * U) * few.double().abs().amax(1, True) + TINY)
 
 
 def test_route_bwd_one_weight():
@@ -521,6 +589,48 @@ def test_gather(B, k, C):
                 want_s[flat[ok]] = scales.repeat_interleave(k, 0)[ok]
                 assert torch.equal(more.t, want_s)
             assert torch.equal(rows.t, want)                 # the rows that no slot names are as they were
+
+
+@pytest.mark.parametrize("B,k,C", [(16384, 2, 32768), (2100, 8, 1040), (3000, 3, 24)])
+def test_gather_many_rows(B, k, C):
+    """More scales than the caches hold (they leave in a launch of their own), and rows of odd lengths."""
+    _say(f"gather many B={B} k={k} C={C}")
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    P, blocks = B * k, -(-C // 32)
+    slots = torch.randperm(P, generator=gen, device="cuda").reshape(B, k).to(torch.int32)
+    slots[5] = -1
+    codes = torch.randint(0, 256, (B, C), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.randint(0, 256, (B, blocks), generator=gen, device="cuda", dtype=torch.uint8)
+    rows, more = Guarded(P, C, dtype=torch.uint8), Guarded(P, blocks, dtype=torch.uint8)
+    mhc.mhc_experts_gather_ckpt(B, k, C, codes, scales, slots, rows.t, more.t)
+    _checked(rows, more)
+    for lo in range(0, B, 1024):
+        at = slots[lo:lo + 1024].reshape(-1).long()
+        ok = at >= 0
+        assert torch.equal(rows.t[at[ok]], codes[lo:lo + 1024].repeat_interleave(k, 0)[ok])
+        assert torch.equal(more.t[at[ok]], scales[lo:lo + 1024].repeat_interleave(k, 0)[ok])
+    left = ~_taken(slots, P)
+    assert int(left.sum()) == k and torch.all(rows.t[left] == 0x7F) and torch.all(more.t[left] == 0x7F)
+
+
+@pytest.mark.parametrize("B,k,C", [(2100, 1, 1032), (1500, 2, 520), (900, 3, 264), (4000, 2, 40)])
+def test_combine_bwd_many_rows(B, k, C):
+    """One and two slots a row of many rows, on both sides of the choice of kernels."""
+    _say(f"combine_bwd many B={B} k={k} C={C}")
+    gen = torch.Generator().manual_seed(B)
+    P, slots = B * k, _slots(gen, B, k)
+    Y, g, w = _normal(gen, P, C), _normal(gen, B, C, scale=1 / 64), _normal(gen, B, k, dtype=torch.float32)
+    taken = _taken(slots, P)
+    Y[~taken] = float("nan")
+    dY, dw = Guarded(P, C, dtype=BF, fill=0x3C), Guarded(B, k)
+    before = dY.t.clone()
+    mhc.mhc_experts_combine_bwd(B, k, C, Y, slots, w, g, dY.t, dw.t)
+    _checked(dY, dw)
+    want, want_w, A = experts.combine_bwd(f64(Y), slots.cpu().numpy(), f64(w), f64(g))
+    t = taken.cpu().numpy()
+    assert torch.equal(dY.t[~taken], before[~taken])
+    _near(f64(dY.t)[t], want[t], (HALF_BF16 + 2 * U) * np.abs(want[t]), "dY")
+    _near(dw.t, want_w, (C + 8) * U * A, "dweights")
 
 
 @pytest.mark.parametrize("B,k,C", MOVES)
