@@ -89,11 +89,13 @@ __device__ __forceinline__ T row_join(T x, F f) {
   x = f(x, dpp<kXor2>(x));
   x = f(x, dpp<kMirror8>(x));
   x = f(x, dpp<kMirror16>(x));
-  if constexpr (L == 64) {
+  if constexpr (L >= 32) {
     const Two<T> s = swap16(x);
     x = f(s.a, s.b);
-    const Two<T> t = swap32(x);
-    x = f(t.a, t.b);
+  }
+  if constexpr (L == 64) {
+    const Two<T> s = swap32(x);
+    x = f(s.a, s.b);
   }
   return x;
 }
@@ -273,7 +275,7 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
     const int start = (l & ((1 << g.lanes_log) - 1)) * V;  // of the lane's experts in the group
     // Lanes start at different ones of their experts, so that their reads fall
     // on different LDS banks.
-    const int turn = (L == 64 ? lane / (64 / V) : r + 4 * (l / (64 / V))) & (V - 1);
+    const int turn = (r + kRows * (l / (64 / V))) & (V - 1);
     const uint64_t row = first + r;
     const bool real = row < B;
     const int total = (int)(B - first < kRows ? B - first : kRows) * a.E;
@@ -617,33 +619,6 @@ hipError_t launch_route_t(int64_t B, const RouteArgs &a, const RouteShape &g, co
   return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_route(int64_t B, const RouteArgs &a, const void *logits, const float *bias, int32_t *ids,
-                        float *weights, hipStream_t st) {
-  RouteShape g;
-  const int v = experts_a_lane(16, a, &g);
-  const auto go = [&](auto kernel) { return kernel(B, a, g, logits, bias, ids, weights, st); };
-  if (v > 0 && v <= 16 && a.k <= 14 && B >= kManyRows) {
-    switch (v) {
-      case 1: return go(launch_route_t<1, 1, 16>);
-      case 2: return go(launch_route_t<2, 2, 16>);
-      case 4: return go(launch_route_t<4, 4, 16>);
-      case 8: return go(launch_route_t<8, 8, 16>);
-      default: return a.k <= 8 ? go(launch_route_t<16, 10, 16>) : go(launch_route_t<16, 16, 16>);
-    }
-  }
-  switch (experts_a_lane(64, a, &g)) {
-    case 1: return go(launch_route_t<1, 1, 64>);
-    case 2: return go(launch_route_t<2, 2, 64>);
-    case 4: return go(launch_route_t<4, 4, 64>);
-    case 8: return go(launch_route_t<8, 8, 64>);
-    case 16: return a.k <= 8 ? go(launch_route_t<16, 10, 64>) : go(launch_route_t<16, 16, 64>);
-    case 32: return a.k <= 8 ? go(launch_route_t<32, 10, 64>) : go(launch_route_t<32, 32, 64>);
-    default: return hipErrorInvalidValue;
-  }
-}
-
 // (The gradient, E=256 in fp32, us: 4.9 against 4.3 at 2048 rows, 5.2 against
 // 5.0 at 4096, 6.1 against 7.0 at 8192, 9.1 against 11.3 at 16384.)
 constexpr int64_t kManyRowsBwd = 4096;
@@ -659,10 +634,46 @@ hipError_t launch_route_bwd_t(int64_t B, const RouteArgs &a, const void *logits,
   return hipGetLastError();
 }
 
+}  // namespace
+
+hipError_t launch_route(int64_t B, const RouteArgs &a, const void *logits, const float *bias, int32_t *ids,
+                        float *weights, hipStream_t st) {
+  RouteShape g;
+  const auto go = [&](auto kernel) { return kernel(B, a, g, logits, bias, ids, weights, st); };
+  // (k + 2 lanes of a row hold what is chosen and the next)
+  const auto fits = [&](int L) {
+    const int v = B >= kManyRows && a.k <= L - 2 ? experts_a_lane(L, a, &g) : 0;
+    return v <= 16 ? v : 0;
+  };
+  if (const int v = fits(16)) {
+    switch (v) {
+      case 1: return go(launch_route_t<1, 1, 16>);
+      case 2: return go(launch_route_t<2, 2, 16>);
+      case 4: return go(launch_route_t<4, 4, 16>);
+      case 8: return go(launch_route_t<8, 8, 16>);
+      default: return a.k <= 8 ? go(launch_route_t<16, 10, 16>) : go(launch_route_t<16, 16, 16>);
+    }
+  }
+  // (E=512 in eight groups, us: 11.1 against 11.2 at 2560 rows, 32 against 43 at
+  // 16384; with k=12 and E=400 the longer lists cost what the fewer waves give:
+  // 44 against 44.)
+  if (a.k <= 8 && fits(32) == 16) return go(launch_route_t<16, 10, 32>);
+  switch (experts_a_lane(64, a, &g)) {
+    case 1: return go(launch_route_t<1, 1, 64>);
+    case 2: return go(launch_route_t<2, 2, 64>);
+    case 4: return go(launch_route_t<4, 4, 64>);
+    case 8: return go(launch_route_t<8, 8, 64>);
+    case 16: return a.k <= 8 ? go(launch_route_t<16, 10, 64>) : go(launch_route_t<16, 16, 64>);
+    case 32: return a.k <= 8 ? go(launch_route_t<32, 10, 64>) : go(launch_route_t<32, 32, 64>);
+    default: return hipErrorInvalidValue;
+  }
+}
+
 hipError_t launch_route_bwd(int64_t B, const RouteArgs &a, const void *logits, const int32_t *ids,
                             const float *dweights, void *dlogits, hipStream_t st) {
   const auto go = [&](auto kernel) { return kernel(B, a, logits, ids, dweights, dlogits, st); };
-  if (a.k <= 16 && a.E <= 256 && B >= kManyRowsBwd) {
+  if (a.k <= 16 && a.E <= 512 && B >= kManyRowsBwd) {
+    if (a.E > 256) return go(launch_route_bwd_t<16, 32>);  // (12.6 against 14.3 at E=512, B=16384)
     return a.E <= 64 ? go(launch_route_bwd_t<4, 16>) : a.E <= 128 ? go(launch_route_bwd_t<8, 16>)
                                                                   : go(launch_route_bwd_t<16, 16>);
   }

@@ -338,7 +338,7 @@ def _some_rows(B):
 @pytest.mark.parametrize("B,E,k,groups,top_groups", [
     (2600, 16, 4, 1, 1), (2561, 30, 5, 3, 2), (2560, 64, 6, 8, 3), (2603, 128, 8, 1, 1), (2562, 100, 14, 4, 2),
     (2600, 256, 8, 8, 4), (2563, 256, 12, 16, 5), (2565, 200, 10, 1, 1), (2560, 11, 3, 11, 7), (2600, 255, 9, 15, 14),
-    (2570, 300, 6, 1, 1), (2570, 64, 15, 1, 1)])
+    (2570, 300, 6, 1, 1), (2570, 64, 15, 1, 1), (2561, 512, 8, 8, 4), (2562, 270, 20, 30, 20), (2561, 513, 3, 1, 1)])
 @pytest.mark.parametrize("dtype", [torch.float32, BF])
 def test_route_many_rows(B, E, k, groups, top_groups, dtype):
     """Rows enough for several to share a wave, masked ones among them, and rows whose choices are nearly equal."""
@@ -422,7 +422,7 @@ def _check_route_bwd(logits, ids, dw, softmax, renorm, scale=1.5):
 
 
 @pytest.mark.parametrize("B,E,k", [(4096, 5, 2), (4099, 64, 6), (4097, 100, 6), (4100, 255, 16), (4096, 256, 8),
-                                   (4098, 33, 1)])
+                                   (4098, 33, 1), (4099, 301, 7)])
 @pytest.mark.parametrize("dtype", [torch.float32, BF])
 def test_route_bwd_many_rows(B, E, k, dtype):
     _say(f"route_bwd many B={B} E={E} k={k} {dtype}")
