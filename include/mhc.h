@@ -693,10 +693,12 @@ int mhc_embed_bwd(int64_t B, int32_t n, int64_t C, int64_t V, const int64_t *tok
  *
  * Rows are B >= 0 and channels C % 8 == 0 as above; k <= 32 experts are chosen
  * of E <= 1024, and B * k < 2^31.  Sums run in fp32 or wider and in a fixed
- * order (no atomics): equal inputs give equal bits.  Conventions, checks and
- * errors are those at the top of this file.  bf16, codes and the gain's
- * tensors are 16-byte aligned; indexes and other fp32 tensors 4-byte; scales
- * are bytes.
+ * order (no atomics): equal inputs give equal bits.  A workspace belongs to one
+ * call at a time: calls on different streams, and graphs that may run side by
+ * side, need one each.  Conventions, checks and errors are those at the top of
+ * this file.  bf16 tensors, codes, workspaces, weight and dweight are 16-byte
+ * aligned, bf16 logits 2-byte, indexes and other fp32 tensors 4-byte; scales are
+ * bytes.
  * ------------------------------------------------------------------------ */
 
 /* Root-mean-square norm of each row, with the shortcut's addition:
@@ -718,7 +720,8 @@ int mhc_embed_bwd(int64_t B, int32_t n, int64_t C, int64_t V, const int64_t *tok
  *   rstd      out fp32 [B], or NULL
  *
  * C <= 65536 (else MHC_ERR_UNSUPPORTED).  With eps = 0 a row of zeros is NaN.
- * Sums of squares are fp32: rows whose squares pass its range give rstd = 0. */
+ * Squares and their sum are fp32: a row whose squares pass its range has
+ * rstd = 0, and squares below it count as 0. */
 int mhc_rmsnorm(int64_t B, int64_t C, const void *x, const void *shortcut, const float *weight,
                 float eps, void *sum, void *y, void *codes, uint8_t *scales, float *rstd,
                 void *stream);
@@ -751,8 +754,8 @@ int mhc_rmsnorm_bwd(int64_t B, int64_t C, const void *sum, const float *weight, 
  * An expert whose logit or choice is minus infinity or NaN cannot be chosen;
  * plus infinity counts as the largest finite fp32 number.  The experts are
  * `groups` groups of E / groups neighbours.  A group ranks by its largest
- * choice, or, with a bias, by the sum of its two largest; the best top_groups
- * groups stay.  Of their experts the k largest choices are taken, in descending
+ * choice, or, with a bias, by the sum of its two largest (of one, where it has no
+ * second); the best top_groups groups stay.  Of their experts the k largest choices are taken, in descending
  * order.  Among equal ones, groups too, the lowest index comes first.  The order
  * is that of the logits where there is no bias, and that of choices in 64-bit
  * arithmetic where there is one.

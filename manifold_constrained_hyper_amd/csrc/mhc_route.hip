@@ -5,12 +5,15 @@
 //
 // Without a bias the order of the choices is that of the logits.  With one it
 // is that of 64-bit arithmetic: 42 bits of the choices are compared, and where
-// these cannot tell the order of two and it matters, the chosen ones and the
-// two behind them (or the groups' sums) are formed once more and compared whole.
+// these cannot tell the order of two and it matters, the chosen ones and the one
+// behind them (all of them where two behind are as near, and the groups' sums)
+// are formed once more and compared whole.
 //
 // Bound by vector instructions: 1514 a wave of four rows of 256 experts in
 // eight groups, of which the scores in 64 bits are a third, the sort and the k
-// maxima half; 18 us at B=16384 (17.8 MB).  One row takes 5.5.
+// maxima half; 18 us at B=16384 (17.8 MB), 24 with bf16 logits and no bias but
+// zeros (groups as good as each other in some rows), 29 where all logits are
+// equal.  One row takes 5.6.
 //
 // Renormalised weights are formed from exp(min(x, 0) - most) / (1 + exp(-|x|)),
 // the scores times a common factor under which the largest does not underflow.
@@ -135,7 +138,7 @@ __device__ __forceinline__ double choice_of(double key) {
   return __builtin_bit_cast(double, u32x2{w[0] & ~(uint32_t)kIndexMask, w[1]});
 }
 
-// exp of each x, |x| <= 700, from 2^n exp(r), |r| <= ln 2 / 2, by the power
+// exp of each x, |x| <= 1000, from 2^n exp(r), |r| <= ln 2 / 2, by the power
 // series up to r^TERMS: to 2^-50 of its value with 12 terms (the next one is
 // below 2^-52), to 2^-36 with 9.  N of them go step by step, as each is a chain
 // of dependent products.
@@ -168,35 +171,37 @@ __device__ __forceinline__ void exp_64(double (&x)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = __builtin_amdgcn_ldexp(p[i], e[i]);
 }
-// 1 / x for x >= 1: the hardware's estimate, to 2^-24, and Newton steps that
-// square its error.
-template <int STEPS, int N>
+// 1 / x for x >= 1 to 2^-47: the hardware's estimate, to 2^-24, and a Newton
+// step, which squares its error.
+template <int N>
 __device__ __forceinline__ void reciprocal_64(double (&x)[N]) {
-  double y[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) y[i] = __builtin_amdgcn_rcp(x[i]);
-#pragma unroll
-  for (int step = 0; step < STEPS; ++step)
-#pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = fma(y[i], fma(-x[i], y[i], 1.0), y[i]);
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = y[i];
+  for (int i = 0; i < N; ++i) {
+    const double y = __builtin_amdgcn_rcp(x[i]);
+    x[i] = fma(y, fma(-x[i], y, 1.0), y);
+  }
 }
-// WHOLE: to all 64 bits; else to 2^-35.
+// WHOLE: to all 64 bits, down to 0; else to 2^-35, and none below exp(-700).
 template <bool WHOLE, int N>
 __device__ __forceinline__ void sigmoid_64(const float (&x)[N], double (&s)[N]) {
+  constexpr float kFar = WHOLE ? 1000.0f : 700.0f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = -(double)__builtin_amdgcn_fmed3f(x[i], -700.0f, 700.0f);
+  for (int i = 0; i < N; ++i) s[i] = -(double)__builtin_amdgcn_fmed3f(x[i], -kFar, kFar);
   exp_64<WHOLE ? 12 : 9>(s);
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] += 1.0;
-  reciprocal_64<WHOLE ? 2 : 1>(s);
+  if constexpr (WHOLE) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = 1.0 / s[i];
+  } else {
+    reciprocal_64(s);
+  }
 }
 // exp(x - top) for x <= top, 0 for minus infinity.
 template <bool WHOLE, int N>
 __device__ __forceinline__ void exp_from(const float (&x)[N], float top, double (&e)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = __builtin_fmax((double)x[i] - (double)top, -700.0);
+  for (int i = 0; i < N; ++i) e[i] = __builtin_fmax((double)x[i] - (double)top, WHOLE ? -1000.0 : -700.0);
   exp_64<WHOLE ? 12 : 9>(e);
 #pragma unroll
   for (int i = 0; i < N; ++i) e[i] = x[i] > -__builtin_inff() ? e[i] : 0.0;
@@ -341,7 +346,7 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
     if (bias) {
       if (a.softmax) {
         double share[1] = {__builtin_fmax(all, 1.0)};  // (the largest term of the sum is 1)
-        reciprocal_64<1>(share);
+        reciprocal_64(share);
 #pragma unroll
         for (int t = 0; t < V; ++t) key[t] *= share[0];
       } else {
@@ -356,9 +361,9 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
 #pragma unroll
       for (int t = 0; t < V; ++t) key[t] = key_of((double)(x[t] + 0.0f), index_at(t));  // (a zero without a sign)
     }
-    // A candidate's choice once more, with all of its bits, and the reciprocal
-    // of the softmax's sum that it needs (a loop: few rows come here).
-    const auto share_64 = [&]() {
+    // An expert's choice once more, with all of its bits, and the softmax's sum
+    // that it needs (a loop: few rows come here).
+    const auto whole_sum = [&]() {
       if (!a.softmax) return 1.0;
       double sum = 0.0;
 #pragma unroll 1
@@ -368,42 +373,42 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
         exp_from<true>(z, top, c);
         sum += c[0];
       }
-      double share[1] = {__builtin_fmax(row_join<L>(sum, [](double p, double q) { return p + q; }), 1.0)};
-      reciprocal_64<2>(share);
-      return share[0];
+      return __builtin_fmax(row_join<L>(sum, [](double p, double q) { return p + q; }), 1.0);
     };
-    const auto whole = [&](double k, double share) {
-      const int e = index_of(k);
-      if (e < 0) return kNoKey;
-      const float z[1] = {x_row[e]};
+    const auto whole = [&](bool is, int e, double sum) {
+      const float z[1] = {is ? x_row[e] : none}, b = is ? bias_lds[e] : none;
       double c[1];
       if (!a.softmax) {
         sigmoid_64<true>(z, c);
       } else {
         exp_from<true>(z, top, c);
-        c[0] *= share;
+        c[0] /= sum;
       }
-      return c[0] + (double)bias_lds[e];
+      return z[0] > none && b > none ? c[0] + (double)b : kNoKey;
     };
     sort_keys<V>(key);
+    bool kept = true;
     if (g.groups > 1) {
       // The group's two largest, joined over its lanes.
-      double a0 = key[0], a1 = V > 1 ? key[V > 1 ? 1 : 0] : kNoKey;
-      const auto join = [&](double b0, double b1) {
-        a1 = __builtin_fmax(__builtin_fmin(a0, b0), __builtin_fmax(a1, b1));
-        a0 = __builtin_fmax(a0, b0);
-      };
-      if (g.lanes_log > 0) join(dpp<kXor1>(a0), dpp<kXor1>(a1));
-      if (g.lanes_log > 1) join(dpp<kXor2>(a0), dpp<kXor2>(a1));
-      if (g.lanes_log > 2) join(dpp<kMirror8>(a0), dpp<kMirror8>(a1));
-      if (g.lanes_log > 3) join(dpp<kMirror16>(a0), dpp<kMirror16>(a1));
-      if constexpr (L == 64) {
-        if (g.lanes_log > 4) {
-          const Two<double> p = swap16(a0), q = swap16(a1);
-          a0 = p.a, a1 = q.a;
-          join(p.b, q.b);
+      const auto join_lanes = [&](double &a0, double &a1) {
+        const auto join = [&](double b0, double b1) {
+          a1 = __builtin_fmax(__builtin_fmin(a0, b0), __builtin_fmax(a1, b1));
+          a0 = __builtin_fmax(a0, b0);
+        };
+        if (g.lanes_log > 0) join(dpp<kXor1>(a0), dpp<kXor1>(a1));
+        if (g.lanes_log > 1) join(dpp<kXor2>(a0), dpp<kXor2>(a1));
+        if (g.lanes_log > 2) join(dpp<kMirror8>(a0), dpp<kMirror8>(a1));
+        if (g.lanes_log > 3) join(dpp<kMirror16>(a0), dpp<kMirror16>(a1));
+        if constexpr (L == 64) {
+          if (g.lanes_log > 4) {
+            const Two<double> p = swap16(a0), q = swap16(a1);
+            a0 = p.a, a1 = q.a;
+            join(p.b, q.b);
+          }
         }
-      }
+      };
+      double a0 = key[0], a1 = V > 1 ? key[V > 1 ? 1 : 0] : kNoKey;
+      join_lanes(a0, a1);
       if (group >= g.groups) a0 = a1 = kNoKey;
       double rank = a0, size = 0.0;  // size: of the choices that a rank is the sum of
       if (bias && is_key(a0)) {
@@ -411,8 +416,7 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
         size = __builtin_fmax(__builtin_fabs(c0), __builtin_fabs(c1));
         rank = key_of(c0 + c1, group);
       }
-      const double own = rank;
-      bool kept = false;
+      kept = false;
       double last = kNoKey;
       for (int t = 0; t < a.top_groups; ++t) {
         last = row_max<L>(rank);
@@ -424,8 +428,16 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
       if (bias) {
         const double next = row_max<L>(rank);
         if (__ballot(is_key(next) && !(last - next > 4 * kNear * (1.0 + row_max<L>(size))))) {
-          const double share = share_64();
-          const double sum = !is_key(own) ? kNoKey : whole(a0, share) + (is_key(a1) ? whole(a1, share) : 0.0);
+          const double all_64 = whole_sum();
+          a0 = a1 = kNoKey;
+#pragma unroll 1
+          for (int t = 0; t < V; ++t) {
+            const double c = whole((t ^ turn) < mine, index_at(t), all_64);
+            a1 = __builtin_fmax(a1, __builtin_fmin(a0, c));
+            a0 = __builtin_fmax(a0, c);
+          }
+          join_lanes(a0, a1);
+          const double sum = a0 + (is_key(a1) ? a1 : 0.0);
           int better = 0;  // groups before the own one
           for (int q = 0; q < g.groups; ++q) {
             const double other = __shfl(sum, (lane & ~(L - 1)) + (q << g.lanes_log));
@@ -452,21 +464,69 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
     int id = index_of(chosen);
     if (bias) {
       // Keys next to each other that are too near, unless they come from the
-      // same numbers.  Behind a pair that is too near at the border there may
-      // be one more.
+      // same numbers.
       const double edge = best;
       const auto close = [](double p, double q) {
         const double c = choice_of(p);
         return is_key(q) && !(c - choice_of(q) > kNear * (1.0 + __builtin_fabs(c)));
       };
       take(a.k);
-      if (__ballot(close(edge, best))) take(a.k + 1);
+      bool many = false;  // that are too near at the border
+      if (__ballot(close(edge, best))) {
+        take(a.k + 1);
+        const bool crowd = close(edge, best);
+        if (__ballot(crowd)) {
+          // Equal numbers are in the order of their indexes already (zeros at
+          // the start of a training, logits in bf16); in 32 bits a score is off
+          // by less than 2^-20.
+          const int e0 = crowd ? index_of(edge) : 0;
+          const float z0 = x_row[e0], b0 = bias_lds[e0];
+          const auto choice = [&](float z, float b) {
+            return b + (a.softmax ? __builtin_amdgcn_exp2f((z - top) * kLog2e) * __builtin_amdgcn_rcpf((float)all)
+                                  : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-z * kLog2e)));
+          };
+          const float c0 = choice(z0, b0), far = 0x1p-18f * (1.0f + fabsf(c0));
+          bool other = false;
+#pragma unroll 4
+          for (int t = 0; t < V; ++t) {
+            const int e = index_at(t);
+            const float z = x_row[e], b = bias_lds[e];
+            other |= (t ^ turn) < mine && z > none && !(z == z0 && b == b0) && fabsf(choice(z, b) - c0) < far;
+          }
+          many = __ballot(crowd && kept && other);
+        }
+      }
       id = index_of(chosen);
       const float z = id >= 0 ? x_row[id] : none, b = id >= 0 ? bias_lds[id] : 0.f;
       const double next = __shfl_down(chosen, 1);
       const bool same = z == __shfl_down(z, 1) && b == __shfl_down(b, 1);
-      if (__ballot(l <= a.k && id >= 0 && close(chosen, next) && !same)) {
-        const double c = whole(chosen, share_64());
+      if (many) {
+        const double all_64 = whole_sum();
+#pragma unroll 1
+        for (int t = 0; t < V; ++t) {  // (key t comes in at the end and moves up to its place)
+          const double c = whole(kept && (t ^ turn) < mine, index_at(t), all_64);
+#pragma unroll
+          for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+          key[V - 1] = c;
+        }
+        for (int j = 0; j < a.k; ++j) {
+          double most = kNoKey;
+          int at = kMaxExperts;
+#pragma unroll
+          for (int t = 0; t < V; ++t) {
+            const int e = index_at(t);
+            const bool ahead = key[t] > most || (key[t] == most && e < at);
+            most = ahead ? key[t] : most;
+            at = ahead ? e : at;
+          }
+          const double first_of = row_max<L>(most);
+          at = -(int)row_max<L>(most == first_of ? -(float)at : none);
+#pragma unroll
+          for (int t = 0; t < V; ++t) key[t] = index_at(t) == at ? kNoKey : key[t];
+          if (l == j) id = is_key(first_of) ? at : -1;
+        }
+      } else if (__ballot(l <= a.k && id >= 0 && close(chosen, next) && !same)) {
+        const double c = whole(id >= 0, id, whole_sum());
         int better = 0;
         for (int q = 0; q < a.k + 2; ++q) {
           const double other = __shfl(c, (lane & ~(L - 1)) + q);

@@ -330,6 +330,40 @@ def test_route_near_ties(softmax):
     _check_route((close * -15).cuda(), k, softmax=softmax)
 
 
+def _crowded(B, E, gen):
+    """Rows whose experts are all within 2^-33 of each other in the choice, or where 64-bit scores end: sigmoids next
+    to 1, logits next to 0, scores that fall out of the type, scores of very different sizes."""
+    at = torch.stack([torch.randperm(E, generator=gen) for _ in range(B)]).double()
+    off = torch.rand(B, E, generator=gen).double()   # (sums of two are not equal by chance)
+    kind = torch.arange(B).reshape(-1, 1) % 5
+    return torch.where(kind == 0, 25 + at * 0.05,
+                       torch.where(kind == 1, (at + 0.3 * off) * 1e-11,
+                                   torch.where(kind == 2, -660 - at,
+                                               torch.where(kind == 3, -0.5 * at, 30 + 0.0 * at)))).float()
+
+
+@pytest.mark.parametrize("B,E,k,groups,top_groups", [
+    (40, 96, 12, 1, 1), (40, 96, 12, 8, 4), (35, 13, 3, 1, 1), (25, 96, 5, 48, 11), (20, 100, 32, 10, 7),
+    (2565, 96, 12, 1, 1), (2563, 96, 8, 8, 4), (2561, 16, 4, 4, 2), (2570, 420, 8, 1, 1), (2560, 112, 7, 1, 1)])
+def test_route_crowded(B, E, k, groups, top_groups):
+    """More choices than k + 2 that 42 bits cannot tell apart: the order is still that of 64-bit arithmetic."""
+    _say(f"route crowded B={B} E={E} k={k} groups={groups} top={top_groups}")
+    gen = torch.Generator().manual_seed(B + E + k)
+    x = _crowded(B, E, gen)
+    if B > 40:
+        x[2:9] = _normal(gen, 7, E, dtype=torch.float32).cpu()      # ordinary rows in the same wave
+    rows = np.arange(B) if B <= 40 else _some_rows(B)
+    for softmax in (False, True):
+        for b in (torch.zeros(E), torch.full((E,), 0.25)):
+            if groups == 1:
+                b[E // 2] = -float("inf")
+            how = dict(groups=groups, top_groups=top_groups, softmax=softmax)
+            ids, _ = _route(x.cuda(), k, b.cuda(), **how)
+            want, _ = experts.route(f64(x)[rows], k, f64(b), **how)
+            got = ids.cpu().numpy()[rows]
+            assert np.array_equal(got, want), np.argwhere(got != want)[:5]
+
+
 def _some_rows(B):
     """Rows to check of many: the first and the last ones, and some between."""
     return np.unique(np.concatenate([np.arange(6), np.arange(B - 9, B), np.linspace(0, B - 1, 60).astype(int)]))
