@@ -9,11 +9,11 @@
 // behind them (all of them where two behind are as near, and the groups' sums)
 // are formed once more and compared whole.
 //
-// Bound by vector instructions: 1514 a wave of four rows of 256 experts in
-// eight groups, of which the scores in 64 bits are a third, the sort and the k
-// maxima half; 18 us at B=16384 (17.8 MB), 24 with bf16 logits and no bias but
+// Bound by vector instructions: 1421 a wave of four rows of 256 experts in
+// eight groups, of which the scores in 64 bits are a third, keys, sort and the k
+// maxima half; 15 us at B=16384 (17.8 MB), 23 with bf16 logits and no bias but
 // zeros (groups as good as each other in some rows), 29 where all logits are
-// equal.  One row takes 5.6.
+// equal.  One row takes 5.7.
 //
 // Renormalised weights are formed from exp(min(x, 0) - most) / (1 + exp(-|x|)),
 // the scores times a common factor under which the largest does not underflow.
@@ -142,11 +142,11 @@ __device__ __forceinline__ double choice_of(double key) {
 // series up to r^TERMS: to 2^-50 of its value with 12 terms (the next one is
 // below 2^-52), to 2^-36 with 9.  N of them go step by step, as each is a chain
 // of dependent products.
+__constant__ const double kInverse[] = {1.0,           1.0,            0.5,        1.0 / 6,     1.0 / 24,
+                                        1.0 / 120,     1.0 / 720,      1.0 / 5040, 1.0 / 40320, 1.0 / 362880,
+                                        1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
 template <int TERMS, int N>
 __device__ __forceinline__ void exp_64(double (&x)[N]) {
-  constexpr double kInverse[] = {1.0,         1.0,          0.5,           1.0 / 6,        1.0 / 24,
-                                 1.0 / 120,   1.0 / 720,    1.0 / 5040,    1.0 / 40320,    1.0 / 362880,
-                                 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
   constexpr double kShift = 0x1.8p52;  // a number added to it is rounded to an integer in the low bits
   double n[N], p[N];
 #pragma unroll
@@ -164,7 +164,8 @@ __device__ __forceinline__ void exp_64(double (&x)[N]) {
   for (int i = 0; i < N; ++i) x[i] = fma(n[i], -1.9082149292705877e-10, x[i]);
 #pragma unroll
   for (int i = 0; i < N; ++i) p[i] = kInverse[TERMS];
-#pragma unroll
+  constexpr int kStep = TERMS > 9 ? 1 : TERMS;  // (few rows come to the long series: its constants stay in memory)
+#pragma unroll kStep
   for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = fma(p[i], x[i], kInverse[t]);
@@ -250,7 +251,40 @@ __device__ __forceinline__ float weight_of(const RouteArgs &a, float x, float to
 struct RouteShape {
   int groups, size;  // groups that are chosen among (1: all experts), experts of one
   int lanes_log;     // lanes of a group: 1 << lanes_log
+  uint32_t inverse;  // 2^20 / size, rounded up: (i * inverse) >> 20 is i / size for i < 1024; 0 where group q's
+                     // lanes follow on those of q - 1 without a gap, and the groups need not be told apart
 };
+
+// A lane's V values in LDS are neighbours, and lanes are apart by as much as
+// lets sixteen of them read 16 bytes each without sharing a bank.
+template <int V>
+struct Slots {
+  static constexpr int kPad = V > 4 ? 4 : 0, kApart = V + kPad;
+};
+
+// The sorted keys of a lane: two in registers and, where there are 8 to 10, the
+// others in LDS (a list that is moved up in registers takes two instructions a
+// key and choice: 17.2 us, not 15.3, at B=16384, E=256), else all in registers.  A list
+// that can be used up ends with no key; one of k + 2 keys cannot.
+template <int V, int KL>
+struct List {
+  static constexpr bool kInLds = KL >= 8 && KL <= 10;
+  static constexpr int kRows = !kInLds ? 0 : KL == V ? KL - 1 : KL - 2;  // of 64 lanes
+};
+template <int V>
+__device__ __forceinline__ void read_slots(const float *from, float (&x)[V]) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int t = 0; t < V; t += 4) {
+      const f32x4 w = *reinterpret_cast<const f32x4 *>(from + t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[t + i] = w[i];
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < V; ++t) x[t] = from[t];
+  }
+}
 
 // L lanes take a row, V experts each: those of a group are neighbours, a
 // group's lanes are too.  Each lane sorts its keys; then the largest of the
@@ -260,61 +294,68 @@ template <int V, int KL, int L>
 __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
     RouteArgs a, RouteShape g, const void *__restrict__ logits, const float *__restrict__ bias,
     int32_t *__restrict__ ids, float *__restrict__ weights, uint32_t B) {
-  // Each wave's rows of logits, the bias, and room behind both for what lanes
-  // read past their experts (and pass over).
-  extern __shared__ float shared[];
-  constexpr int kRows = 64 / L;
+  // Each wave's rows of logits and the bias, where the lanes find them.  A
+  // lane's places without an expert hold minus infinity.
+  extern __shared__ __attribute__((aligned(16))) float shared[];
+  constexpr bool kInLds = List<V, KL>::kInLds;
+  constexpr int kRows = 64 / L, kPad = Slots<V>::kPad, kApart = Slots<V>::kApart, kRowSize = L * kApart;
   const int wave = uniform((int)threadIdx.x >> 6);
-  float *x_lds = shared + wave * kRows * a.E, *bias_lds = shared + kWaves * kRows * a.E + L * V;
+  constexpr int kList = List<V, KL>::kRows * 64;  // (a read past a wave's list is one of what follows, and not used)
+  double *list = reinterpret_cast<double *>(shared) + wave * kList;
+  float *rows_lds = shared + 2 * kWaves * kList, *x_lds = rows_lds + wave * kRows * kRowSize;
+  float *bias_lds = rows_lds + kWaves * kRows * kRowSize;
+  const auto place = [&](uint32_t i) {  // of a row's expert i
+    const uint32_t q = __umul24(i, g.inverse) >> 20, e = i - __umul24(q, (uint32_t)g.size);
+    return e + kPad * (e / V) + q * (uint32_t)(kApart << g.lanes_log);
+  };
+  const float none = -__builtin_inff();
   if (bias) {
-    for (int i = threadIdx.x; i < a.E; i += 64 * kWaves) bias_lds[i] = clean(bias[i]);
+    for (int i = threadIdx.x; i < a.E; i += 64 * kWaves) bias_lds[place(i)] = clean(bias[i]);
     __syncthreads();
   }
-  const float none = -__builtin_inff();
+  const bool full = a.E == L * V && g.inverse == 0;
+  if (!full) {
+#pragma unroll
+    for (int t = 0; t < V; ++t) x_lds[(threadIdx.x & 63) * kApart + t] = none;
+    wave_lds_fence();
+  }
   const bool sums = a.softmax && (bias || !a.renorm);
   for (uint64_t first = ((uint64_t)blockIdx.x * kWaves + wave) * kRows; first < B;
        first += (uint64_t)gridDim.x * kWaves * kRows) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));  // or the compiler keeps 64 registers of indexes and addresses over the rows
     const int l = lane & (L - 1), r = lane / L, group = l >> g.lanes_log;
-    const int start = (l & ((1 << g.lanes_log) - 1)) * V;  // of the lane's experts in the group
-    // Lanes start at different ones of their experts, so that their reads fall
-    // on different LDS banks.
-    const int turn = (r + kRows * (l / (64 / V))) & (V - 1);
+    const int base = group * g.size + (l & ((1 << g.lanes_log) - 1)) * V;  // the lane's first expert
     const uint64_t row = first + r;
     const bool real = row < B;
-    const int total = (int)(B - first < kRows ? B - first : kRows) * a.E;
-    const float *x_row = x_lds + r * a.E;
+    float *x_row = x_lds + r * kRowSize;
+    const float *x_own = x_lds + lane * kApart, *bias_own = bias_lds + l * kApart;
     float x[V];
-    if (total == 64 * V && !a.bf16) {
+    if (L * V >= 64 && full && !a.bf16 && B - first >= kRows) {
       const float *from = static_cast<const float *>(logits) + first * a.E;
+      float *to = x_lds + lane + kPad * (lane / V);
 #pragma unroll
       for (int t = 0; t < V; ++t) x[t] = from[lane + 64 * t];
 #pragma unroll
-      for (int t = 0; t < V; ++t) x_lds[lane + 64 * t] = clean(x[t]);
+      for (int t = 0; t < V; ++t) to[64 / V * t * kApart] = clean(x[t]);
     } else {
+      // (Lanes behind the last expert take it too, and write it where it is.)
+      const size_t begin = (real ? row : first) * a.E;
+      const auto at = [&](int t) { return min(l + L * t, a.E - 1); };
       if (a.bf16) {
-        const uint16_t *from = static_cast<const uint16_t *>(logits) + first * a.E;
+        const uint16_t *from = static_cast<const uint16_t *>(logits) + begin;
 #pragma unroll
-        for (int t = 0; t < V; ++t) x[t] = lane + 64 * t < total ? bf16_lo(from[lane + 64 * t]) : 0.f;
+        for (int t = 0; t < V; ++t) x[t] = bf16_lo(from[at(t)]);
       } else {
-        const float *from = static_cast<const float *>(logits) + first * a.E;
+        const float *from = static_cast<const float *>(logits) + begin;
 #pragma unroll
-        for (int t = 0; t < V; ++t) x[t] = lane + 64 * t < total ? from[lane + 64 * t] : 0.f;
+        for (int t = 0; t < V; ++t) x[t] = from[at(t)];
       }
 #pragma unroll
-      for (int t = 0; t < V; ++t)
-        if (lane + 64 * t < total) x_lds[lane + 64 * t] = clean(x[t]);
+      for (int t = 0; t < V; ++t) x_row[place(at(t))] = real ? clean(x[t]) : none;
     }
     wave_lds_fence();
-    const int mine = real && group < g.groups ? g.size - start : 0;  // experts of the lane, V or more: all
-    const int base = (group < g.groups ? group : 0) * g.size + start;
-    const auto index_at = [&](int t) { return base + (t ^ turn); };
-#pragma unroll
-    for (int t = 0; t < V; ++t) {
-      const float z = x_row[index_at(t)];
-      x[t] = (t ^ turn) < mine ? z : none;
-    }
+    read_slots<V>(x_own, x);
     float top = none;
     double all = 0.0, key[V];
     constexpr int kN = V < kAtOnce ? V : kAtOnce;
@@ -352,14 +393,13 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
       } else {
         by_parts([&](const float(&z)[kN], double(&k)[kN]) { sigmoid_64<false>(z, k); });
       }
+      float b[V];
+      read_slots<V>(bias_own, b);
 #pragma unroll
-      for (int t = 0; t < V; ++t) {
-        const float b = bias_lds[index_at(t)];
-        key[t] = key_of(key[t] + (double)(x[t] > none ? b : none), index_at(t));
-      }
+      for (int t = 0; t < V; ++t) key[t] = key_of(key[t] + (double)(x[t] > none ? b[t] : none), base + t);
     } else {
 #pragma unroll
-      for (int t = 0; t < V; ++t) key[t] = key_of((double)(x[t] + 0.0f), index_at(t));  // (a zero without a sign)
+      for (int t = 0; t < V; ++t) key[t] = key_of((double)(x[t] + 0.0f), base + t);  // (a zero without a sign)
     }
     // An expert's choice once more, with all of its bits, and the softmax's sum
     // that it needs (a loop: few rows come here).
@@ -368,15 +408,15 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
       double sum = 0.0;
 #pragma unroll 1
       for (int t = 0; t < V; ++t) {
-        const float z[1] = {(t ^ turn) < mine ? x_row[index_at(t)] : none};
+        const float z[1] = {x_own[t]};
         double c[1];
         exp_from<true>(z, top, c);
         sum += c[0];
       }
       return __builtin_fmax(row_join<L>(sum, [](double p, double q) { return p + q; }), 1.0);
     };
-    const auto whole = [&](bool is, int e, double sum) {
-      const float z[1] = {is ? x_row[e] : none}, b = is ? bias_lds[e] : none;
+    const auto whole = [&](float x, float b, double sum) {
+      const float z[1] = {x};
       double c[1];
       if (!a.softmax) {
         sigmoid_64<true>(z, c);
@@ -384,7 +424,7 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
         exp_from<true>(z, top, c);
         c[0] /= sum;
       }
-      return z[0] > none && b > none ? c[0] + (double)b : kNoKey;
+      return x > none && b > none ? c[0] + (double)b : kNoKey;
     };
     sort_keys<V>(key);
     bool kept = true;
@@ -432,7 +472,7 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
           a0 = a1 = kNoKey;
 #pragma unroll 1
           for (int t = 0; t < V; ++t) {
-            const double c = whole((t ^ turn) < mine, index_at(t), all_64);
+            const double c = whole(x_own[t], bias_own[t], all_64);
             a1 = __builtin_fmax(a1, __builtin_fmin(a0, c));
             a0 = __builtin_fmax(a0, c);
           }
@@ -448,16 +488,30 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
       }
       if (!kept) {
 #pragma unroll
-        for (int t = 0; t < KL; ++t) key[t] = kNoKey;
+        for (int t = 0; t < (kInLds ? 1 : KL); ++t) key[t] = kNoKey;
       }
+    }
+    const double *next_key = list + lane;
+    if constexpr (kInLds) {
+#pragma unroll
+      for (int t = 2; t < KL; ++t) list[64 * (t - 2) + lane] = key[t];
+      if constexpr (KL == V) list[64 * (KL - 2) + lane] = kNoKey;
     }
     double chosen = kNoKey, best = kNoKey;  // of lane j: the j-th key
     const auto take = [&](int j) {
       best = row_max<L>(key[0]);
-      const bool win = key[0] == best;
+      const bool win = key[0] == best && is_key(best);
+      if constexpr (kInLds) {
+        if (win) {
+          key[0] = key[1];
+          key[1] = *next_key;
+          next_key += 64;
+        }
+      } else {
 #pragma unroll
-      for (int t = 0; t + 1 < KL; ++t) key[t] = win ? key[t + 1] : key[t];
-      if (win) key[KL - 1] = kNoKey;
+        for (int t = 0; t + 1 < KL; ++t) key[t] = win ? key[t + 1] : key[t];
+        if (win) key[KL - 1] = kNoKey;
+      }
       if (l == j) chosen = best;
     };
     for (int j = 0; j < a.k; ++j) take(j);
@@ -479,7 +533,7 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
           // Equal numbers are in the order of their indexes already (zeros at
           // the start of a training, logits in bf16); in 32 bits a score is off
           // by less than 2^-20.
-          const int e0 = crowd ? index_of(edge) : 0;
+          const uint32_t e0 = crowd ? place(index_of(edge)) : 0;
           const float z0 = x_row[e0], b0 = bias_lds[e0];
           const auto choice = [&](float z, float b) {
             return b + (a.softmax ? __builtin_amdgcn_exp2f((z - top) * kLog2e) * __builtin_amdgcn_rcpf((float)all)
@@ -489,22 +543,22 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
           bool other = false;
 #pragma unroll 4
           for (int t = 0; t < V; ++t) {
-            const int e = index_at(t);
-            const float z = x_row[e], b = bias_lds[e];
-            other |= (t ^ turn) < mine && z > none && !(z == z0 && b == b0) && fabsf(choice(z, b) - c0) < far;
+            const float z = x_own[t], b = bias_own[t];
+            other |= z > none && !(z == z0 && b == b0) && fabsf(choice(z, b) - c0) < far;
           }
           many = __ballot(crowd && kept && other);
         }
       }
       id = index_of(chosen);
-      const float z = id >= 0 ? x_row[id] : none, b = id >= 0 ? bias_lds[id] : 0.f;
+      const uint32_t at_id = id >= 0 ? place(id) : 0;
+      const float z = id >= 0 ? x_row[at_id] : none, b = id >= 0 ? bias_lds[at_id] : 0.f;
       const double next = __shfl_down(chosen, 1);
       const bool same = z == __shfl_down(z, 1) && b == __shfl_down(b, 1);
       if (many) {
         const double all_64 = whole_sum();
 #pragma unroll 1
         for (int t = 0; t < V; ++t) {  // (key t comes in at the end and moves up to its place)
-          const double c = whole(kept && (t ^ turn) < mine, index_at(t), all_64);
+          const double c = whole(kept ? x_own[t] : none, bias_own[t], all_64);
 #pragma unroll
           for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
           key[V - 1] = c;
@@ -514,19 +568,18 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
           int at = kMaxExperts;
 #pragma unroll
           for (int t = 0; t < V; ++t) {
-            const int e = index_at(t);
-            const bool ahead = key[t] > most || (key[t] == most && e < at);
+            const bool ahead = key[t] > most;
             most = ahead ? key[t] : most;
-            at = ahead ? e : at;
+            at = ahead ? base + t : at;
           }
           const double first_of = row_max<L>(most);
           at = -(int)row_max<L>(most == first_of ? -(float)at : none);
 #pragma unroll
-          for (int t = 0; t < V; ++t) key[t] = index_at(t) == at ? kNoKey : key[t];
+          for (int t = 0; t < V; ++t) key[t] = base + t == at ? kNoKey : key[t];
           if (l == j) id = is_key(first_of) ? at : -1;
         }
       } else if (__ballot(l <= a.k && id >= 0 && close(chosen, next) && !same)) {
-        const double c = whole(id >= 0, id, whole_sum());
+        const double c = whole(z, b, whole_sum());
         int better = 0;
         for (int q = 0; q < a.k + 2; ++q) {
           const double other = __shfl(c, (lane & ~(L - 1)) + q);
@@ -537,7 +590,7 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
         id = __builtin_amdgcn_ds_permute(4 * to, id);
       }
     }
-    const float w = weight_of<L>(a, l < a.k && id >= 0 ? x_row[id] : none, top, (float)all);
+    const float w = weight_of<L>(a, l < a.k && id >= 0 ? x_row[place(id)] : none, top, (float)all);
     if (real && l < a.k) {
       ids[row * a.k + l] = id;
       weights[row * a.k + l] = w * a.scale;
@@ -661,26 +714,32 @@ int experts_a_lane(int L, const RouteArgs &a, RouteShape *g) {
   const int each = (g->size + (1 << g->lanes_log) - 1) >> g->lanes_log;
   int v = 1;
   while (v < each) v *= 2;
+  const bool close = g->groups == 1 || g->size == v << g->lanes_log;
+  g->inverse = close ? 0 : ((1u << 20) + g->size - 1) / g->size;
   return v;
 }
 
-// Rows from which sixteen lanes take one, where it fits them: with fewer rows
-// the shorter chains of a wave a row count (E=256 in eight groups, k=8, us:
-// 8.3 against 7.6 at 2048 rows, 8.7 against 10.9 at 4096, 18.2 against 31 at 16384).
-constexpr int64_t kManyRows = 2560;
+// Waves that have a SIMD each.  Two rows share a wave where there are more of
+// them than that, and four where there are more than twice as many: a wave's
+// chain of dependent steps is what few rows take (E=256 in eight groups, k=8,
+// softmax, us with 1, 2 and 4 rows a wave: 6.7, 7.0, 8.1 at 1024 rows; 7.8, 7.1,
+// 8.1 at 2048; -, 8.6, 8.1 at 2560).
+constexpr int64_t kSimds = 1024;
 
 template <int V, int KL, int L>
 hipError_t launch_route_t(int64_t B, const RouteArgs &a, const RouteShape &g, const void *logits, const float *bias,
                           int32_t *ids, float *weights, hipStream_t st) {
   constexpr int kRows = 64 / L;
-  const size_t lds = ((size_t)(kWaves * kRows + (bias ? 1 : 0)) * a.E + (bias ? 2 : 1) * L * V) * sizeof(float);
+  const size_t lds = (size_t)(kWaves * kRows + (bias ? 1 : 0)) * L * Slots<V>::kApart * sizeof(float) +
+                     (size_t)kWaves * List<V, KL>::kRows * 64 * sizeof(double);
   route_kernel<V, KL, L><<<grid_of(kWaves * kRows, B), 64 * kWaves, lds, st>>>(a, g, logits, bias, ids, weights,
                                                                               (uint32_t)B);
   return hipGetLastError();
 }
 
-// (The gradient, E=256 in fp32, us: 4.9 against 4.3 at 2048 rows, 5.2 against
-// 5.0 at 4096, 6.1 against 7.0 at 8192, 9.1 against 11.3 at 16384.)
+// Rows from which several share a wave of the gradient (E=256 in fp32, us with
+// four a wave and one: 4.9 against 4.3 at 2048 rows, 5.2 against 5.0 at 4096,
+// 6.1 against 7.0 at 8192, 9.1 against 11.3 at 16384).
 constexpr int64_t kManyRowsBwd = 4096;
 
 template <int V, int L>
@@ -700,24 +759,27 @@ hipError_t launch_route(int64_t B, const RouteArgs &a, const void *logits, const
                         float *weights, hipStream_t st) {
   RouteShape g;
   const auto go = [&](auto kernel) { return kernel(B, a, g, logits, bias, ids, weights, st); };
-  // (k + 2 lanes of a row hold what is chosen and the next)
+  // k + 2 lanes of a row hold what is chosen and the next.  With k above 8 the
+  // lists of 16 a lane cost more than the fewer waves give (E=200, k=16, 16384
+  // rows: 36 us with sixteen lanes a row, 25 with 32).
   const auto fits = [&](int L) {
-    const int v = B >= kManyRows && a.k <= L - 2 ? experts_a_lane(L, a, &g) : 0;
-    return v <= 16 ? v : 0;
+    const int v = B * L > 32 * kSimds && a.k <= L - 2 ? experts_a_lane(L, a, &g) : 0;
+    return v <= (a.k <= 8 ? 16 : 8) ? v : 0;
   };
-  if (const int v = fits(16)) {
-    switch (v) {
-      case 1: return go(launch_route_t<1, 1, 16>);
-      case 2: return go(launch_route_t<2, 2, 16>);
-      case 4: return go(launch_route_t<4, 4, 16>);
-      case 8: return go(launch_route_t<8, 8, 16>);
-      default: return a.k <= 8 ? go(launch_route_t<16, 10, 16>) : go(launch_route_t<16, 16, 16>);
-    }
+  switch (fits(16)) {
+    case 1: return go(launch_route_t<1, 1, 16>);
+    case 2: return go(launch_route_t<2, 2, 16>);
+    case 4: return go(launch_route_t<4, 4, 16>);
+    case 8: return go(launch_route_t<8, 8, 16>);
+    case 16: return go(launch_route_t<16, 10, 16>);
   }
-  // (E=512 in eight groups, us: 11.1 against 11.2 at 2560 rows, 32 against 43 at
-  // 16384; with k=12 and E=400 the longer lists cost what the fewer waves give:
-  // 44 against 44.)
-  if (a.k <= 8 && fits(32) == 16) return go(launch_route_t<16, 10, 32>);
+  switch (fits(32)) {
+    case 1: return go(launch_route_t<1, 1, 32>);
+    case 2: return go(launch_route_t<2, 2, 32>);
+    case 4: return go(launch_route_t<4, 4, 32>);
+    case 8: return go(launch_route_t<8, 8, 32>);
+    case 16: return go(launch_route_t<16, 10, 32>);
+  }
   switch (experts_a_lane(64, a, &g)) {
     case 1: return go(launch_route_t<1, 1, 64>);
     case 2: return go(launch_route_t<2, 2, 64>);

@@ -372,7 +372,9 @@ def _some_rows(B):
 @pytest.mark.parametrize("B,E,k,groups,top_groups", [
     (2600, 16, 4, 1, 1), (2561, 30, 5, 3, 2), (2560, 64, 6, 8, 3), (2603, 128, 8, 1, 1), (2562, 100, 14, 4, 2),
     (2600, 256, 8, 8, 4), (2563, 256, 12, 16, 5), (2565, 200, 10, 1, 1), (2560, 11, 3, 11, 7), (2600, 255, 9, 15, 14),
-    (2570, 300, 6, 1, 1), (2570, 64, 15, 1, 1), (2561, 512, 8, 8, 4), (2562, 270, 20, 30, 20), (2561, 513, 3, 1, 1)])
+    (2570, 300, 6, 1, 1), (2570, 64, 15, 1, 1), (2561, 512, 8, 8, 4), (2562, 270, 20, 30, 20), (2561, 513, 3, 1, 1),
+    (2561, 30, 18, 1, 1), (2563, 32, 4, 32, 6), (2560, 60, 16, 1, 1), (2565, 96, 17, 24, 19), (2562, 128, 15, 1, 1),
+    (2561, 200, 12, 25, 9), (2563, 256, 30, 32, 9), (1025, 512, 8, 8, 4), (2048, 100, 6, 1, 1), (2049, 256, 8, 8, 4)])
 @pytest.mark.parametrize("dtype", [torch.float32, BF])
 def test_route_many_rows(B, E, k, groups, top_groups, dtype):
     """Rows enough for several to share a wave, masked ones among them, and rows whose choices are nearly equal."""
