@@ -10,7 +10,7 @@
 //
 // Bound by HBM: 144 us for B=16384, C=7168 with the shortcut in 8 bits (826 MB,
 // 5.7 TB/s), 163 for its gradients with the shortcut's (940 MB, 5.8 TB/s, of
-// which 5 us join dweight).  One row takes 3.6, a launch.
+// which 5 us join dweight).  One row takes 3.6, and its gradients 4.4.
 #include "mhc_experts.h"
 #include "mhc_finish.h"
 #include "mhc_held.h"
@@ -122,12 +122,13 @@ struct BwdRow {
   float rstd;
 };
 template <int V>
-__device__ __forceinline__ void load_row(const NormBwdArgs &a, uint32_t row, uint32_t cvec, BwdRow<V> &x) {
+__device__ __forceinline__ void load_row(const NormBwdArgs &a, uint32_t row, uint32_t cvec, uint32_t thread,
+                                         uint32_t threads, BwdRow<V> &x) {
   const size_t first = (size_t)row * cvec;
   x.rstd = a.rstd[row];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const uint32_t v = threadIdx.x + i * blockDim.x;
+    const uint32_t v = thread + i * threads;
     x.s[i] = x.d[i] = x.p[i] = u32x4{0u, 0u, 0u, 0u};
     if (v >= cvec) continue;
     x.s[i] = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.sum) + first + v);
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, float 
   BwdRow<kHeld> next;
   if constexpr (kStay) {
     load_weight(threadIdx.x < cvec ? a.weight : nullptr, threadIdx.x, held[0]);
-    load_row<kHeld>(a, blockIdx.x, cvec, next);
+    load_row<kHeld>(a, blockIdx.x, cvec, threadIdx.x, T, next);
   }
   const auto weight_at = [&](uint32_t v, float(&w)[8]) {
     if constexpr (kStay) {
@@ -169,9 +170,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, float 
     BwdRow<kRow> x;
     if constexpr (kStay) {
       x = next;
-      if (row + gridDim.x < B) load_row<kHeld>(a, row + gridDim.x, cvec, next);
+      if (row + gridDim.x < B) load_row<kHeld>(a, row + gridDim.x, cvec, threadIdx.x, T, next);
     } else if constexpr (kKeep) {
-      load_row<kRow>(a, row, cvec, x);
+      load_row<kRow>(a, row, cvec, threadIdx.x, T, x);
     } else {
       x.rstd = a.rstd[row];
     }
@@ -218,6 +219,85 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, float 
     f32x4 *p = reinterpret_cast<f32x4 *>(partial) + ((size_t)blockIdx.x * cvec + v) * 2;
     p[0] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
     p[1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+  }
+}
+
+// Few rows: one launch.  The first workgroups take 32 columns of dweight each,
+// which needs no sum over a row (rstd is given), and read dy and the rows a
+// second time, from the cache; the others take a row for each `threads` of
+// theirs.
+constexpr int kColumnVecs = 4;
+template <int V>
+__global__ __launch_bounds__(1024) void rmsnorm_bwd_few_kernel(NormBwdArgs a, uint32_t B, uint32_t cvec,
+                                                               uint32_t column_wgs, uint32_t threads, float inv_c) {
+  __shared__ float part[kMostWaves][kColumnVecs * 8];
+  const uint32_t T = blockDim.x;
+  if (blockIdx.x < column_wgs) {
+    const uint32_t lane = threadIdx.x % kColumnVecs, v = blockIdx.x * kColumnVecs + lane, teams = T / kColumnVecs;
+    float dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (v < cvec) {
+#pragma unroll 4
+      for (uint32_t row = threadIdx.x / kColumnVecs; row < B; row += teams) {
+        const size_t at = (size_t)row * cvec + v;
+        float n[8], g[8];
+        widen8(static_cast<const u32x4 *>(a.sum)[at], n);
+        widen8(static_cast<const u32x4 *>(a.dy)[at], g);
+        const float rstd = a.rstd[row];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[e] = fmaf(g[e], n[e] * rstd, dw[e]);
+      }
+    }
+#pragma unroll
+    for (int m = kColumnVecs; m < 64; m *= 2)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[e] += __shfl_xor(dw[e], m);
+    if ((threadIdx.x & 63) < kColumnVecs) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[threadIdx.x >> 6][lane * 8 + e] = dw[e];
+    }
+    __syncthreads();
+    const uint32_t c = blockIdx.x * kColumnVecs * 8 + threadIdx.x;
+    if (threadIdx.x < kColumnVecs * 8 && c < cvec * 8) {
+      float t = 0.f;
+      for (uint32_t w = 0; w < T / 64; ++w) t += part[w][threadIdx.x];
+      a.dweight[c] = t;
+    }
+    return;
+  }
+  const uint32_t wave = uniform((int)threadIdx.x >> 6), waves = threads >> 6, which = wave / waves;
+  const uint32_t row = (blockIdx.x - column_wgs) * (T / threads) + which, thread = threadIdx.x - which * threads;
+  BwdRow<V> x{};
+  if (row < B) load_row<V>(a, row, cvec, thread, threads, x);
+  float dot = 0.f, g[V][8], n[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t v = thread + i * threads;
+    float w[8];
+    widen8(x.s[i], n[i]);
+    widen8(x.d[i], g[i]);
+    load_weight(v < cvec ? a.weight : nullptr, v, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[i][e] *= w[e];
+      n[i][e] *= x.rstd;
+      dot = fmaf(g[i][e], n[i][e], dot);
+    }
+  }
+  dot = wave_sum(dot);
+  if ((threadIdx.x & 63) == 0) part[wave][0] = dot;
+  __syncthreads();
+  float mean = 0.f;
+  for (uint32_t w = 0; w < waves; ++w) mean += part[which * waves + w][0];
+  mean *= inv_c;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t v = thread + i * threads;
+    if (row >= B || v >= cvec) continue;
+    float o[8];
+    widen8(x.p[i], o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] += x.rstd * (g[i][e] - n[i][e] * mean);
+    store16_nt(static_cast<u32x4 *>(a.dx) + (size_t)row * cvec + v, pack8(o));
   }
 }
 
@@ -279,6 +359,15 @@ hipError_t launch_rmsnorm(int64_t B, int64_t C, const NormArgs &a, hipStream_t s
   return hipGetLastError();
 }
 
+// One launch for the gradients instead of two (us, one against two: C=7168 4.4
+// and 6.1 for one row, 4.6 and 7.2 for 64, 7.5 and 11.8 for 256, 12.3 and 12.9
+// for 512, 22 and 18 for 1024; C=256 6.7 and 9.6 for 2048 rows, 13 and 10.8 for
+// 4096; B=1001, C=1000, more than the L2 caches keep, 10.3 and 8.8).  The
+// workspace is as large as without it.
+bool few_rows(int64_t B, int64_t C) {
+  return C <= 16384 && ((B <= 512 && B * C < (4 << 20)) || (B <= 2048 && B * C <= (3 << 18)));
+}
+
 NormBwdPlan plan_rmsnorm_bwd(int64_t B, int64_t C) {
   NormBwdPlan p;
   // Workgroups, each with its own partial sums of dweight: 512, or two waves a
@@ -302,6 +391,14 @@ hipError_t launch_rmsnorm_bwd(const NormBwdPlan &p, int64_t B, int64_t C, const 
   const uint32_t grid = (uint32_t)p.parts, cvec = (uint32_t)(C / 8);
   const float inv_c = 1.0f / (float)C;
   float *partial = a.dweight ? static_cast<float *>(ws) : nullptr;
+  if (few_rows(B, C)) {
+    const uint32_t rows = s.threads >= 512 ? 1 : 512 / s.threads;  // a workgroup
+    const uint32_t column_wgs = partial ? (cvec + kColumnVecs - 1) / kColumnVecs : 0;
+    const uint32_t wgs = column_wgs + ((uint32_t)B + rows - 1) / rows, threads = s.threads * rows;
+    const auto kernel = s.v == 1 ? rmsnorm_bwd_few_kernel<1> : rmsnorm_bwd_few_kernel<2>;
+    kernel<<<wgs, threads, 0, st>>>(a, (uint32_t)B, cvec, column_wgs, s.threads, inv_c);
+    return hipGetLastError();
+  }
   switch (s.v) {
     case 1: rmsnorm_bwd_kernel<1><<<grid, s.threads, 0, st>>>(a, partial, (uint32_t)B, cvec, inv_c); break;
     case 2: rmsnorm_bwd_kernel<2><<<grid, s.threads, 0, st>>>(a, partial, (uint32_t)B, cvec, inv_c); break;

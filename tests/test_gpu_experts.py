@@ -186,7 +186,9 @@ def test_rmsnorm_borders():
     assert np.isnan(f64(_rmsnorm(torch.zeros(1, C, dtype=BF, device="cuda"), None, None, eps=0.0)["y"])).all()
 
 
-@pytest.mark.parametrize("B,C", NORM_SHAPES)
+# Both sides of the row and channel counts at which one launch does it, and several rows a workgroup.
+@pytest.mark.parametrize("B,C", NORM_SHAPES + [(1, 64), (9, 64), (301, 136), (512, 4104), (513, 4104), (512, 520), (255, 16384),
+                                              (256, 16384), (2048, 384), (2048, 392), (768, 1024)])
 def test_rmsnorm_bwd(B, C):
     _say(f"rmsnorm_bwd B={B} C={C}")
     gen = torch.Generator().manual_seed(B * 11 + C)
