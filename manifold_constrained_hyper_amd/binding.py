@@ -547,19 +547,24 @@ def _dev_ptrs(dev, tensors, sizes):
     (the kernels would run on another device than the tensor's)."""
     out = []
     for t, (nbytes, esize, name) in zip(tensors, sizes):
-        if t is None:
-            out.append(None)
-            continue
-        # What nearly every tensor is, decided in a few attribute reads.
-        if (type(t) is torch.Tensor and t.get_device() == dev and dev >= 0 and t.is_contiguous()
-                and (t.itemsize == esize or esize is None) and t.nbytes >= nbytes):
-            out.append(t.data_ptr() or None)
-            continue
-        p = _ptr(t, nbytes, esize, name)
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
-        out.append(p)
+        if t is not None:
+            # What nearly every tensor is, decided in a few attribute reads (a
+            # raw address has none of them).
+            try:
+                usual = (t.get_device() == dev >= 0 and (t.itemsize == esize or esize is None) and t.nbytes >= nbytes
+                         and t.is_contiguous())
+            except AttributeError:
+                usual = False
+            t = t.data_ptr() if usual else _dev_ptr(t, dev, nbytes, esize, name)
+        out.append(t)
     return out
+
+
+def _dev_ptr(t, dev, nbytes, esize, name):
+    p = _ptr(t, nbytes, esize, name)
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    return p
 
 
 def _dev_stream(stream, dev):
