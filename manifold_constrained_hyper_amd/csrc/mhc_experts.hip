@@ -20,8 +20,9 @@ namespace {
 // which lanes have the same one, so its rank is the wave's count so far (LDS)
 // and its earlier peers.  The waves' counts are then added up in their order.
 // Up to 4096 pairs one workgroup does it all.  Above, each workgroup ranks a
-// tile, and a second launch adds the counts of the earlier tiles and of the
-// smaller experts, which each of its workgroups sums up for itself.
+// tile of 1024 pairs or more, and a second launch adds the counts of the
+// earlier tiles and of the smaller experts, which each of its workgroups sums
+// up for itself.
 constexpr int kIdBits = 10;
 static_assert(kMaxExperts == 1 << kIdBits, "experts' bits");
 constexpr int kRounds = 4;  // of 64 pairs a wave and chunk
@@ -523,14 +524,20 @@ hipError_t gather_t(int64_t B, int k, int64_t vecs, const void *x, const uint8_t
 
 }  // namespace
 
-// Tiles of at least 4096 pairs, at most 256 of them: their counts are added up
-// by every workgroup of the second kernel, which is most of its time (all of
-// them read 4 tiles E bytes).
+// Small tiles are ranked by more workgroups, but their counts are added up by
+// every workgroup of the second kernel (all of them read 4 tiles E bytes).  us
+// with tiles of 1024, 2048 and 4096 pairs, E=256: 7.6, 8.5, 10.2 for 8192 pairs;
+// 9.4, 9.4, 10.7 for 32768; 16.1, 12.9, 12.6 for 131072; E=1024 44, 27, 20 there.
+// From 2^20 pairs on there are 256 tiles.
 OrderPlan plan_experts_order(int64_t pairs, int E) {
   OrderPlan p;
   constexpr int64_t kMost = 256;
   const int64_t chunks = (pairs + kChunk - 1) / kChunk;
-  p.tile = (chunks + kMost - 1) / kMost * kChunk;
+  const auto fits = [&](int64_t tile, int64_t counts) {
+    const int64_t tiles = (pairs + tile - 1) / tile;
+    return chunks > 1 && tiles <= kMost && tiles * E <= counts;
+  };
+  p.tile = fits(1024, 8192) ? 1024 : fits(2048, 12288) ? 2048 : (chunks + kMost - 1) / kMost * kChunk;
   p.tiles = (pairs + p.tile - 1) / p.tile;
   p.total_bytes = (size_t)p.tiles * E * 4;
   return p;

@@ -184,7 +184,7 @@ void check_sizes() {
         CHECK((ws > 0) == pairs);
         if (!pairs) continue;
         const mhc::OrderPlan p = mhc::plan_experts_order(B * k, E);
-        CHECK(p.total_bytes == ws && p.tiles >= 1 && p.tiles <= 256 && p.tile % 4096 == 0);
+        CHECK(p.total_bytes == ws && p.tiles >= 1 && p.tiles <= 256 && p.tile % 1024 == 0);
         CHECK(p.tile * p.tiles >= B * k && p.tile * (p.tiles - 1) < B * k);
         CHECK(ws == (size_t)p.tiles * (size_t)E * 4);
       }

@@ -524,7 +524,8 @@ def test_route_bwd_differences():
 # -- the experts' order -----------------------------------------------------------------------------
 
 ORDERS = [(1, 1, 1), (1, 8, 256), (5, 3, 2), (64, 8, 256), (65, 1, 7), (513, 4, 1024), (200, 32, 33), (1001, 6, 100),
-          (3000, 8, 64), (20000, 8, 256), (40000, 5, 1000), (140001, 2, 3)]
+          (3000, 8, 64), (20000, 8, 256), (40000, 5, 1000), (140001, 2, 3), (513, 8, 256), (4097, 8, 250), (6000, 8, 255),
+          (12000, 8, 256), (2000, 7, 1024), (33000, 8, 31)]
 
 
 def _order(ids, E):
