@@ -8,8 +8,8 @@
 // use, so every tensor is read or written once.  Squares and sums are fp32
 // (products of two bf16 values are exact there).
 //
-// Bound by HBM: 144 us for B=16384, C=7168 with the shortcut in 8 bits (826 MB,
-// 5.7 TB/s), 163 for its gradients with the shortcut's (940 MB, 5.8 TB/s, of
+// Bound by HBM: 139 us for B=16384, C=7168 with the shortcut in 8 bits (826 MB,
+// 6.0 TB/s), 160 for its gradients with the shortcut's (940 MB, 5.9 TB/s, of
 // which 5 us join dweight).  One row takes 3.6, and its gradients 4.4.
 #include "mhc_experts.h"
 #include "mhc_finish.h"

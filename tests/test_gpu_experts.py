@@ -736,6 +736,56 @@ def test_more_than_2_32_bytes():
     assert torch.all((dw - want).abs() <= (C + 8) * U * want)
 
 
+def test_more_rows_than_workgroups():
+    """Rows and pairs past what one grid takes: workgroups go on to the next."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    B, C = (1 << 21) + 5, 8
+    _say("many rows: norm")
+    x = torch.randn(B, C, generator=gen, device="cuda", dtype=BF)
+    y, rstd = torch.empty_like(x), torch.empty(B, device="cuda")
+    mhc.mhc_rmsnorm(B, C, x, None, y=y, rstd=rstd)
+    want = 1 / (x.double().square().mean(1) + 1e-5).sqrt()
+    assert torch.all((rstd - want).abs() <= 50 * U * want)
+    n = x.double() * want[:, None]
+    assert torch.all((y - n).abs() <= (HALF_BF16 + 54 * U) * n.abs())
+
+    _say("many rows: order, gather, combine and its gradient")
+    k, C, E = 8, 264, 5
+    x = torch.randn(B, C, generator=gen, device="cuda", dtype=BF)
+    ids = torch.randint(0, E, (B, k), generator=gen, device="cuda", dtype=torch.int32)
+    slots, offsets = _order(ids, E)
+    _, at = torch.sort(ids.reshape(-1), stable=True)
+    assert torch.equal(slots.reshape(-1)[at], torch.arange(B * k, device="cuda", dtype=torch.int32))
+    assert torch.equal(offsets[1:].long(), torch.bincount(ids.reshape(-1), minlength=E).cumsum(0))
+    rows = torch.empty(B * k, C, dtype=BF, device="cuda")
+    mhc.mhc_experts_gather(B, k, C, x, slots, rows)
+    w = torch.full((B, k), 0.125, device="cuda")
+    out, dY, dw = torch.empty_like(x), torch.empty_like(rows), torch.empty(B, k, device="cuda")
+    mhc.mhc_experts_combine(B, k, C, rows, slots, w, out)
+    mhc.mhc_experts_combine_bwd(B, k, C, rows, slots, w, x, dY, dw)
+    assert torch.equal(out, x)                               # eight equal eighths
+    for some in (slice(0, 3000), slice(B // 2, B // 2 + 3000), slice(B - 3000, B)):
+        mine = slots[some].reshape(-1).long()
+        assert torch.equal(rows[mine], x[some].repeat_interleave(k, 0))
+        assert torch.equal(dY[mine], (x[some] / 8).repeat_interleave(k, 0))
+    want = x.double().square().sum(1, keepdim=True)
+    assert torch.all((dw - want).abs() <= (C + 8) * U * want)
+    del x, rows, out, dY, dw, w, slots, ids, at, want
+
+    _say("many rows: choice and its gradient")
+    B = (1 << 26) + 17
+    x = torch.randn(B, 2, generator=gen, device="cuda")
+    ids, w, d = torch.empty(B, 1, device="cuda", dtype=torch.int32), torch.empty(B, 1, device="cuda"), torch.empty_like(x)
+    mhc.mhc_route(B, 2, 1, x, ids, w, renorm=False)
+    assert torch.equal(ids[:, 0], (x[:, 1] > x[:, 0]).int())
+    want = torch.sigmoid(x.double().amax(1))
+    assert torch.all((w[:, 0] - want).abs() <= 32 * U * want)
+    mhc.mhc_route_bwd(B, 2, 1, x, ids, w, d, renorm=False)
+    best = x.double().amax(1, keepdim=True)
+    want = torch.zeros_like(x, dtype=torch.float64).scatter_(1, ids.long(), best.sigmoid() * w * (-best).sigmoid())
+    assert torch.all((d - want).abs() <= (48 + 2 * best.abs()) * U * want)
+
+
 # -- streams, graphs --------------------------------------------------------------------------------
 
 class _Layer:
