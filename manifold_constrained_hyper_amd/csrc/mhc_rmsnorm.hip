@@ -41,7 +41,8 @@ __device__ __forceinline__ void load_weight(const float *w, uint32_t v, float (&
     for (int e = 0; e < 8; ++e) o[e] = 1.f;
     return;
   }
-  const f32x4 a = reinterpret_cast<const f32x4 *>(w)[2 * (size_t)v], b = reinterpret_cast<const f32x4 *>(w)[2 * (size_t)v + 1];
+  const f32x4 *from = reinterpret_cast<const f32x4 *>(w) + 2 * (size_t)v;
+  const f32x4 a = from[0], b = from[1];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     o[e] = a[e];
@@ -343,10 +344,18 @@ Shape shape_of(int64_t C, uint32_t wide) {
 }  // namespace
 
 hipError_t launch_rmsnorm(int64_t B, int64_t C, const NormArgs &a, hipStream_t st) {
-  // Many rows of up to 8192 channels: at most 256 threads a row (C=7168 in
-  // 8 bits, us: 147 against 163 with a thread a vector at 16384 rows, 24.8
-  // against 24.5 at 2048, 6.3 against 4.6 at 64).
-  const Shape s = shape_of(C, B >= 4096 && C <= 8192 ? 256 : 1024);
+  // Vectors a thread: one where there is little work, as a row's chain is what
+  // takes the time, else enough to have four loads in flight, two with the
+  // shortcut (its own come on top), in at least a wave.  us with 1, 2 and 4:
+  //   C=7168, shortcut, 8 bits  8.2 8.0 9.4 (512 rows)   14.7 13.0 14.8 (1024)  162 147 143 (16384)
+  //   C=7168, shortcut, bf16    7.4 7.2 8.6 (512 rows)   14.4 13.3 13.3 (1024)  163 157 161 (16384)
+  //   C=7168, bf16              5.2 5.4 6.0 (512 rows)   9.7 8.7 7.8 (1024)     116 107 88 (16384)
+  //   C=2048, bf16              4.4 4.7 5.3 (1024 rows)  9.3 8.6 7.5 (4096)     27 27 28 (16384)
+  // (Which outputs are asked for has no part in it, so that it changes no bits.)
+  const int64_t all = B * C;
+  const int v = all < (7 << 20) ? 1 : a.shortcut && (C <= 4096 || all < (56 << 20)) ? 2 : 4;
+  const int64_t wide = (C / 8 + v - 1) / v;
+  const Shape s = shape_of(C, (uint32_t)(wide < 64 ? 64 : wide < 1024 ? wide : 1024));
   const uint32_t cvec = (uint32_t)(C / 8), blocks = (uint32_t)ckpt_blocks(C), rows = (uint32_t)B;
   const float inv_c = 1.0f / (float)C;
   const uint32_t grid = (uint32_t)(B < (1 << 21) ? B : (1 << 21));

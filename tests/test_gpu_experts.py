@@ -149,6 +149,31 @@ def test_rmsnorm(B, C):
             assert torch.equal(part["codes"], o["codes"]) and torch.equal(part["scales"], o["scales"])
 
 
+@pytest.mark.parametrize("B,C", [(8195, 7168), (1100, 7168), (4000, 2048), (3600, 2056), (8200, 1024), (900, 16392)])
+def test_rmsnorm_many_values(B, C):
+    """Sizes from which a thread takes several vectors of a row, and rows that end inside them."""
+    _say(f"rmsnorm many values B={B} C={C}")
+    gen = torch.Generator(device="cuda").manual_seed(B + C)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, short, w = (normal(B, C) * torch.exp2(normal(B, 1))).to(BF), normal(B, C).to(BF), 1 + 0.3 * normal(C)
+    for shortcut in (None, short):
+        o = _rmsnorm(x, w, shortcut)
+        s = x.double()
+        if shortcut is not None:
+            s = s + short.double()
+            assert torch.all((o["sum"] - s).abs() <= (HALF_BF16 + U) * s.abs())
+            s = o["sum"].double()
+        rstd = 1 / (s.square().mean(1) + 1e-5).sqrt()
+        assert torch.all((o["rstd"] - rstd).abs() <= 50 * U * rstd)
+        y = s.mul_(rstd[:, None]).mul_(w.double())
+        assert torch.all((o["y"] - y).abs() <= (HALF_BF16 + 54 * U) * y.abs())
+        step = torch.exp2(o["scales"].double() - 127).repeat_interleave(32, 1)[:, :C]
+        got = o["codes"].view(torch.float8_e4m3fn).double() * step
+        assert torch.all((got - y).abs() <= (2.0 ** -4 + 54 * U) * y.abs() + 2.0 ** -10 * step)
+        part = _rmsnorm(x, w, shortcut, codes=False)
+        assert torch.equal(part["y"], o["y"]) and torch.equal(part["rstd"], o["rstd"])
+
+
 def test_rmsnorm_without_extras():
     """sum and rstd left out."""
     gen = torch.Generator().manual_seed(5)
@@ -187,8 +212,9 @@ def test_rmsnorm_borders():
 
 
 # Both sides of the row and channel counts at which one launch does it, and several rows a workgroup.
-@pytest.mark.parametrize("B,C", NORM_SHAPES + [(1, 64), (9, 64), (301, 136), (512, 4104), (513, 4104), (512, 520), (255, 16384),
-                                              (256, 16384), (2048, 384), (2048, 392), (768, 1024)])
+@pytest.mark.parametrize("B,C", NORM_SHAPES + [
+    (1, 64), (9, 64), (301, 136), (512, 4104), (513, 4104), (512, 520), (255, 16384), (256, 16384), (2048, 384),
+    (2048, 392), (768, 1024)])
 def test_rmsnorm_bwd(B, C):
     _say(f"rmsnorm_bwd B={B} C={C}")
     gen = torch.Generator().manual_seed(B * 11 + C)
@@ -524,8 +550,8 @@ def test_route_bwd_differences():
 # -- the experts' order -----------------------------------------------------------------------------
 
 ORDERS = [(1, 1, 1), (1, 8, 256), (5, 3, 2), (64, 8, 256), (65, 1, 7), (513, 4, 1024), (200, 32, 33), (1001, 6, 100),
-          (3000, 8, 64), (20000, 8, 256), (40000, 5, 1000), (140001, 2, 3), (513, 8, 256), (4097, 8, 250), (6000, 8, 255),
-          (12000, 8, 256), (2000, 7, 1024), (33000, 8, 31)]
+          (3000, 8, 64), (20000, 8, 256), (40000, 5, 1000), (140001, 2, 3), (513, 8, 256), (4097, 8, 250),
+          (6000, 8, 255), (12000, 8, 256), (2000, 7, 1024), (33000, 8, 31)]
 
 
 def _order(ids, E):
@@ -775,7 +801,8 @@ def test_more_rows_than_workgroups():
     _say("many rows: choice and its gradient")
     B = (1 << 26) + 17
     x = torch.randn(B, 2, generator=gen, device="cuda")
-    ids, w, d = torch.empty(B, 1, device="cuda", dtype=torch.int32), torch.empty(B, 1, device="cuda"), torch.empty_like(x)
+    ids, w = torch.empty(B, 1, device="cuda", dtype=torch.int32), torch.empty(B, 1, device="cuda")
+    d = torch.empty_like(x)
     mhc.mhc_route(B, 2, 1, x, ids, w, renorm=False)
     assert torch.equal(ids[:, 0], (x[:, 1] > x[:, 0]).int())
     want = torch.sigmoid(x.double().amax(1))
