@@ -54,6 +54,23 @@ __device__ __forceinline__ u32x4 pack8(const float (&y)[8]) {
   return u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
 }
 
+// Vector v of a row in 8 bits; four neighbouring lanes have a block.
+__device__ __forceinline__ void store_codes(const NormArgs &a, float (&y)[8], size_t row, uint32_t v,
+                                            size_t first, uint32_t blocks, bool real) {
+  uint32_t amax = 0;  // of the finite values; their bits order like they do
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t m = __float_as_uint(y[e]) & 0x7fffffffu;
+    amax = m < 0x7f800000u && m > amax ? m : amax;
+  }
+  const int sc = ckpt_scale32(quad_max(amax));
+  const u32x2 q = held_codes(y, sc);
+  if (real) {
+    __builtin_nontemporal_store(q, static_cast<u32x2 *>(a.codes) + first + v);
+    if ((v & 3u) == 0) a.scales[row * blocks + (v >> 2)] = (uint8_t)sc;
+  }
+}
+
 // V vectors of eight channels a thread, all of a row.
 template <int V>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a, uint32_t B, uint32_t cvec, uint32_t blocks,
@@ -96,21 +113,50 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormArgs a, uint32_t B, u
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = v < cvec ? y[e] * rstd * w[e] : 0.f;
       if (a.y && v < cvec) store16_nt(static_cast<u32x4 *>(a.y) + first + v, pack8(y));
-      if (a.codes) {
-        uint32_t amax = 0;  // of the finite values; their bits order like they do
+      if (a.codes) store_codes(a, y, row, v, first, blocks, v < cvec);
+    }
+  }
+}
+
+// Rows of up to 32 vectors: `lanes` of a wave (a power of two, four at least)
+// take one.  us for 65536 rows with the shortcut in 8 bits, and with a
+// workgroup a row: C=64 7.8 and 27, C=256 25 and 32, C=512 46 and 44.
+constexpr int kShortWaves = 4, kShortVecs = 32;
+__device__ __forceinline__ float lanes_sum(float x, uint32_t lanes) {
+  for (uint32_t m = 1; m < lanes; m <<= 1) x += __shfl_xor(x, m);
+  return x;
+}
+__global__ __launch_bounds__(64 * kShortWaves) void rmsnorm_short_kernel(NormArgs a, uint32_t B, uint32_t cvec,
+                                                                         uint32_t lanes, uint32_t blocks, float inv_c) {
+  const uint32_t lane = threadIdx.x & 63, rows = 64 / lanes, v = lane & (lanes - 1);
+  const uint64_t step = (uint64_t)gridDim.x * kShortWaves * rows;
+  for (uint64_t base = ((uint64_t)blockIdx.x * kShortWaves + (threadIdx.x >> 6)) * rows; base < B; base += step) {
+    const uint64_t row = base + lane / lanes;
+    const size_t first = row * cvec;
+    const bool real = row < B && v < cvec;
+    u32x4 s = {0u, 0u, 0u, 0u};
+    if (real) {
+      s = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.x) + first + v);
+      if (a.shortcut) {
+        const u32x4 c = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.shortcut) + first + v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t m = __float_as_uint(y[e]) & 0x7fffffffu;
-          amax = m < 0x7f800000u && m > amax ? m : amax;
-        }
-        const int sc = ckpt_scale32(quad_max(amax));
-        const u32x2 q = held_codes(y, sc);
-        if (v < cvec) {
-          __builtin_nontemporal_store(q, static_cast<u32x2 *>(a.codes) + first + v);
-          if ((v & 3u) == 0) a.scales[(size_t)row * blocks + (v >> 2)] = (uint8_t)sc;
-        }
+        for (int q = 0; q < 4; ++q)
+          s[q] = pack_bf16x2(bf16_lo(s[q]) + bf16_lo(c[q]), bf16_hi(s[q]) + bf16_hi(c[q]));
+        if (a.sum) store16_nt(static_cast<u32x4 *>(a.sum) + first + v, s);
       }
     }
+    float sq = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sq = dot2_bf16(s[q], s[q], sq);
+    const float rstd = 1.0f / sqrtf(lanes_sum(sq, lanes) * inv_c + a.eps);
+    if (a.rstd && real && v == 0) a.rstd[row] = rstd;
+    float y[8], w[8];
+    widen8(s, y);
+    load_weight(real ? a.weight : nullptr, v, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = real ? y[e] * rstd * w[e] : 0.f;
+    if (a.y && real) store16_nt(static_cast<u32x4 *>(a.y) + first + v, pack8(y));
+    if (a.codes) store_codes(a, y, row, v, first, blocks, real);
   }
 }
 
@@ -220,6 +266,62 @@ __global__ __launch_bounds__(1024) void rmsnorm_bwd_kernel(NormBwdArgs a, float 
     f32x4 *p = reinterpret_cast<f32x4 *>(partial) + ((size_t)blockIdx.x * cvec + v) * 2;
     p[0] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
     p[1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+  }
+}
+
+// The gradients, of rows of up to 64 vectors (C=64 12 us, 36 with a workgroup a
+// row; C=256 30, 43; C=512 55, 55, but 19, 23 for 16384 rows).
+constexpr int kShortVecsBwd = 64;
+__global__ __launch_bounds__(64 * kShortWaves) void rmsnorm_bwd_short_kernel(NormBwdArgs a, float *partial, uint32_t B,
+                                                                             uint32_t cvec, uint32_t lanes,
+                                                                             float inv_c) {
+  __shared__ float part[kShortWaves][kShortVecsBwd * 8];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, rows = 64 / lanes, v = lane & (lanes - 1);
+  const uint64_t step = (uint64_t)gridDim.x * kShortWaves * rows;
+  float w[8], dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  load_weight(v < cvec ? a.weight : nullptr, v, w);
+  for (uint64_t base = ((uint64_t)blockIdx.x * kShortWaves + wave) * rows; base < B; base += step) {
+    const uint64_t row = base + lane / lanes;
+    const size_t at = row * cvec + v;
+    const bool real = row < B && v < cvec;
+    u32x4 s = {0u, 0u, 0u, 0u}, d = s, p = s;
+    float rstd = 0.f;
+    if (real) {
+      s = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.sum) + at);
+      d = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.dy) + at);
+      if (a.dsum) p = __builtin_nontemporal_load(static_cast<const u32x4 *>(a.dsum) + at);
+      rstd = a.rstd[row];
+    }
+    float n[8], g[8], o[8], dot = 0.f;
+    widen8(s, n);
+    widen8(d, g);
+    widen8(p, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      n[e] *= rstd;
+      dw[e] = fmaf(g[e], n[e], dw[e]);
+      g[e] *= w[e];
+      dot = fmaf(g[e], n[e], dot);
+    }
+    const float mean = lanes_sum(dot, lanes) * inv_c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] += rstd * (g[e] - n[e] * mean);
+    if (real) store16_nt(static_cast<u32x4 *>(a.dx) + at, pack8(o));
+  }
+  if (!partial) return;
+  for (uint32_t m = lanes; m < 64; m <<= 1)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[e] += __shfl_xor(dw[e], m);
+  if (lane < cvec) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[wave][lane * 8 + e] = dw[e];
+  }
+  __syncthreads();
+  for (uint32_t c = threadIdx.x; c < cvec * 8; c += 64 * kShortWaves) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kShortWaves; ++i) t += part[i][c];
+    partial[(size_t)blockIdx.x * cvec * 8 + c] = t;
   }
 }
 
@@ -341,6 +443,14 @@ Shape shape_of(int64_t C, uint32_t wide) {
   return s;
 }
 
+// Lanes that take a short row, 0 for one of more than `most` vectors.
+uint32_t short_lanes(int64_t C, int most) {
+  if (C > 8 * most) return 0;
+  uint32_t lanes = 4;
+  while (lanes * 8 < C) lanes *= 2;
+  return lanes;
+}
+
 }  // namespace
 
 hipError_t launch_rmsnorm(int64_t B, int64_t C, const NormArgs &a, hipStream_t st) {
@@ -358,6 +468,12 @@ hipError_t launch_rmsnorm(int64_t B, int64_t C, const NormArgs &a, hipStream_t s
   const Shape s = shape_of(C, (uint32_t)(wide < 64 ? 64 : wide < 1024 ? wide : 1024));
   const uint32_t cvec = (uint32_t)(C / 8), blocks = (uint32_t)ckpt_blocks(C), rows = (uint32_t)B;
   const float inv_c = 1.0f / (float)C;
+  if (const uint32_t lanes = short_lanes(C, kShortVecs)) {
+    const int64_t per = kShortWaves * 64 / lanes, wgs = (B + per - 1) / per;
+    rmsnorm_short_kernel<<<(uint32_t)(wgs < (1 << 21) ? wgs : (1 << 21)), 64 * kShortWaves, 0, st>>>(
+        a, rows, cvec, lanes, blocks, inv_c);
+    return hipGetLastError();
+  }
   const uint32_t grid = (uint32_t)(B < (1 << 21) ? B : (1 << 21));
   switch (s.v) {
     case 1: rmsnorm_kernel<1><<<grid, s.threads, 0, st>>>(a, rows, cvec, blocks, inv_c); break;
@@ -383,7 +499,14 @@ NormBwdPlan plan_rmsnorm_bwd(int64_t B, int64_t C) {
   // SIMD where rows are short, but not fewer than eight rows each (C=1000, us:
   // 9.1 with 256 for 1001 rows, 12.9 with 1024; 34.5 with 1024 for 16384 rows,
   // 37 with 512; C=7168: 164 with 512 for 16384 rows, 169 with 1024).
+  // Of short rows a workgroup takes two turns at least.
   constexpr int64_t kPer = 8, kLeast = 256;
+  if (const uint32_t lanes = short_lanes(C, kShortVecsBwd)) {
+    const int64_t turns = 2 * kShortWaves * 64 / lanes, wgs = (B + turns - 1) / turns;
+    p.parts = wgs < 512 ? wgs : 512;
+    p.total_bytes = (size_t)p.parts * C * 4;
+    return p;
+  }
   const int64_t waves = shape_of(C, 1024).threads / 64;
   int64_t parts = 2048 / waves;
   parts = parts < 512 ? 512 : parts;
@@ -408,7 +531,11 @@ hipError_t launch_rmsnorm_bwd(const NormBwdPlan &p, int64_t B, int64_t C, const 
     kernel<<<wgs, threads, 0, st>>>(a, (uint32_t)B, cvec, column_wgs, s.threads, inv_c);
     return hipGetLastError();
   }
-  switch (s.v) {
+  const uint32_t lanes = short_lanes(C, kShortVecsBwd);
+  switch (lanes ? 0 : s.v) {
+    case 0:
+      rmsnorm_bwd_short_kernel<<<grid, 64 * kShortWaves, 0, st>>>(a, partial, (uint32_t)B, cvec, lanes, inv_c);
+      break;
     case 1: rmsnorm_bwd_kernel<1><<<grid, s.threads, 0, st>>>(a, partial, (uint32_t)B, cvec, inv_c); break;
     case 2: rmsnorm_bwd_kernel<2><<<grid, s.threads, 0, st>>>(a, partial, (uint32_t)B, cvec, inv_c); break;
     case 4: rmsnorm_bwd_kernel<4><<<grid, s.threads, 0, st>>>(a, partial, (uint32_t)B, cvec, inv_c); break;

@@ -214,7 +214,8 @@ def test_rmsnorm_borders():
 # Both sides of the row and channel counts at which one launch does it, and several rows a workgroup.
 @pytest.mark.parametrize("B,C", NORM_SHAPES + [
     (1, 64), (9, 64), (301, 136), (512, 4104), (513, 4104), (512, 520), (255, 16384), (256, 16384), (2048, 384),
-    (2048, 392), (768, 1024)])
+    (2048, 392), (768, 1024), (3000, 8), (2500, 24), (4100, 32), (2049, 40), (2100, 64), (2051, 136), (2060, 256), (2100, 264),
+    (2049, 512), (5000, 504)])
 def test_rmsnorm_bwd(B, C):
     _say(f"rmsnorm_bwd B={B} C={C}")
     gen = torch.Generator().manual_seed(B * 11 + C)
