@@ -428,7 +428,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void combine_bwd_kernel(
   }
 }
 
-// Short rows, several a wave.
+// Short rows, several a wave, BATCH rows of Y in flight.
+template <int BATCH>
 __global__ __launch_bounds__(kThreads) void combine_bwd_short_kernel(
     const u32x4 *__restrict__ Y, const int32_t *__restrict__ slots, const float *__restrict__ weights,
     const u32x4 *__restrict__ dout, u32x4 *__restrict__ dY, float *__restrict__ dweights, Short r, uint64_t B, int k,
@@ -440,16 +441,28 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_short_kernel(
     const bool real = place_of(r, u, B, &row, &v);
     const bool mine = real && v < r.vecs;
     const u32x4 g = mine ? dout[row * r.vecs + v] : u32x4{0u, 0u, 0u, 0u};
-    for (int j = 0; j < k; ++j) {
-      const uint32_t slot = real ? (uint32_t)slots[row * k + j] : ~0u;
-      float dot = 0.f;
-      if (mine && slot < pairs) {
-        const size_t at = (size_t)slot * r.vecs + v;
-        dot = dot8(g, __builtin_nontemporal_load(Y + at), 0.f);
-        store16_nt(dY + at, weighted(g, weights[row * k + j]));
+    for (int j0 = 0; j0 < k; j0 += BATCH) {
+      u32x4 y[BATCH];
+      float dot[BATCH];
+      uint32_t slot[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) slot[j] = mine && j0 + j < k ? (uint32_t)slots[row * k + j0 + j] : ~0u;
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (slot[j] < pairs) y[j] = __builtin_nontemporal_load(Y + (size_t)slot[j] * r.vecs + v);
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        dot[j] = 0.f;
+        if (slot[j] >= pairs) continue;
+        dot[j] = dot8(g, y[j], 0.f);
+        store16_nt(dY + (size_t)slot[j] * r.vecs + v, weighted(g, weights[row * k + j0 + j]));
       }
-      for (uint32_t m = 1; m < r.lanes; m <<= 1) dot += __shfl_xor(dot, m);
-      if (real && v == 0) dweights[row * k + j] = dot;
+      for (uint32_t m = 1; m < r.lanes; m <<= 1)
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) dot[j] += __shfl_xor(dot[j], m);
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (real && v == 0 && j0 + j < k) dweights[row * k + j0 + j] = dot[j];
     }
   }
 }
@@ -598,13 +611,18 @@ hipError_t launch_experts_combine_bwd(int64_t B, int k, int64_t C, const void *Y
   const uint32_t pairs = (uint32_t)(B * k), cvec = (uint32_t)(C / 8);
   if (!is_long(cvec)) {
     const Short r = short_of(B, cvec);
-    combine_bwd_short_kernel<<<grid_of(r.units, kWaves), kThreads, 0, st>>>(y, slots, weights, g, dy, dweights, r,
-                                                                            (uint64_t)B, k, pairs);
-  } else if (k <= 2 && pairs >= 2048) {
+    // Rows of Y in flight, us with one and with as many as there are: C=64 15.1
+    // and 8.9 for 16384 rows at k=8, 8.6 and 6.3 at k=4; C=256 30.4 and 32.1, 16.7
+    // and 15.5, but 7.8 and 5.5 for 64 rows at k=8.
+    const auto kernel = k == 1   ? combine_bwd_short_kernel<1>
+                        : k <= 4 ? combine_bwd_short_kernel<4>
+                                 : combine_bwd_short_kernel<8>;
+    kernel<<<grid_of(r.units, kWaves), kThreads, 0, st>>>(y, slots, weights, g, dy, dweights, r, (uint64_t)B, k, pairs);
+  } else if (k <= 2 && B >= 768) {
     // A workgroup a row has few loads in flight at k = 1 and 2 (C=7168, us: 30
-    // against 40 for 4096 rows at k=1, 51 against 59 at k=2); from k = 3 on it
-    // is faster (183 against 188 at k=8), and with few rows (4.5 against 7.4
-    // for 64 at k=2).
+    // against 40 for 4096 rows at k=1, 51 against 59 at k=2, 10.4 against 11.0
+    // for 768 at k=1, 14.1 against 14.4 at k=2); from k = 3 on it is faster (183
+    // against 188 at k=8), and with fewer rows (7.2 against 8.7 for 512 at k=1).
     combine_bwd_pair_kernel<<<grid_of(pairs, kWaves), kThreads, 0, st>>>(y, slots, weights, g, dy, dweights, cvec,
                                                                          (uint32_t)k, pairs);
   } else {

@@ -679,7 +679,9 @@ def test_gather_many_rows(B, k, C):
     assert int(left.sum()) == k and torch.all(rows.t[left] == 0x7F) and torch.all(more.t[left] == 0x7F)
 
 
-@pytest.mark.parametrize("B,k,C", [(2100, 1, 1032), (1500, 2, 520), (900, 3, 264), (4000, 2, 40)])
+@pytest.mark.parametrize("B,k,C", [
+    (2100, 1, 1032), (1500, 2, 520), (900, 3, 264), (4000, 2, 40), (767, 1, 776), (768, 1, 776), (769, 2, 264),
+    (700, 1, 256), (301, 3, 64), (90, 4, 8), (77, 9, 128), (41, 17, 200)])
 def test_combine_bwd_many_rows(B, k, C):
     """One and two slots a row of many rows, on both sides of the choice of kernels."""
     _say(f"combine_bwd many B={B} k={k} C={C}")
