@@ -142,6 +142,9 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t *__r
   const uint32_t tid = threadIdx.x, e = tid & (stride - 1), teams = kPlaceThreads / stride;
   const uint64_t first = (uint64_t)blockIdx.x * share, last = first + share < pairs ? first + share : pairs;
   const uint32_t mine = (uint32_t)(first / tile);
+  // The thread's first pair (mostly its only one), asked for ahead of the counts.
+  const uint64_t own = first + tid;
+  const int32_t own_id = own < last ? ids[own] : -1, own_rank = own < last ? slots[own] : 0;
   uint32_t b = 0, all = 0;
   if (e < (uint32_t)E) {
 #pragma unroll 8
@@ -168,7 +171,8 @@ __global__ __launch_bounds__(kPlaceThreads) void place_kernel(const int32_t *__r
   }
   if (blockIdx.x == 0 && tid == 0) offsets[E] = (int32_t)every;
   __syncthreads();
-  for (uint64_t p = first + tid; p < last; p += kPlaceThreads) {
+  if (own_id >= 0 && own_id < E) slots[own] = own_rank + (int32_t)before[own_id];
+  for (uint64_t p = own + kPlaceThreads; p < last; p += kPlaceThreads) {
     const int32_t id = ids[p];
     if (id >= 0 && id < E) slots[p] += (int32_t)before[id];
   }
