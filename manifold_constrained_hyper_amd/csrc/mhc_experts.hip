@@ -243,7 +243,8 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(const T *__restrict__ 
     }
     if (more) {
       if (lane < blocks) row_scales[(size_t)slot * blocks + lane] = s;
-      for (uint32_t i = lane + 64; i < blocks; i += 64) row_scales[(size_t)slot * blocks + i] = scales[row * blocks + i];
+      for (uint32_t i = lane + 64; i < blocks; i += 64)
+        row_scales[(size_t)slot * blocks + i] = scales[row * blocks + i];
     }
   }
 }
@@ -631,8 +632,8 @@ hipError_t launch_experts_combine_bwd(int64_t B, int k, int64_t C, const void *Y
                                                                          (uint32_t)k, pairs);
   } else {
     const uint32_t waves = (cvec + 63) / 64 < kRowWaves ? (cvec + 63) / 64 : kRowWaves;
-    combine_bwd_kernel<<<(uint32_t)(B < (1 << 21) ? B : (1 << 21)), 64 * waves, 0, st>>>(y, slots, weights, g, dy, dweights, (uint32_t)B, cvec, k,
-                                                           pairs);
+    combine_bwd_kernel<<<(uint32_t)(B < (1 << 21) ? B : (1 << 21)), 64 * waves, 0, st>>>(
+        y, slots, weights, g, dy, dweights, (uint32_t)B, cvec, k, pairs);
   }
   return hipGetLastError();
 }

@@ -177,8 +177,9 @@ int mhc_experts_combine(int64_t B, int32_t k, int64_t C, const void *Y, const in
   int st = check_pair_rows(B, k, C);
   if (st != MHC_OK || B == 0) return st;
   const size_t row = (size_t)B * C * 2, pairs = (size_t)B * k * 4;
-  st = check_buffers({{Y, row * k, 16}, {slots, pairs, 4}, {weights, pairs, 4, kOptional}, {shared, row, 16, kOptional}},
-                     {{F_out, row, 16}});
+  st = check_buffers(
+      {{Y, row * k, 16}, {slots, pairs, 4}, {weights, pairs, 4, kOptional}, {shared, row, 16, kOptional}},
+      {{F_out, row, 16}});
   if (st != MHC_OK) return st;
   return from_hip(
       launch_experts_combine(B, k, C, Y, slots, weights, shared, F_out, static_cast<hipStream_t>(stream)));
