@@ -764,6 +764,8 @@ int mhc_rmsnorm_bwd(int64_t B, int64_t C, const void *sum, const float *weight, 
  *              scale * score_j / (sum of the chosen scores), which holds for
  *              logits of any size (no score underflows in it)
  *
+ * in 64 bits, rounded once to fp32.
+ *
  *   flags    MHC_ROUTE_SOFTMAX, MHC_ROUTE_RENORM, MHC_ROUTE_BF16 (bf16 logits)
  *   logits   in  fp32 [B, E], or bf16
  *   bias     in  fp32 [E], or NULL

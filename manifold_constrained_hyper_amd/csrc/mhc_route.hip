@@ -17,6 +17,7 @@
 //
 // Renormalised weights are formed from exp(min(x, 0) - most) / (1 + exp(-|x|)),
 // the scores times a common factor under which the largest does not underflow.
+// Weights are formed in 64 bits and rounded once.
 #include "mhc_experts.h"
 #include "mhc_finish.h"
 
@@ -145,12 +146,20 @@ __device__ __forceinline__ double choice_of(double key) {
 __constant__ const double kInverse[] = {1.0,           1.0,            0.5,        1.0 / 6,     1.0 / 24,
                                         1.0 / 120,     1.0 / 720,      1.0 / 5040, 1.0 / 40320, 1.0 / 362880,
                                         1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
-template <int TERMS, int N>
+// HERE: the constants are formed where they are used; or the compiler keeps them
+// in vector registers over the rows (133 of them, and three waves a SIMD, for the
+// weights of sixteen experts a lane).
+template <bool HERE>
+__device__ __forceinline__ double constant(double c) {
+  if constexpr (HERE) asm volatile("" : "+s"(c));
+  return c;
+}
+template <int TERMS, bool HERE = false, int N>
 __device__ __forceinline__ void exp_64(double (&x)[N]) {
   constexpr double kShift = 0x1.8p52;  // a number added to it is rounded to an integer in the low bits
   double n[N], p[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) n[i] = fma(x[i], 1.4426950408889634, kShift);
+  for (int i = 0; i < N; ++i) n[i] = fma(x[i], constant<HERE>(1.4426950408889634), kShift);
   int e[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -159,16 +168,16 @@ __device__ __forceinline__ void exp_64(double (&x)[N]) {
   }
   // ln 2 in two parts, the upper one with few enough bits for n times it to be exact
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = fma(n[i], -0.6931471803691238, x[i]);
+  for (int i = 0; i < N; ++i) x[i] = fma(n[i], constant<HERE>(-0.6931471803691238), x[i]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = fma(n[i], -1.9082149292705877e-10, x[i]);
+  for (int i = 0; i < N; ++i) x[i] = fma(n[i], constant<HERE>(-1.9082149292705877e-10), x[i]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) p[i] = kInverse[TERMS];
+  for (int i = 0; i < N; ++i) p[i] = constant<HERE>(kInverse[TERMS]);
   constexpr int kStep = TERMS > 9 ? 1 : TERMS;  // (few rows come to the long series: its constants stay in memory)
 #pragma unroll kStep
   for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = fma(p[i], x[i], kInverse[t]);
+    for (int i = 0; i < N; ++i) p[i] = fma(p[i], x[i], constant<HERE>(kInverse[t]));
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = __builtin_amdgcn_ldexp(p[i], e[i]);
 }
@@ -183,12 +192,12 @@ __device__ __forceinline__ void reciprocal_64(double (&x)[N]) {
   }
 }
 // WHOLE: to all 64 bits, down to 0; else to 2^-35, and none below exp(-700).
-template <bool WHOLE, int N>
+template <bool WHOLE, bool HERE = false, int N>
 __device__ __forceinline__ void sigmoid_64(const float (&x)[N], double (&s)[N]) {
   constexpr float kFar = WHOLE ? 1000.0f : 700.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] = -(double)__builtin_amdgcn_fmed3f(x[i], -kFar, kFar);
-  exp_64<WHOLE ? 12 : 9>(s);
+  exp_64<WHOLE ? 12 : 9, HERE>(s);
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] += 1.0;
   if constexpr (WHOLE) {
@@ -199,11 +208,11 @@ __device__ __forceinline__ void sigmoid_64(const float (&x)[N], double (&s)[N]) 
   }
 }
 // exp(x - top) for x <= top, 0 for minus infinity.
-template <bool WHOLE, int N>
+template <bool WHOLE, bool HERE = false, int N>
 __device__ __forceinline__ void exp_from(const float (&x)[N], float top, double (&e)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) e[i] = __builtin_fmax((double)x[i] - (double)top, WHOLE ? -1000.0 : -700.0);
-  exp_64<WHOLE ? 12 : 9>(e);
+  exp_64<WHOLE ? 12 : 9, HERE>(e);
 #pragma unroll
   for (int i = 0; i < N; ++i) e[i] = x[i] > -__builtin_inff() ? e[i] : 0.0;
 }
@@ -234,18 +243,38 @@ __device__ __forceinline__ void sort_keys(double (&x)[N]) {
 constexpr double kNear = 0x1p-33;
 
 // The weight (without the scale) of a chosen logit, one a lane of a row's L;
-// minus infinity where there is none.  top, all: the row's softmax.
+// minus infinity where there is none.  top, all: the row's softmax.  In 64 bits
+// to 2^-33, as weights are rounded once, with the scale: in 32 they were off by
+// up to three roundings, and sigmoids and shares below 2^-126 were lost before
+// the scale came to them.  (An IEEE division: a single weight is 1.)
 template <int L>
-__device__ __forceinline__ float weight_of(const RouteArgs &a, float x, float top, float all) {
+__device__ __forceinline__ double weight_of(const RouteArgs &a, float x, float top, double all) {
   const bool is = x > -__builtin_inff();
+  double w;
   if (a.renorm) {
-    const float most = row_max<L>(a.softmax ? x : fminf(x, 0.f));
-    float e = 0.f;
-    if (is) e = a.softmax ? expf(x - most) : expf(fminf(x, 0.f) - most) / (1.0f + expf(-fabsf(x)));
-    const float sum = row_sum<L>(e);
-    return is ? e / sum : 0.f;
+    const float z[1] = {a.softmax ? x : fminf(x, 0.f)};
+    const float most = row_max<L>(z[0]);
+    double e[1];
+    exp_from<false, true>(z, most, e);
+    if (!a.softmax) {
+      const float y[1] = {fabsf(x)};
+      double s[1];
+      sigmoid_64<false, true>(y, s);
+      e[0] *= s[0];
+    }
+    w = e[0] / row_join<L>(is ? e[0] : 0.0, [](double p, double q) { return p + q; });
+  } else if (a.softmax) {
+    const float z[1] = {x};
+    double e[1];
+    exp_from<false, true>(z, top, e);
+    w = e[0] / all;
+  } else {
+    const float z[1] = {x};
+    double s[1];
+    sigmoid_64<false, true>(z, s);
+    w = s[0];
   }
-  return !is ? 0.f : a.softmax ? expf(x - top) / all : 1.0f / (1.0f + expf(-x));
+  return is ? w : 0.0;
 }
 
 struct RouteShape {
@@ -590,10 +619,10 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
         id = __builtin_amdgcn_ds_permute(4 * to, id);
       }
     }
-    const float w = weight_of<L>(a, l < a.k && id >= 0 ? x_row[place(id)] : none, top, (float)all);
+    const double w = weight_of<L>(a, l < a.k && id >= 0 ? x_row[place(id)] : none, top, all);
     if (real && l < a.k) {
       ids[row * a.k + l] = id;
-      weights[row * a.k + l] = w * a.scale;
+      weights[row * a.k + l] = (float)(w * (double)a.scale);
     }
     wave_lds_fence();  // the next rows' logits go where these were
   }
@@ -666,7 +695,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteArgs a, con
       for (int t = 0; t < V; ++t)
         if (lane + 64 * t < total) out[lane + 64 * t] = 0.f;
       d = dw;
-      const float w = weight_of<L>(a, x, 0.f, 1.f);  // the score itself where it is not renormalised
+      const float w = (float)weight_of<L>(a, x, 0.f, 1.0);  // the score itself where it is not renormalised
       d = a.renorm ? w * (dw - row_sum<L>(w * dw)) : w * dw;
       if (!a.softmax) d = d / (1.0f + expf(x));
       if (!(x > none)) d = 0.f;
