@@ -635,6 +635,9 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
 //   sigmoid          dx_j = dz_j (1 - sigmoid(x_j)), dz_j = sigmoid(x_j) dw_j if
 //                    not renormalised
 //
+// In fp32.  Sigmoids on either side of 0 are formed from exp(-|x|), so that they
+// have a gradient below 2^-126 too.
+//
 // L lanes take a row and form its gradient in LDS (the chosen ones' parts are
 // added to zeros or to the softmax's), which leaves in memory order, V values a
 // lane.  B=16383, E=100, k=6, softmax in bf16: 6.1 us (6.9 MB, and a launch is
@@ -694,10 +697,20 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteArgs a, con
 #pragma unroll
       for (int t = 0; t < V; ++t)
         if (lane + 64 * t < total) out[lane + 64 * t] = 0.f;
-      d = dw;
-      const float w = (float)weight_of<L>(a, x, 0.f, 1.0);  // the score itself where it is not renormalised
-      d = a.renorm ? w * (dw - row_sum<L>(w * dw)) : w * dw;
-      if (!a.softmax) d = d / (1.0f + expf(x));
+      const float u = expf(-fabsf(x)), near = 1.0f / (1.0f + u);  // the sigmoid of |x|; that of -|x| is u near
+      float w;
+      if (a.renorm) {
+        const float z = a.softmax ? x : fminf(x, 0.f), most = row_max<L>(z);
+        float e = 0.f;
+        if (x > none) e = a.softmax ? expf(z - most) : expf(z - most) * near;
+        const float sum = row_sum<L>(e);
+        w = x > none ? e / sum : 0.f;
+      } else {
+        w = x > none ? (x < 0.f ? u * near : near) : 0.f;
+      }
+      d = w * dw;
+      if (a.renorm) d = w * (dw - row_sum<L>(d));
+      if (!a.softmax) d *= x < 0.f ? near : u * near;
       if (!(x > none)) d = 0.f;
     }
     // An expert that was given twice: the first of its lanes adds all parts.

@@ -64,3 +64,29 @@ def test_route_weights_are_rounded_once(B, E, k, groups, top_groups, dtype):
                     assert np.array_equal(ids.cpu().numpy()[rows], want)
                     _within(f64(weights)[rows], want_w, (1 + 2.0 ** -8) * U * np.abs(want_w) + 2.0 ** -150,
                             f"weights softmax={softmax} renorm={renorm} scale={scale}")
+
+
+@pytest.mark.parametrize("B,E,k", [(40, 24, 4), (4100, 33, 6)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_bwd_of_far_sigmoids(B, E, k, renorm):
+    """Sigmoids next to 0 and next to 1, whose gradients are below fp32's normal numbers but for dweights: exp is off by
+    4 u (2^-148 there), a sigmoid by 3 more, a weight by 2 exps, sigmoid, sum of k <= 6 (its terms' 11 and 4) and division: 27 u;
+    with products and difference 40 u of w sigmoid(-x) (|dw| + sum w |dw|)."""
+    _say(f"route_bwd far sigmoids B={B} E={E} k={k} renorm={renorm}")
+    gen = torch.Generator().manual_seed(B + k)
+    x = _far_logits(B, E, gen, torch.float32).cpu()
+    ids = torch.argsort(torch.rand(B, E, generator=gen), 1)[:, :k].int()
+    dw = torch.randn(B, k, generator=gen) * 2.0 ** 70
+    out = Guarded(B, E)
+    mhc.mhc_route_bwd(B, E, k, x.cuda(), ids.cuda(), dw.cuda(), out.t, softmax=False, renorm=renorm, scale=1.5)
+    _checked(out)
+    rows = np.arange(B) if B < 100 else _some_rows(B)
+    x, at, dw = f64(x)[rows], ids.numpy()[rows], f64(dw)[rows]
+    want = experts.route_bwd(x, at, dw, False, renorm, 1.5)
+    size, far = np.zeros_like(want), np.zeros_like(want)
+    for b, z in enumerate(x):
+        w = experts.weights_of(z, list(at[b]), False, renorm, 1.0)
+        all_of = np.abs(1.5 * dw[b]) + (np.sum(np.abs(w * 1.5 * dw[b])) if renorm else 0.0)
+        size[b, at[b]] = w * experts.sigmoid(-z[at[b]]) * all_of
+        far[b, at[b]] = all_of                               # (two of the factors may be below the normal numbers)
+    _within(f64(out.t)[rows], want, 40 * U * size + 2.0 ** -146 * far, "dlogits")
