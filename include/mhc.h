@@ -791,7 +791,10 @@ int mhc_route(int64_t B, int32_t E, int32_t k, int32_t groups, int32_t top_group
  *                         occur twice)
  *   dweights  in  fp32 [B, k]
  *   dlogits   out fp32 [B, E], or bf16 as the logits: every value is written,
- *                 zeros where no gradient arrives */
+ *                 zeros where no gradient arrives
+ *
+ * In fp32; under MHC_ROUTE_SOFTMAX alone, shares of less than 2^-126 of the
+ * largest count as 0 for experts that were not chosen. */
 int mhc_route_bwd(int64_t B, int32_t E, int32_t k, int32_t flags, float scale, const void *logits,
                   const int32_t *ids, const float *dweights, void *dlogits, void *stream);
 

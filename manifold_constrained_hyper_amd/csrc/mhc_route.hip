@@ -628,6 +628,15 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
   }
 }
 
+// exp(x) for x <= 0 to 4 roundings; 0 below 2^-126.  The product h = x log2 e is
+// off by up to |x| of them, which the factor 1 + (x - h ln 2) makes good, ln 2 in
+// two parts (expf took 6.7 us for 6.1 at B=16383, E=100 in bf16).
+__device__ __forceinline__ float exp_32(float x) {
+  x = fmaxf(x, -200.0f);
+  const float h = x * kLog2e, e = __builtin_amdgcn_exp2f(h);
+  return fmaf(e, fmaf(h, 1.9046542e-9f, fmaf(h, -0.69314718f, x)), e);
+}
+
 // -- gradient ---------------------------------------------------------------
 //
 //   softmax          dx_i = p_i (dw_i - sum p dw)           over all experts
@@ -635,8 +644,8 @@ __global__ __launch_bounds__(64 * kWaves, V <= 16 ? 3 : 2) void route_kernel(
 //   sigmoid          dx_j = dz_j (1 - sigmoid(x_j)), dz_j = sigmoid(x_j) dw_j if
 //                    not renormalised
 //
-// In fp32.  Sigmoids on either side of 0 are formed from exp(-|x|), so that they
-// have a gradient below 2^-126 too.
+// In fp32.  Sigmoids on either side of 0 are formed from exp(-|x|), and the chosen
+// ones' shares by expf, so that they have a gradient below 2^-126 too.
 //
 // L lanes take a row and form its gradient in LDS (the chosen ones' parts are
 // added to zeros or to the softmax's), which leaves in memory order, V values a
@@ -682,12 +691,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteArgs a, con
       top = row_max<L>(top);
 #pragma unroll
       for (int t = 0; t < V; ++t) {
-        y[t] = y[t] > none ? __builtin_amdgcn_exp2f((y[t] - top) * kLog2e) : 0.f;
+        y[t] = exp_32(y[t] - top);  // (0 where there is no expert)
         all += y[t];
       }
       all = row_sum<L>(all);
       const float share = all > 0.f ? 1.0f / all : 0.f;
-      d = x > none ? __builtin_amdgcn_exp2f((x - top) * kLog2e) * share * dw : 0.f;
+      d = x > none ? expf(x - top) * share * dw : 0.f;
       const float along = row_sum<L>(d) * share;
       wave_lds_fence();
 #pragma unroll

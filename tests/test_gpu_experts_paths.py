@@ -66,6 +66,33 @@ def test_route_weights_are_rounded_once(B, E, k, groups, top_groups, dtype):
                             f"weights softmax={softmax} renorm={renorm} scale={scale}")
 
 
+@pytest.mark.parametrize("B,E,k", [(30, 64, 5), (12, 1000, 20), (4099, 50, 6), (4097, 200, 3)])
+def test_route_bwd_of_small_shares(B, E, k):
+    """The softmax's gradient where shares are far below the largest, to their own size.  Logits are multiples of 2^-6,
+    so that x - top is exact; exp is off by 4 u, the sum of E <= 1024 terms by 4 and 22 more, its inverse by 1, the
+    products of share and dw by 2: 33 u of a chosen one's p dw, and 2^-149 below the normal numbers.  The others' part
+    takes the sum over the chosen (33 u and 5 for its own terms), the inverse once more (27 u), exp (4 u) and 2
+    products: 72 u of p sum(p dw); its shares below 2^-126 count as 0."""
+    _say(f"route_bwd small shares B={B} E={E} k={k}")
+    gen = torch.Generator().manual_seed(B + E)
+    x = -30 - torch.randint(0, 64 * 70, (B, E), generator=gen) / 64
+    top = torch.randint(0, E, (B, 1), generator=gen)
+    x.scatter_(1, top, 0.5)
+    ids = torch.argsort(torch.rand(B, E, generator=gen).scatter_(1, top, 2.0), 1)[:, :k].int()   # far ones
+    dw = torch.randn(B, k, generator=gen) * 2.0 ** 40
+    out = Guarded(B, E)
+    mhc.mhc_route_bwd(B, E, k, x.cuda(), ids.cuda(), dw.cuda(), out.t, softmax=True, renorm=False)
+    _checked(out)
+    p, d, at = torch.softmax(x.double(), 1), dw.double(), ids.long()
+    part = torch.zeros_like(p).scatter_(1, at, p.gather(1, at) * d)
+    along = part.sum(1, keepdim=True)
+    size = part.abs().sum(1, keepdim=True)
+    given = torch.zeros_like(p).scatter_(1, at, d.abs())
+    tol = U * (34 * part.abs() + 72 * p * size) + 2.0 ** -148 * (given + p * given.sum(1, keepdim=True))
+    tol += torch.where(p < 2.0 ** -125, 2.0 ** -125, 0.0) * size + 2.0 ** -149
+    _within(out.t, (part - p * along).numpy(), tol.numpy(), "dlogits")
+
+
 @pytest.mark.parametrize("B,E,k", [(40, 24, 4), (4100, 33, 6)])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_bwd_of_far_sigmoids(B, E, k, renorm):
