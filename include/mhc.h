@@ -787,7 +787,8 @@ int mhc_route(int64_t B, int32_t E, int32_t k, int32_t groups, int32_t top_group
 /* The logits' gradient from the weights': the choice itself has none.
  *
  *   logits, flags, scale  as in the forward;  ids in int32 [B, k], as it wrote
- *                         them (ids outside [0, E) have no weight; an id may
+ *                         them (ids outside [0, E), and of experts whose logit
+ *                         is minus infinity or NaN, have no weight; an id may
  *                         occur twice)
  *   dweights  in  fp32 [B, k]
  *   dlogits   out fp32 [B, E], or bf16 as the logits: every value is written,

@@ -671,7 +671,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_bwd_kernel(RouteArgs a, con
     if (id >= a.E) id = -1;
     const float given = slot ? dweights[row * a.k + l] : 0.f;
     const float x = id >= 0 ? logit_at(logits, row * a.E + id, a.bf16) : none;
-    const float dw = id >= 0 ? a.scale * given : 0.f;
+    const float dw = x > none ? a.scale * given : 0.f;  // (a masked expert's weight is 0 whatever its gradient)
     float d;  // the chosen logit's part
     if (every) {
       float y[V];

@@ -117,3 +117,26 @@ def test_route_bwd_of_far_sigmoids(B, E, k, renorm):
         size[b, at[b]] = w * experts.sigmoid(-z[at[b]]) * all_of
         far[b, at[b]] = all_of                               # (two of the factors may be below the normal numbers)
     _within(f64(out.t)[rows], want, 40 * U * size + 2.0 ** -146 * far, "dlogits")
+
+
+@pytest.mark.parametrize("B", [9, 4100])
+def test_route_bwd_of_masked_ids(B):
+    """An id whose logit is masked has no weight: what stands in its place of dweights changes nothing."""
+    _say(f"route_bwd masked ids B={B}")
+    gen = torch.Generator().manual_seed(B)
+    E, k = 40, 5
+    x, dw = _normal(gen, B, E, dtype=torch.float32), _normal(gen, B, k, dtype=torch.float32)
+    ids = torch.argsort(torch.rand(B, E, generator=gen), 1)[:, :k].int().cuda()
+    off = ids[:, 2:4].long()
+    x.scatter_(1, off, torch.tensor([-float("inf"), float("nan")], device="cuda").expand(B, 2))
+    for softmax in (False, True):
+        for renorm in (False, True):
+            got = []
+            for value in (0.0, float("nan"), float("inf")):
+                dw[:, 2:4] = value
+                out = Guarded(B, E)
+                mhc.mhc_route_bwd(B, E, k, x, ids, dw, out.t, softmax=softmax, renorm=renorm)
+                _checked(out)
+                got.append(out.t)
+            assert torch.isfinite(got[0]).all() and torch.all(got[0].gather(1, off) == 0)
+            assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
