@@ -542,17 +542,18 @@ def _device():
 
 
 def _dev_ptrs(dev, tensors, sizes):
-    """_ptr of every tensor with its (bytes, element size, name), and
-    ValueError where a device tensor is not on device `dev`, the current one
-    (the kernels would run on another device than the tensor's)."""
+    """_ptr of each tensor, with its (nbytes, esize, name), on the current
+    device (index dev).  A tensor of another device is refused, not launched on
+    (the kernels would run on another device than the tensor's).  Where a type
+    stands for esize, a tensor of other numbers of its size is refused."""
     out = []
     for t, (nbytes, esize, name) in zip(tensors, sizes):
         if t is not None:
             # What nearly every tensor is, decided in a few attribute reads (a
             # raw address has none of them).
             try:
-                usual = (t.get_device() == dev >= 0 and (t.itemsize == esize or esize is None) and t.nbytes >= nbytes
-                         and t.is_contiguous())
+                usual = (t.get_device() == dev >= 0 and (t.dtype is esize or t.itemsize == esize or esize is None)
+                         and t.nbytes >= nbytes and t.is_contiguous())
             except AttributeError:
                 usual = False
             t = t.data_ptr() if usual else _dev_ptr(t, dev, nbytes, esize, name)
@@ -560,7 +561,17 @@ def _dev_ptrs(dev, tensors, sizes):
     return out
 
 
+# What holds a type's values besides it and raw bytes (uint8).
+_SAME = {torch.bfloat16: (torch.uint16, torch.int16), "codes": (torch.float8_e4m3fn,),
+         "scales": (torch.float8_e8m0fnu,)}
+
+
 def _dev_ptr(t, dev, nbytes, esize, name):
+    if isinstance(esize, torch.dtype):
+        if (isinstance(t, torch.Tensor) and t.numel() > 0 and t.itemsize == esize.itemsize
+                and t.dtype not in (esize, torch.uint8, *_SAME.get(esize, ()), *_SAME.get(name, ()))):
+            raise ValueError(f"{name}: {t.dtype}, the call takes {esize}")
+        esize = esize.itemsize
     p = _ptr(t, nbytes, esize, name)
     if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
@@ -722,14 +733,19 @@ def mhc_embed_bwd(B, n, C, V, tokens, dX_0, scale, dtable, workspace, accumulate
 
 
 # Around a layer of experts: norm, choice of experts, rows into the experts'
-# order and back.  On the current device, as the training calls.
+# order and back.  On the current device, as the training calls; tensors are of
+# the types that include/mhc.h names (the gather copies any of their size).
+
+_BF16, _FP32, _INT32, _BYTE = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
 
 @functools.lru_cache(maxsize=256)
 def _rmsnorm_sizes(B, C):
     B = max(B, 0)
     some = 4 * C if B > 0 else 0  # at B == 0 nothing is touched
-    return ((B * C * 2, 2, "x"), (B * C * 2, 2, "shortcut"), (some, 4, "weight"), (B * C * 2, 2, "sum"),
-            (B * C * 2, 2, "y"), (B * C, 1, "codes"), (B * -(-C // 32), 1, "scales"), (B * 4, 4, "rstd"))
+    return ((B * C * 2, _BF16, "x"), (B * C * 2, _BF16, "shortcut"), (some, _FP32, "weight"), (B * C * 2, _BF16, "sum"),
+            (B * C * 2, _BF16, "y"), (B * C, _BYTE, "codes"), (B * -(-C // 32), _BYTE, "scales"),
+            (B * 4, _FP32, "rstd"))
 
 
 def mhc_rmsnorm(B, C, x, weight, y=None, codes=None, scales=None, shortcut=None, sum=None, rstd=None, eps=1e-5,
@@ -753,8 +769,8 @@ def mhc_rmsnorm_bwd_workspace_size(B, C):
 def _rmsnorm_bwd_sizes(B, C):
     B = max(B, 0)
     some = 4 * C if B > 0 else 0
-    return ((B * C * 2, 2, "sum"), (some, 4, "weight"), (B * 4, 4, "rstd"), (B * C * 2, 2, "dy"),
-            (B * C * 2, 2, "dsum"), (B * C * 2, 2, "dx"), (4 * C, 4, "dweight"))
+    return ((B * C * 2, _BF16, "sum"), (some, _FP32, "weight"), (B * 4, _FP32, "rstd"), (B * C * 2, _BF16, "dy"),
+            (B * C * 2, _BF16, "dsum"), (B * C * 2, _BF16, "dx"), (4 * C, _FP32, "dweight"))
 
 
 def mhc_rmsnorm_bwd(B, C, sum, weight, rstd, dy, dx, dweight=None, workspace=None, dsum=None, workspace_bytes=None,
@@ -771,13 +787,13 @@ def mhc_rmsnorm_bwd(B, C, sum, weight, rstd, dy, dx, dweight=None, workspace=Non
     return st
 
 
-def _logits_size(logits, softmax, renorm, bf16):
-    """Element size and flags: the logits' type is the tensor's (bf16 says it for raw addresses)."""
+def _logits_type(logits, softmax, renorm, bf16):
+    """Type and flags: the logits' type is the tensor's (bf16 says it for raw addresses)."""
     if bf16 is None:
         bf16 = isinstance(logits, torch.Tensor) and logits.dtype == torch.bfloat16
     if isinstance(logits, torch.Tensor) and logits.dtype not in (torch.bfloat16, torch.float32, torch.uint8):
         raise ValueError(f"logits: {logits.dtype}, the call takes float32 or bfloat16")
-    return (2 if bf16 else 4,
+    return (_BF16 if bf16 else _FP32,
             (MHC_ROUTE_SOFTMAX if softmax else 0) | (MHC_ROUTE_RENORM if renorm else 0) | (MHC_ROUTE_BF16 if bf16 else 0))
 
 
@@ -786,11 +802,11 @@ def mhc_route(B, E, k, logits, ids, weights, bias=None, groups=1, top_groups=1, 
     """The k experts of each row of logits (fp32 or bf16 [B, E]): ids (int32)
     and weights (fp32), both [B, k] (see include/mhc.h)."""
     B, E, k, dev = int(B), int(E), int(k), _device()
-    one, flags = _logits_size(logits, softmax, renorm, bf16)
-    rows = max(B, 0)
+    kind, flags = _logits_type(logits, softmax, renorm, bf16)
+    rows, one = max(B, 0), kind.itemsize
     logits, bias, ids, weights = _dev_ptrs(dev, (logits, bias, ids, weights), (
-        (rows * E * one, one, "logits"), (4 * E if rows else 0, 4, "bias"), (rows * k * 4, 4, "ids"),
-        (rows * k * 4, 4, "weights")))
+        (rows * E * one, kind, "logits"), (4 * E if rows else 0, _FP32, "bias"), (rows * k * 4, _INT32, "ids"),
+        (rows * k * 4, _FP32, "weights")))
     st = load().mhc_route(B, E, k, int(groups), int(top_groups), flags, float(scale), logits, bias, ids, weights,
                           _dev_stream(stream, dev))
     if check:
@@ -803,11 +819,11 @@ def mhc_route_bwd(B, E, k, logits, ids, dweights, dlogits, softmax=False, renorm
     """Gradient of mhc_route's weights with respect to the logits, in their
     type (see include/mhc.h)."""
     B, E, k, dev = int(B), int(E), int(k), _device()
-    one, flags = _logits_size(logits, softmax, renorm, bf16)
-    rows = max(B, 0)
+    kind, flags = _logits_type(logits, softmax, renorm, bf16)
+    rows, one = max(B, 0), kind.itemsize
     logits, ids, dweights, dlogits = _dev_ptrs(dev, (logits, ids, dweights, dlogits), (
-        (rows * E * one, one, "logits"), (rows * k * 4, 4, "ids"), (rows * k * 4, 4, "dweights"),
-        (rows * E * one, one, "dlogits")))
+        (rows * E * one, kind, "logits"), (rows * k * 4, _INT32, "ids"), (rows * k * 4, _FP32, "dweights"),
+        (rows * E * one, kind, "dlogits")))
     st = load().mhc_route_bwd(B, E, k, flags, float(scale), logits, ids, dweights, dlogits, _dev_stream(stream, dev))
     if check:
         _check(st, "mhc_route_bwd")
@@ -825,7 +841,7 @@ def mhc_experts_order(B, k, E, ids, slots, offsets, workspace, workspace_bytes=N
     B, k, E, dev = int(B), int(k), int(E), _device()
     rows, wb = max(B, 0), _ws_bytes(workspace, workspace_bytes)
     ids, slots, offsets, workspace = _dev_ptrs(dev, (ids, slots, offsets, workspace), (
-        (rows * k * 4, 4, "ids"), (rows * k * 4, 4, "slots"), ((max(E, 0) + 1) * 4, 4, "offsets"),
+        (rows * k * 4, _INT32, "ids"), (rows * k * 4, _INT32, "slots"), ((max(E, 0) + 1) * 4, _INT32, "offsets"),
         (wb, None, "workspace")))
     st = load().mhc_experts_order(B, k, E, ids, slots, offsets, workspace, wb, _dev_stream(stream, dev))
     if check:
@@ -839,20 +855,20 @@ def mhc_experts_order(B, k, E, ids, slots, offsets, workspace, workspace_bytes=N
 def _gather_sizes(B, k, C, ckpt):
     B = max(B, 0)
     if not ckpt:
-        return ((B * C * 2, 2, "X"), (B * k * 4, 4, "slots"), (B * k * C * 2, 2, "rows"))
+        return ((B * C * 2, 2, "X"), (B * k * 4, _INT32, "slots"), (B * k * C * 2, 2, "rows"))
     blocks = -(-C // 32)
-    return ((B * C, 1, "codes"), (B * blocks, 1, "scales"), (B * k * 4, 4, "slots"), (B * k * C, 1, "row_codes"),
-            (B * k * blocks, 1, "row_scales"))
+    return ((B * C, 1, "codes"), (B * blocks, 1, "scales"), (B * k * 4, _INT32, "slots"),
+            (B * k * C, 1, "row_codes"), (B * k * blocks, 1, "row_scales"))
 
 
 @functools.lru_cache(maxsize=256)
 def _combine_sizes(B, k, C, bwd):
     B = max(B, 0)
     rows, pairs, row = B * k * C * 2, B * k * 4, B * C * 2
-    sizes = ((rows, 2, "Y"), (pairs, 4, "slots"), (pairs, 4, "weights"))
+    sizes = ((rows, _BF16, "Y"), (pairs, _INT32, "slots"), (pairs, _FP32, "weights"))
     if bwd:
-        return sizes + ((row, 2, "dF_out"), (rows, 2, "dY"), (pairs, 4, "dweights"))
-    return sizes + ((row, 2, "shared"), (row, 2, "F_out"))
+        return sizes + ((row, _BF16, "dF_out"), (rows, _BF16, "dY"), (pairs, _FP32, "dweights"))
+    return sizes + ((row, _BF16, "shared"), (row, _BF16, "F_out"))
 
 
 def mhc_experts_gather(B, k, C, X, slots, rows, stream=None, check=True):

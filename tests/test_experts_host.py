@@ -177,6 +177,32 @@ def test_binding_refuses_wrong_tensors():
         mhc.mhc_experts_combine_bwd(B, k, C, 1 << 40, 1 << 41, 1 << 42, 1 << 43, 1 << 44, torch.zeros(4), stream=0)
 
 
+# Types of the same size as each tensor's own, which hold other numbers.
+OTHERS = {torch.bfloat16: (torch.float16,), torch.float32: (torch.int32,), torch.int32: (torch.float32,),
+          "codes": (torch.float8_e5m2, torch.int8, torch.float8_e8m0fnu),
+          "scales": (torch.float8_e4m3fn, torch.bool)}
+TYPES = {torch.float32: "weight rstd dweight bias logits weights dweights dlogits".split(),
+         torch.int32: "ids slots offsets".split(), "codes": ["codes"], "scales": ["scales"]}
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_binding_refuses_other_numbers(name):
+    """A tensor of another type is refused, not read as what it is not; raw bytes and words are not, and a gather copies
+    what it is given."""
+    s = {"B": 4, "C": 32, "E": 8, "k": 2}
+    for what, _, _ in _tensors(name):
+        if what == "workspace" or "gather" in name and what != "slots":
+            continue
+        kind = next((k for k, names in TYPES.items() if what in names), torch.bfloat16)
+        for dtype in OTHERS[kind]:
+            with pytest.raises(ValueError, match=f"{what}: {dtype}"):
+                _call(name, **s, **{what: torch.zeros(4096, dtype=dtype)})
+        own = {"codes": torch.float8_e4m3fn, "scales": torch.float8_e8m0fnu}.get(kind, kind)
+        for dtype in (own, torch.uint8, *([torch.int16] if own == torch.bfloat16 else [])):  # (but are on the host)
+            with pytest.raises(ValueError, match="device tensors"):
+                _call(name, **s, **{what: torch.zeros(4096 * 4, dtype=dtype)})
+
+
 @pytest.mark.skipif(torch.cuda.device_count() > 0, reason="needs a host without a HIP device (fake addresses)")
 def test_no_device_is_mhc_err_hip():
     for name in sorted(CALLS):
