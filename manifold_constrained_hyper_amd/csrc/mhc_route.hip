@@ -166,11 +166,13 @@ __device__ __forceinline__ void exp_64(double (&x)[N]) {
     e[i] = (int)__builtin_bit_cast(u32x2, n[i])[0];
     n[i] -= kShift;
   }
-  // ln 2 in two parts, the upper one with few enough bits for n times it to be exact
+  // The reduction of Cody and Waite: ln 2 = kHigh + kLow, kHigh its first 42 bits, so
+  // that n times it is exact for n of 11.
+  constexpr double kHigh = 0x1.62e42fefa38p-1, kLow = 0x1.ef35793c7673p-45;
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = fma(n[i], constant<HERE>(-0.6931471803691238), x[i]);
+  for (int i = 0; i < N; ++i) x[i] = fma(n[i], constant<HERE>(-kHigh), x[i]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = fma(n[i], constant<HERE>(-1.9082149292705877e-10), x[i]);
+  for (int i = 0; i < N; ++i) x[i] = fma(n[i], constant<HERE>(-kLow), x[i]);
 #pragma unroll
   for (int i = 0; i < N; ++i) p[i] = constant<HERE>(kInverse[TERMS]);
   constexpr int kStep = TERMS > 9 ? 1 : TERMS;  // (few rows come to the long series: its constants stay in memory)
