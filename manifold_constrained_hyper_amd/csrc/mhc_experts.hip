@@ -616,9 +616,10 @@ hipError_t launch_experts_combine_bwd(int64_t B, int k, int64_t C, const void *Y
   const uint32_t pairs = (uint32_t)(B * k), cvec = (uint32_t)(C / 8);
   if (!is_long(cvec)) {
     const Short r = short_of(B, cvec);
-    // Rows of Y in flight, us with one and with as many as there are: C=64 15.1
-    // and 8.9 for 16384 rows at k=8, 8.6 and 6.3 at k=4; C=256 30.4 and 32.1, 16.7
-    // and 15.5, but 7.8 and 5.5 for 64 rows at k=8.
+    // Rows of Y in flight, us with 1, 4 and 8: 16384 rows at k=8 C=64 15.2, 10.8, 9.0,
+    // C=128 19.3, 17.0, 15.1; C=256 30.5, 31.0, 32.1 there, but 8.1, 5.6, 5.5 for 64
+    // rows, and with 4 and 8 11.1, 9.1 for 4096, 17.0, 15.1 for 8192, 68.3, 70.9 for
+    // 40000.  At k=4 with 1 and 4: C=64 8.6, 6.3, C=256 16.9, 15.6.
     const auto kernel = k == 1   ? combine_bwd_short_kernel<1>
                         : k <= 4 ? combine_bwd_short_kernel<4>
                                  : combine_bwd_short_kernel<8>;
