@@ -11,7 +11,7 @@ import torch
 
 import manifold_constrained_hyper_amd as mhc
 from oracle import experts
-from tests.test_gpu_experts import Guarded, U, _checked, _normal, _route, _say, _some_rows, f64
+from tests.test_gpu_experts import Guarded, U, _checked, _crowded, _normal, _route, _say, _some_rows, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -66,6 +66,47 @@ def test_route_weights_are_rounded_once(B, E, k, groups, top_groups, dtype):
                             f"weights softmax={softmax} renorm={renorm} scale={scale}")
 
 
+@pytest.mark.parametrize("B,E,k,groups,top_groups", [
+    (5, 1000, 8, 5, 3), (5, 1000, 16, 5, 3), (9, 1023, 8, 33, 4), (7, 1023, 20, 33, 4), (3, 1020, 8, 3, 2),
+    (6, 1020, 32, 17, 9), (70, 800, 8, 10, 4), (2600, 1015, 6, 5, 2), (5, 600, 24, 1, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_many_experts_in_groups(B, E, k, groups, top_groups, dtype):
+    """Groups that leave a lane up to 32 experts, with short and long lists of the best."""
+    _say(f"route in groups B={B} E={E} k={k} groups={groups} top={top_groups} {dtype}")
+    gen = torch.Generator().manual_seed(E * 10 + k + groups)
+    x = torch.randn(B, E, generator=gen) * 2
+    x[torch.rand(B, E, generator=gen) < 0.05] = -float("inf")
+    x[1], x[2, 1:], x[0, ::7], x[min(3, B - 1), ::5] = -float("inf"), -float("inf"), float("nan"), float("inf")
+    x = x.to(dtype).cuda()
+    rows = np.arange(B) if B <= 100 else _some_rows(B)
+    bias = _normal(gen, E, scale=0.1, dtype=torch.float32)
+    for b in (None, bias):
+        for softmax in (False, True):
+            how = dict(groups=groups, top_groups=top_groups, softmax=softmax, renorm=b is None, scale=1.5)
+            ids, weights = _route(x, k, b, **how)
+            want, want_w = experts.route(f64(x)[rows], k, None if b is None else f64(b), **how)
+            assert np.array_equal(ids.cpu().numpy()[rows], want)
+            _within(f64(weights)[rows], want_w, (1 + 2.0 ** -8) * U * np.abs(want_w) + 2.0 ** -150, "weights")
+
+
+@pytest.mark.parametrize("B,E,k,groups,top_groups", [
+    (20, 1000, 8, 5, 3), (15, 1000, 16, 5, 3), (15, 1023, 20, 33, 4), (20, 1000, 8, 1, 1), (15, 700, 20, 1, 1),
+    (20, 512, 8, 1, 1), (15, 400, 20, 1, 1)])
+def test_route_crowded_of_many_experts(B, E, k, groups, top_groups):
+    """Choices that 42 bits cannot tell apart, with 8 to 32 experts a lane and a wave a row."""
+    _say(f"route crowded B={B} E={E} k={k} groups={groups} top={top_groups}")
+    gen = torch.Generator().manual_seed(B + E + k)
+    x = _crowded(B, E, gen)
+    x[7] = torch.randn(E, generator=gen)
+    for softmax in (False, True):
+        for b in (torch.zeros(E), torch.full((E,), 0.25)):
+            b[E // 2] = -float("inf")
+            how = dict(groups=groups, top_groups=top_groups, softmax=softmax)
+            ids, _ = _route(x.cuda(), k, b.cuda(), **how)
+            want, _ = experts.route(f64(x), k, f64(b), **how)
+            assert np.array_equal(ids.cpu().numpy(), want), np.argwhere(ids.cpu().numpy() != want)[:5]
+
+
 @pytest.mark.parametrize("B,E,k", [(30, 64, 5), (12, 1000, 20), (4099, 50, 6), (4097, 200, 3)])
 def test_route_bwd_of_small_shares(B, E, k):
     """The softmax's gradient where shares are far below the largest, to their own size.  Logits are multiples of 2^-6,
@@ -97,8 +138,8 @@ def test_route_bwd_of_small_shares(B, E, k):
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_bwd_of_far_sigmoids(B, E, k, renorm):
     """Sigmoids next to 0 and next to 1, whose gradients are below fp32's normal numbers but for dweights: exp is off by
-    4 u (2^-148 there), a sigmoid by 3 more, a weight by 2 exps, sigmoid, sum of k <= 6 (its terms' 11 and 4) and division: 27 u;
-    with products and difference 40 u of w sigmoid(-x) (|dw| + sum w |dw|)."""
+    4 u (2^-148 there), a sigmoid by 3 more, a weight by 2 exps, sigmoid, sum of k <= 6 (its terms' 11 and 4) and
+    division: 27 u; with products and difference 40 u of w sigmoid(-x) (|dw| + sum w |dw|)."""
     _say(f"route_bwd far sigmoids B={B} E={E} k={k} renorm={renorm}")
     gen = torch.Generator().manual_seed(B + k)
     x = _far_logits(B, E, gen, torch.float32).cpu()
