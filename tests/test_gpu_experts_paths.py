@@ -181,3 +181,60 @@ def test_route_bwd_of_masked_ids(B):
                 got.append(out.t)
             assert torch.isfinite(got[0]).all() and torch.all(got[0].gather(1, off) == 0)
             assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+# -- rows to their places ---------------------------------------------------------------------------
+
+def _codes_and_slots(B, k, C, gen):
+    P, blocks = B * k, -(-C // 32)
+    slots = torch.randperm(P, generator=gen, device="cuda").reshape(B, k).to(torch.int32)
+    slots[5], slots[B - 2, 0] = -1, P
+    codes = torch.randint(0, 256, (B, C), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.randint(0, 256, (B * blocks,), generator=gen, device="cuda", dtype=torch.uint8)
+    return codes, scales, slots
+
+
+@pytest.mark.parametrize("B,k,C", [
+    (16640, 8, 7168), (16384, 7, 8192), (3900, 28, 8192),   # above 26 MB, in 224 and 256 blocks: a launch of their own
+    (14000, 8, 7168), (3700, 28, 8192),                     # below: with the rows
+    (16640, 8, 7200), (16700, 8, 7176),                     # 225 blocks, which four does not divide: with the rows
+    (15000, 2, 32768)])                                     # 1024 blocks: with the rows
+def test_gather_scales_on_both_sides(B, k, C):
+    """Rows in 8 bits whose scales fit the caches together, and where they do not."""
+    _say(f"gather scales B={B} k={k} C={C}")
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    P, blocks = B * k, -(-C // 32)
+    codes, scales, slots = _codes_and_slots(B, k, C, gen)
+    scales = scales.view(B, blocks)
+    rows, more = Guarded(P, C, dtype=torch.uint8), Guarded(P, blocks, dtype=torch.uint8)
+    mhc.mhc_experts_gather_ckpt(B, k, C, codes, scales, slots, rows.t, more.t)
+    _checked(rows, more)
+    left = torch.ones(P, dtype=torch.bool, device="cuda")
+    for lo in range(0, B, 1024):
+        at = slots[lo:lo + 1024].reshape(-1).long()
+        ok = (at >= 0) & (at < P)
+        assert torch.equal(rows.t[at[ok]], codes[lo:lo + 1024].repeat_interleave(k, 0)[ok])
+        assert torch.equal(more.t[at[ok]], scales[lo:lo + 1024].repeat_interleave(k, 0)[ok])
+        left[at[ok]] = False
+    assert int(left.sum()) == k + 1 and torch.all(rows.t[left] == 0x7F) and torch.all(more.t[left] == 0x7F)
+
+
+@pytest.mark.parametrize("B,k,C", [(16640, 8, 7168), (300, 5, 2048), (40, 3, 256)])
+@pytest.mark.parametrize("start", [1, 2])
+def test_gather_scales_at_any_byte(B, k, C, start):
+    """Scales are bytes, wherever they begin."""
+    _say(f"gather scales at byte {start} B={B} k={k} C={C}")
+    gen = torch.Generator(device="cuda").manual_seed(B + start)
+    P, blocks = B * k, C // 32
+    codes, scales, slots = _codes_and_slots(B, k, C, gen)
+    given = torch.empty(start + B * blocks, dtype=torch.uint8, device="cuda")
+    given[start:] = scales
+    rows, other = Guarded(P, C, dtype=torch.uint8), 3 - start
+    more = torch.full((P * blocks + 16,), 0xA5, dtype=torch.uint8, device="cuda")
+    mhc.mhc_experts_gather_ckpt(B, k, C, codes, given[start:], slots, rows.t, more[other:other + P * blocks])
+    _checked(rows)
+    assert torch.all(more[:other] == 0xA5) and torch.all(more[other + P * blocks:] == 0xA5)
+    more = more[other:other + P * blocks].view(P, blocks)
+    at = slots.reshape(-1).long()
+    ok = (at >= 0) & (at < P)
+    assert torch.equal(more[at[ok]], scales.view(B, blocks).repeat_interleave(k, 0)[ok])
