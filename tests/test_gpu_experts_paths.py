@@ -238,3 +238,39 @@ def test_gather_scales_at_any_byte(B, k, C, start):
     at = slots.reshape(-1).long()
     ok = (at >= 0) & (at < P)
     assert torch.equal(more[at[ok]], scales.view(B, blocks).repeat_interleave(k, 0)[ok])
+
+
+# -- norm -------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,C", [(1030, 8200), (1030, 16384), (300, 16376), (2, 16392), (700, 24584), (700, 32768),
+                                 (600, 32776), (520, 65536), (2050, 7168), (9000, 1000)])
+def test_rmsnorm_bwd_several_rows_a_workgroup(B, C):
+    """Every number of vectors a thread with several rows to a workgroup; bounds as in test_rmsnorm_bwd."""
+    _say(f"rmsnorm_bwd several rows B={B} C={C}")
+    gen = torch.Generator(device="cuda").manual_seed(B + C)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    s = (normal(B, C) * torch.exp2(normal(B, 1))).bfloat16()
+    dy, dsum, w = (normal(B, C) / 64).bfloat16(), (normal(B, C) / 64).bfloat16(), 1 + 0.3 * normal(C)
+    rstd = (s.float().square().mean(1) + 1e-5).rsqrt()
+    n = s.double() * rstd.double()[:, None]
+    for weight in (None, w):
+        g = dy.double() if weight is None else dy.double() * w.double()
+        A = (g * n).abs().sum(1, keepdim=True)
+        mean = (g * n).mean(1, keepdim=True)
+        for more in (None, dsum):
+            dx, dw = Guarded(B, C, dtype=torch.bfloat16), Guarded(C)
+            ws = Guarded(mhc.mhc_rmsnorm_bwd_workspace_size(B, C), dtype=torch.uint8, fill=0xFF)
+            mhc.mhc_rmsnorm_bwd(B, C, s, weight, rstd, dy, dx.t, dweight=dw.t, workspace=ws.t, dsum=more)
+            _checked(dx, dw, ws)
+            want = rstd.double()[:, None] * (g - n * mean)
+            if more is not None:
+                want = want + dsum.double()
+            e = rstd.double()[:, None] * (n.abs() * 96 * U * A / C + 8 * U * (g.abs() + (n * mean).abs()))
+            e += U * want.abs()
+            assert torch.all((dx.t.double() - want).abs() <= 2.0 ** -8 * (want.abs() + e) + e)
+            each = dy.double() * n
+            assert torch.all((dw.t.double() - each.sum(0)).abs() <= (B + 40) * U * each.abs().sum(0))
+            alone = Guarded(B, C, dtype=torch.bfloat16)
+            mhc.mhc_rmsnorm_bwd(B, C, s, weight, rstd, dy, alone.t, dsum=more)
+            _checked(alone)
+            assert torch.equal(alone.t, dx.t)
