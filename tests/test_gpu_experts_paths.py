@@ -274,3 +274,47 @@ def test_rmsnorm_bwd_several_rows_a_workgroup(B, C):
             mhc.mhc_rmsnorm_bwd(B, C, s, weight, rstd, dy, alone.t, dsum=more)
             _checked(alone)
             assert torch.equal(alone.t, dx.t)
+
+
+# -- more work than one grid ------------------------------------------------------------------------
+
+def test_rmsnorm_of_more_rows_than_workgroups():
+    """Rows of a workgroup each, past 2^21 of them: workgroups go on to the next."""
+    B, C = (1 << 21) + 5, 264
+    _say(f"rmsnorm B={B} C={C}")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(B, C, generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = 1 + 0.3 * torch.randn(C, generator=gen, device="cuda")
+    o = {"y": Guarded(B, C, dtype=torch.bfloat16), "codes": Guarded(B, C, dtype=torch.uint8),
+         "scales": Guarded(B, -(-C // 32), dtype=torch.uint8), "rstd": Guarded(B)}
+    mhc.mhc_rmsnorm(B, C, x, w, **{k: v.t for k, v in o.items()})
+    _checked(*o.values())
+    for lo in range(0, B, 1 << 19):
+        at = slice(lo, min(B, lo + (1 << 19)))
+        s = x[at].double()
+        rstd = 1 / (s.square().mean(1) + 1e-5).sqrt()
+        assert torch.all((o["rstd"].t[at] - rstd).abs() <= 50 * U * rstd)
+        y = s.mul_(rstd[:, None]).mul_(w.double())
+        assert torch.all((o["y"].t[at] - y).abs() <= (2.0 ** -8 + 54 * U) * y.abs())
+        step = torch.exp2(o["scales"].t[at].double() - 127).repeat_interleave(32, 1)[:, :C]
+        got = o["codes"].t[at].view(torch.float8_e4m3fn).double() * step
+        assert torch.all((got - y).abs() <= (2.0 ** -4 + 54 * U) * y.abs() + 2.0 ** -10 * step)
+
+
+def test_combine_of_more_rows_than_waves():
+    """Rows that a wave takes, past 2^24 of them, and 2^32 bytes."""
+    B, C = (1 << 24) + 9, 264
+    _say(f"combine B={B} C={C}")
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    Y = torch.randint(-2 ** 31, 2 ** 31, (B, C // 2), generator=gen, device="cuda", dtype=torch.int32)
+    Y &= ~0x40004000                                             # no NaN and no infinity: exponents below 128
+    Y = Y.view(torch.bfloat16)
+    slots = torch.arange(B - 1, -1, -1, device="cuda", dtype=torch.int32)
+    slots[::1000003] = -1
+    out = torch.full_like(Y, 7.0)
+    mhc.mhc_experts_combine(B, 1, C, Y, slots, None, out)
+    for lo in range(0, B, 1 << 21):
+        hi = min(B, lo + (1 << 21))
+        want = Y[B - hi:B - lo].flip(0)
+        want[slots[lo:hi] < 0] = 0
+        assert torch.all(out[lo:hi] == want)                     # (a zero's sign is lost in the sum)
