@@ -207,10 +207,12 @@ __device__ __forceinline__ bool place_of(const Short &r, uint64_t u, uint64_t B,
 //
 // A wave copies a row (T: vectors of 16 or 8 bytes), or one of `parts` of it,
 // to one place, in one piece; the row's k waves share it in the cache.  Bound
-// by the writes: 198 us for the codes of B=16384, k=8, C=7168 (1.06 GB, 5.3
-// TB/s; 183 without any read).  Waves that write 1 KB each to all of a row's
-// places take 20 us more.
-constexpr int kGatherAhead = 8;  // vectors in flight a lane (222 us with the order; with four 242)
+// by the writes: 203 us for B=16384, k=8, C=7168 in 8 bits (1.09 GB, 5.4 TB/s;
+// 183 for the codes without any read), 363 in bf16 (2.11 GB, 5.8 TB/s).  Waves
+// that write 1 KB each to all of a row's places take 20 us more, and scales in
+// a launch of their own as much or more (k=8, C=7168, us with the order: 106
+// apart, 100 so at 8192 rows; 218, 215 at 16384; 303, 290 at k=2, 65536 rows).
+constexpr int kGatherAhead = 8;  // vectors in flight a lane (227 us with the order; with four 260)
 template <class T, class S>
 __global__ __launch_bounds__(kThreads) void gather_kernel(const T *__restrict__ x, const S *__restrict__ scales,
                                                           const int32_t *__restrict__ slots, T *__restrict__ rows,
@@ -491,12 +493,6 @@ Short short_of(int64_t B, int64_t vecs) {
 // times the waves; from 2048 rows on they are the same).
 constexpr int64_t kManyWaves = 4096;
 
-// Scales beyond what the L2 caches hold together leave them as parts of lines
-// when they are written between the rows: a launch of their own is faster
-// there (k=8, C=7168, us with the order: 187 apart, 178 between at 14336 rows,
-// 25.7 MB of scales; 210, 258 at 16384, 29.4 MB).
-constexpr int64_t kScalesApart = 26 << 20;
-
 template <class T, class S>
 hipError_t gather_long(int64_t B, int k, int64_t vecs, const void *x, const void *scales, int64_t blocks,
                        const int32_t *slots, void *rows, void *row_scales, hipStream_t st) {
@@ -517,18 +513,8 @@ template <class T>
 hipError_t gather_t(int64_t B, int k, int64_t vecs, const void *x, const uint8_t *scales, int64_t blocks,
                     const int32_t *slots, void *rows, uint8_t *row_scales, hipStream_t st) {
   if (is_long(vecs)) {
-    const int64_t pairs = B * k;
     // Scale bytes four at a time where rows and tensors allow it.
     const uintptr_t where = reinterpret_cast<uintptr_t>(scales) | reinterpret_cast<uintptr_t>(row_scales);
-    if (blocks % 4 == 0 && where % 4 == 0 && blocks <= 256 && pairs * blocks > kScalesApart) {
-      const hipError_t e = gather_long<T, uint8_t>(B, k, vecs, x, nullptr, 0, slots, rows, nullptr, st);
-      if (e != hipSuccess) return e;
-      const Short r = short_of(B, blocks / 4);
-      gather_short_kernel<uint32_t><<<grid_of(r.units, kWaves), kThreads, 0, st>>>(
-          reinterpret_cast<const uint32_t *>(scales), nullptr, slots, reinterpret_cast<uint32_t *>(row_scales), nullptr,
-          r, (uint64_t)B, 0, k, (uint32_t)pairs);
-      return hipGetLastError();
-    }
     if (blocks % 4 == 0 && where % 4 == 0)
       return gather_long<T, uint32_t>(B, k, vecs, x, scales, blocks / 4, slots, rows, row_scales, st);
     return gather_long<T, uint8_t>(B, k, vecs, x, scales, blocks, slots, rows, row_scales, st);

@@ -195,12 +195,11 @@ def _codes_and_slots(B, k, C, gen):
 
 
 @pytest.mark.parametrize("B,k,C", [
-    (16640, 8, 7168), (16384, 7, 8192), (3900, 28, 8192),   # above 26 MB, in 224 and 256 blocks: a launch of their own
-    (14000, 8, 7168), (3700, 28, 8192),                     # below: with the rows
-    (16640, 8, 7200), (16700, 8, 7176),                     # 225 blocks, which four does not divide: with the rows
-    (15000, 2, 32768)])                                     # 1024 blocks: with the rows
-def test_gather_scales_on_both_sides(B, k, C):
-    """Rows in 8 bits whose scales fit the caches together, and where they do not."""
+    (16640, 8, 7168), (16384, 7, 8192), (3900, 28, 8192), (14000, 8, 7168), (3700, 28, 8192),   # in 224 and 256 blocks
+    (16640, 8, 7200), (16700, 8, 7176),                       # 225 blocks, which four does not divide
+    (15000, 2, 32768)])                                       # 1024 blocks
+def test_gather_scales_of_large_batches(B, k, C):
+    """Rows in 8 bits, with scales that the caches hold together and more than they do (about 26 MB)."""
     _say(f"gather scales B={B} k={k} C={C}")
     gen = torch.Generator(device="cuda").manual_seed(B)
     P, blocks = B * k, -(-C // 32)
