@@ -4,13 +4,18 @@
 //   s = bf16(x + shortcut)   rstd = 1 / sqrt(mean(s^2) + eps)   y = s rstd w
 //   n = s rstd, g = dy w:    dx = rstd (g - n mean(g n)) + dsum,  dw = sum over rows of dy n
 //
-// A workgroup takes a row, which stays in registers between the sum and its
-// use, so every tensor is read or written once.  Squares and sums are fp32
-// (products of two bf16 values are exact there).
+// A workgroup takes a row at a time (of short rows several), which stays in
+// registers between the sum and its use, so that every tensor is read or written
+// once.  Two gradient kernels read a row twice, the second time from the cache
+// where it holds it: that of rows above C=16384, and that of few rows, by rows
+// and by columns.  Squares and sums are fp32 (products of two bf16 values are
+// exact there).
 //
 // Bound by HBM: 139 us for B=16384, C=7168 with the shortcut in 8 bits (826 MB,
 // 6.0 TB/s), 160 for its gradients with the shortcut's (940 MB, 5.9 TB/s, of
-// which 5 us join dweight).  One row takes 3.6, and its gradients 4.4.
+// which 5 us join dweight).  One row takes 3.1, and its gradients 4.0.
+// Long rows, 4096 of them without the shortcut, and their gradients: C=16384 52
+// us (5.1 TB/s) and 98 (4.1), C=32768 102 (5.3) and 243 (3.3, read twice).
 #include "mhc_experts.h"
 #include "mhc_finish.h"
 #include "mhc_held.h"
@@ -162,7 +167,7 @@ __global__ __launch_bounds__(64 * kShortWaves) void rmsnorm_short_kernel(NormArg
 
 // The partial sums of dweight stay in registers; with one vector a thread the
 // weight does too, and the next row is loaded while this one is worked on.
-// From four on a row does not fit beside them and is read twice (from the cache).
+// From four on a row does not fit beside them and is read twice.
 template <int V>
 struct BwdRow {
   u32x4 s[V], d[V], p[V];
