@@ -755,10 +755,10 @@ int mhc_rmsnorm_bwd(int64_t B, int64_t C, const void *sum, const float *weight, 
  * plus infinity counts as the largest finite fp32 number.  The experts are
  * `groups` groups of E / groups neighbours.  A group ranks by its largest
  * choice, or, with a bias, by the sum of its two largest (of one, where it has no
- * second); the best top_groups groups stay.  Of their experts the k largest choices are taken, in descending
- * order.  Among equal ones, groups too, the lowest index comes first.  The order
- * is that of the logits where there is no bias, and that of choices in 64-bit
- * arithmetic where there is one.
+ * second); the best top_groups groups stay.  Of their experts the k largest
+ * choices are taken, in descending order.  Among equal ones, groups too, the
+ * lowest index comes first.  The order is that of the logits where there is no
+ * bias, and that of choices in 64-bit arithmetic where there is one.
  *
  *   weight_j = scale * score_j, or with MHC_ROUTE_RENORM
  *              scale * score_j / (sum of the chosen scores), which holds for
